@@ -1,5 +1,6 @@
 /*
- * ct.h -- C ABI of the B200 (sm_100a) ONNX ConvTranspose library (libct.so).
+ * ct.h -- C ABI of the B200 (sm_100a) ONNX ConvTranspose library (libct.so),
+ * and of the group norm and dropout that follow it in a decoder.
  *
  * The operation (ai.onnx.ConvTranspose README, "Description", "Inputs",
  * "Outputs", "Attributes" and "Type constraints"): Y is the transposed
@@ -67,7 +68,9 @@ typedef enum ct_status {
     CT_ERR_NOMEM = 10      /* host allocation of the plan failed */
 } ct_status;
 
-typedef enum ct_dtype { CT_F32 = 0, CT_F16 = 1 } ct_dtype;
+/* ConvTranspose takes CT_F32 and CT_F16; the group norm and dropout also
+ * CT_BF16. */
+typedef enum ct_dtype { CT_F32 = 0, CT_F16 = 1, CT_BF16 = 2 } ct_dtype;
 typedef enum ct_layout { CT_NCHW = 0, CT_NHWC = 1 } ct_layout;
 
 /* auto_pad (README "Attributes"): NOTSET uses pads; SAME_UPPER/SAME_LOWER give
@@ -105,10 +108,13 @@ typedef enum ct_algo {
  * conv_transpose, parameter `activation`, default Identity).  The page does
  * not list the Activation members; this library offers identity and ReLU
  * (max(v, 0)), applied in fp32 before the output is rounded to its dtype.
- * Any other value is CT_ERR_ATTR. */
+ * Any other value is CT_ERR_ATTR.  The group norm also takes SILU (v /
+ * (1 + exp(-v))) and GELU (v/2 * (1 + erf(v / sqrt 2))). */
 typedef enum ct_activation {
     CT_ACT_IDENTITY = 0,
-    CT_ACT_RELU = 1
+    CT_ACT_RELU = 1,
+    CT_ACT_SILU = 2,
+    CT_ACT_GELU = 3
 } ct_activation;
 
 /* One ConvTranspose call.  Every array has 3 slots; only the first `rank`
@@ -232,6 +238,76 @@ CT_API ct_status ct_run_noalloc(const ct_plan_t *plan, const void *x, const void
                                 const void *bias, void *y, void *stream);
 
 CT_API void ct_plan_destroy(ct_plan_t *plan);
+
+/* ---- the operators that follow a transposed convolution in a decoder -------
+ *
+ * Dropout.  Element i of a tensor (its row-major index) is kept when a 16-bit
+ * random value is at least t = floor(65536 p + 1/2), and then scaled by
+ * 65536 / (65536 - t), so that the expectation is the input whatever p is;
+ * it is 0 otherwise, also where the input is infinite or NaN.  p is in
+ * [0, 1] and takes effect as t / 65536.  The value is 16-bit part i % 8 (low
+ * half of word 0 first) of Philox4x32-10 (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011) with the four counter words (i / 8 low,
+ * i / 8 high, offset low, offset high) and the key (seed low, seed high).
+ * The mask is thus a function of (i, seed, offset): it is never stored, and
+ * the gradient draws it again.  `rng`, when not NULL, points to two 64-bit
+ * words on the device (8-byte aligned), seed and offset, which the kernel
+ * reads in place of the arguments: a captured graph can so draw another mask
+ * at each replay.  A step uses a new offset for each step and a new seed, or
+ * an offset of its own, for each tensor. */
+
+/* y = drop(x) + residual, computed in fp32 and rounded once.  n elements;
+ * residual may be NULL.  y may be x or residual; other overlap is not
+ * allowed.  The gradient in x is this call on dy with the same p, seed and
+ * offset and no residual; the gradient in the residual is dy itself. */
+CT_API ct_status ct_dropout(int32_t dtype, int64_t n, const void *x, const void *residual, double p,
+                            uint64_t seed, uint64_t offset, const void *rng, void *y, void *stream);
+
+/* Group norm of channels-last images x[N, S, C] (S pixels, of any number of
+ * axes), C / groups neighbouring channels to a group, followed by an
+ * activation and dropout:
+ *
+ *     mean = sum x / M,  rstd = (sum (x - mean)^2 / M + eps)^-1/2   per (image, group),
+ *     a = (x - mean) * rstd * weight[c] + bias[c],   y = drop(act(a)),
+ *
+ * with M = S * C / groups.  Everything is computed in fp32 and y rounded
+ * once.  dtype is x's, y's, dy's and dx's; param_dtype weight's, bias's and
+ * their gradients', CT_F32 or dtype.  Limits: N <= 2^30, 1 <= C <= 2^24,
+ * N * S * C <= 2^60 (CT_ERR_CHANNELS for C and groups, else CT_ERR_ATTR). */
+typedef struct ct_group_norm_desc {
+    int32_t dtype;         /* ct_dtype */
+    int32_t param_dtype;   /* CT_F32, or dtype */
+    int32_t activation;    /* ct_activation */
+    int32_t reserved;      /* not read */
+    int64_t N, S, C, groups;
+    double eps;            /* >= 0 */
+} ct_group_norm_desc;
+
+/* Bytes of device workspace (256-byte aligned) of one forward and one
+ * backward call.  Its contents need not be set before a call and mean
+ * nothing after it; calls that may run at the same time need one each. */
+CT_API ct_status ct_group_norm_workspace_bytes(const ct_group_norm_desc *desc, size_t *forward_bytes,
+                                               size_t *backward_bytes);
+
+/* Forward.  weight and bias may be NULL (1 and 0).  mean and rstd, each
+ * [N, groups] fp32, may be NULL; the backward call needs them.  p = 0: no
+ * dropout, seed, offset and rng are then not read.  Asynchronous on `stream`.
+ * y may not overlap x. */
+CT_API ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, const void *weight,
+                               const void *bias, double p, uint64_t seed, uint64_t offset, const void *rng,
+                               void *y, float *mean, float *rstd, void *workspace, void *stream);
+
+/* Backward: dx (of x), dweight and dbias (of weight and bias, summed over
+ * images and pixels), each NULL when it is not wanted.  x, weight, bias,
+ * mean, rstd, p, seed, offset and rng as the forward call had and gave them;
+ * a is computed again from x.  With S or N of 0 the parameters' gradients
+ * are 0.  The same call gives the same bits: no sum's order depends on
+ * timing. */
+CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const void *dy, const void *x,
+                                        const float *mean, const float *rstd, const void *weight,
+                                        const void *bias, double p, uint64_t seed, uint64_t offset,
+                                        const void *rng, void *dx, void *dweight, void *dbias,
+                                        void *workspace, void *stream);
 
 /* Static, human-readable text for a status code. */
 CT_API const char *ct_status_string(ct_status status);

@@ -1,5 +1,6 @@
-"""B200 (sm_100a) ONNX ConvTranspose: a C-ABI CUDA library (libct.so, declared
-in include/ct.h) and its thin Python binding.  ``build.build()`` compiles the
+"""B200 (sm_100a) ONNX ConvTranspose, with the group norm and dropout that
+follow it in a decoder: a C-ABI CUDA library (libct.so, declared in
+include/ct.h) and its thin Python binding.  ``build.build()`` compiles the
 library in-tree; ``workloads`` holds the seeded synthetic inputs."""
 
 from .ct import (  # noqa: F401
@@ -18,5 +19,9 @@ from .ct import (  # noqa: F401
     ct_run_noalloc,
     ct_status_string,
     ct_workspace_bytes,
+    dropout,
+    dropout_backward,
+    group_norm_nhwc,
+    group_norm_nhwc_backward,
     make_desc,
 )

@@ -10,7 +10,10 @@
 #include <atomic>
 #include <new>
 
+#include <math.h>
+
 #include "ct_internal.h"
+#include "group_norm.h"
 
 using namespace ct;
 
@@ -223,6 +226,59 @@ ct_status check_device() {
 
 bool aligned(const void *ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
+size_t dtype_bytes(int dtype) { return dtype == CT_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype == CT_F32 || dtype == CT_F16 || dtype == CT_BF16; }
+
+// Drop probability -> 16-bit threshold and the scale of what is kept.
+ct_status resolve_rng(double p, uint64_t seed, uint64_t offset, const void *rng, RngArgs *out) {
+    if (!(p >= 0.0 && p <= 1.0)) return CT_ERR_ATTR;
+    out->seed = seed;
+    out->offset = offset;
+    out->dev = (const uint64_t *)rng;
+    out->threshold = (uint32_t)floor(p * 65536.0 + 0.5);
+    out->scale = out->threshold < 65536 ? (float)(65536.0 / (65536.0 - out->threshold)) : 0.f;
+    if (out->threshold == 0) out->dev = nullptr;   // nothing is drawn
+    return aligned(rng, 8) ? CT_OK : CT_ERR_ALIGN;
+}
+
+constexpr int64_t kMaxNormChannels = int64_t(1) << 24;
+
+ct_status resolve_norm(const ct_group_norm_desc *d, GnGeom *g) {
+    if (!d) return CT_ERR_NULL;
+    if (!known_dtype(d->dtype)) return CT_ERR_DTYPE;
+    if (d->param_dtype != CT_F32 && d->param_dtype != d->dtype) return CT_ERR_DTYPE;
+    if (d->activation < CT_ACT_IDENTITY || d->activation > CT_ACT_GELU) return CT_ERR_ATTR;
+    if (!(d->eps >= 0.0) || !isfinite(d->eps)) return CT_ERR_ATTR;
+    if (d->N < 0 || d->N > kMaxDim || d->S < 0 || d->S > kMaxElems) return CT_ERR_ATTR;
+    if (d->C < 1 || d->C > kMaxNormChannels) return CT_ERR_CHANNELS;
+    if (d->groups < 1 || d->C % d->groups != 0) return CT_ERR_CHANNELS;
+    if (mul_capped(mul_capped(d->N, d->S), d->C) < 0) return CT_ERR_ATTR;
+    if (mul_capped(d->S, d->C) < 0) return CT_ERR_ATTR;
+    *g = gn_geom(d->N, d->S, d->C, d->groups);
+    return CT_OK;
+}
+
+// What both directions of the group norm check and pass on.
+ct_status norm_args(const ct_group_norm_desc *d, const GnGeom &g, const void *weight, const void *bias, double p,
+                    uint64_t seed, uint64_t offset, const void *rng, void *workspace, size_t ws, GnArgs *a) {
+    memset(a, 0, sizeof(*a));
+    ct_status st = resolve_rng(p, seed, offset, rng, &a->rng);
+    if (st != CT_OK) return st;
+    const size_t pb = dtype_bytes(d->param_dtype);
+    if (!aligned(weight, pb) || !aligned(bias, pb)) return CT_ERR_ALIGN;
+    if (ws > 0 && !workspace) return CT_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CT_ERR_ALIGN;
+    a->dtype = d->dtype;
+    a->param_dtype = d->param_dtype;
+    a->act = d->activation;
+    a->eps = (float)d->eps;
+    a->weight = weight;
+    a->bias = bias;
+    a->drop = a->rng.threshold > 0;
+    a->ws = (float *)workspace;
+    return CT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -388,6 +444,83 @@ ct_status ct_run_parts(const ct_plan_t *plan, const void *x, const void *w_packe
         case CT_ALGO_GROUPED: return (parts & CT_PART_MAIN) ? grouped_run(p, x, w_packed, bias, y, s) : CT_OK;
         default: return (parts & CT_PART_MAIN) ? generic_run(p, x, w_packed, bias, y, s) : CT_OK;
     }
+}
+
+ct_status ct_group_norm_workspace_bytes(const ct_group_norm_desc *desc, size_t *forward_bytes,
+                                        size_t *backward_bytes) {
+    if (!forward_bytes || !backward_bytes) return CT_ERR_NULL;
+    GnGeom g;
+    ct_status st = resolve_norm(desc, &g);
+    if (st != CT_OK) return st;
+    *forward_bytes = gn_forward_ws(g);
+    *backward_bytes = gn_backward_ws(g);
+    return CT_OK;
+}
+
+ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, const void *weight, const void *bias,
+                        double p, uint64_t seed, uint64_t offset, const void *rng, void *y, float *mean,
+                        float *rstd, void *workspace, void *stream) {
+    GnGeom g;
+    ct_status st = resolve_norm(desc, &g);
+    if (st != CT_OK) return st;
+    if (g.N == 0) return CT_OK;
+    GnArgs a;
+    st = norm_args(desc, g, weight, bias, p, seed, offset, rng, workspace, gn_forward_ws(g), &a);
+    if (st != CT_OK) return st;
+    if (g.E > 0 && (!x || !y)) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(desc->dtype);
+    if (!aligned(x, eb) || !aligned(y, eb) || !aligned(mean, 4) || !aligned(rstd, 4)) return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    a.x = x;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    return gn_forward(g, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const void *dy, const void *x, const float *mean,
+                                 const float *rstd, const void *weight, const void *bias, double p,
+                                 uint64_t seed, uint64_t offset, const void *rng, void *dx, void *dweight,
+                                 void *dbias, void *workspace, void *stream) {
+    GnGeom g;
+    ct_status st = resolve_norm(desc, &g);
+    if (st != CT_OK) return st;
+    GnArgs a;
+    st = norm_args(desc, g, weight, bias, p, seed, offset, rng, workspace, gn_backward_ws(g), &a);
+    if (st != CT_OK) return st;
+    if (!dx && !dweight && !dbias) return CT_OK;
+    if (g.N * g.E > 0 && (!dy || !x || !mean || !rstd)) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(desc->dtype), pb = dtype_bytes(desc->param_dtype);
+    if (!aligned(x, eb) || !aligned(dy, eb) || !aligned(dx, eb) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+        !aligned(dweight, pb) || !aligned(dbias, pb))
+        return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    a.x = x;
+    a.dy = dy;
+    a.mean = const_cast<float *>(mean);
+    a.rstd = const_cast<float *>(rstd);
+    a.dx = dx;
+    a.dweight = dweight;
+    a.dbias = dbias;
+    return gn_backward(g, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_dropout(int32_t dtype, int64_t n, const void *x, const void *residual, double p, uint64_t seed,
+                     uint64_t offset, const void *rng, void *y, void *stream) {
+    if (!known_dtype(dtype)) return CT_ERR_DTYPE;
+    if (n < 0 || n > kMaxElems) return CT_ERR_ATTR;
+    RngArgs r;
+    ct_status st = resolve_rng(p, seed, offset, rng, &r);
+    if (st != CT_OK) return st;
+    if (n == 0) return CT_OK;
+    if (!x || !y) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(dtype);
+    if (!aligned(x, eb) || !aligned(residual, eb) || !aligned(y, eb)) return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    return dropout_run(dtype, x, residual, y, n, r, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ct_status ct_take_device_error(void *stream, int32_t *code) {

@@ -1,0 +1,68 @@
+// Philox4x32-10, the counter-based generator of Salmon, Moraes, Dror and Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3" (2011), and the keep decisions
+// of dropout drawn from it.
+//
+// Element i of a tensor takes 16-bit value i % 8 (low half of word 0 first) of
+// the block at counter (i / 8, offset) under the key `seed`: one evaluation
+// serves the eight elements that a thread loads at once, and a mask is a
+// function of (i, seed, offset) alone, so the backward pass draws it again
+// instead of reading it.  Sixteen bits per element halve the evaluations that
+// 32 would need; the drop probability is rounded to a multiple of 2^-16.
+#pragma once
+
+#include <stdint.h>
+
+namespace ct {
+
+struct RngArgs {
+    uint64_t seed, offset;
+    const uint64_t *dev;   // when set: {seed, offset} read on the device instead
+    uint32_t threshold;    // dropped where the 16-bit value is below it
+    float scale;           // 65536 / (65536 - threshold); 0 when all is dropped
+};
+
+#ifdef __CUDACC__
+
+struct Philox {
+    uint32_t k0, k1, c2, c3;
+
+    __device__ __forceinline__ explicit Philox(const RngArgs &a) {
+        const uint64_t s = a.dev ? a.dev[0] : a.seed, o = a.dev ? a.dev[1] : a.offset;
+        k0 = (uint32_t)s;
+        k1 = (uint32_t)(s >> 32);
+        c2 = (uint32_t)o;
+        c3 = (uint32_t)(o >> 32);
+    }
+
+    __device__ __forceinline__ uint4 operator()(uint64_t block) const {
+        uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = c2, x3 = c3;
+        uint32_t a = k0, b = k1;
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+            const uint64_t p0 = (uint64_t)x0 * 0xD2511F53u, p1 = (uint64_t)x2 * 0xCD9E8D57u;
+            x0 = (uint32_t)(p1 >> 32) ^ x1 ^ a;
+            x1 = (uint32_t)p1;
+            x2 = (uint32_t)(p0 >> 32) ^ x3 ^ b;
+            x3 = (uint32_t)p0;
+            a += 0x9E3779B9u;
+            b += 0xBB67AE85u;
+        }
+        return make_uint4(x0, x1, x2, x3);
+    }
+};
+
+// Bit k: element k of the block is kept.
+__device__ __forceinline__ uint32_t keep_bits(uint4 r, uint32_t threshold) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m |= (uint32_t)((w[j] & 0xFFFFu) >= threshold) << (2 * j);
+        m |= (uint32_t)((w[j] >> 16) >= threshold) << (2 * j + 1);
+    }
+    return m;
+}
+
+#endif
+
+}  // namespace ct

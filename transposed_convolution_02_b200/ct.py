@@ -12,7 +12,9 @@ Attribute names follow the ai.onnx.ConvTranspose README ("Attributes");
 weight [C_in, K.., O/groups], padding as (lo, hi) per spatial dim).
 """
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -24,7 +26,7 @@ CT_OK = 0
 STATUS_NAMES = {0: "CT_OK", 1: "CT_ERR_CHANNELS", 2: "CT_ERR_SPAN", 3: "CT_ERR_DTYPE",
                 4: "CT_ERR_ATTR", 5: "CT_ERR_ALIGN", 6: "CT_ERR_NULL", 7: "CT_ERR_DEVICE",
                 8: "CT_ERR_WORKSPACE", 9: "CT_ERR_UNSUPPORTED", 10: "CT_ERR_NOMEM"}
-CT_F32, CT_F16 = 0, 1
+CT_F32, CT_F16, CT_BF16 = 0, 1, 2
 CT_NCHW, CT_NHWC = 0, 1
 AUTOPAD = {"NOTSET": 0, "SAME_UPPER": 1, "SAME_LOWER": 2, "VALID": 3}
 ALGO = {"auto": 0, "generic": 1, "dense_tc": 2, "fp32_gemm": 3, "grouped": 4,
@@ -36,7 +38,8 @@ EXPORTED = ["ct_output_shape", "ct_plan", "ct_plan_kernel", "ct_plan_launches",
             "ct_prepacked_weight_bytes",
             "ct_workspace_bytes", "ct_prepack_weights", "ct_run", "ct_run_parts",
             "ct_run_noalloc", "ct_plan_destroy", "ct_status_string", "ct_take_device_error",
-            "ct_selftest_wait_timeout"]
+            "ct_selftest_wait_timeout", "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
+            "ct_group_norm_workspace_bytes"]
 
 
 class CtError(RuntimeError):
@@ -57,6 +60,13 @@ class ct_desc(ctypes.Structure):
                 ("has_kernel_shape", ctypes.c_int32), ("has_output_shape", ctypes.c_int32),
                 ("kernel_shape", ctypes.c_int64 * 3), ("output_shape", ctypes.c_int64 * 3),
                 ("algo", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class ct_group_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("N", ctypes.c_int64), ("S", ctypes.c_int64), ("C", ctypes.c_int64),
+                ("groups", ctypes.c_int64), ("eps", ctypes.c_double)]
 
 
 _lib = None
@@ -89,11 +99,18 @@ def lib():
         L.ct_plan_destroy.argtypes = [P]
         L.ct_plan_destroy.restype = None
         L.ct_take_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_int32)]
+        gp, u64, f64 = ctypes.POINTER(ct_group_norm_desc), ctypes.c_uint64, ctypes.c_double
+        L.ct_dropout.argtypes = [ctypes.c_int32, ctypes.c_int64, P, P, f64, u64, u64, P, P, P]
+        L.ct_group_norm_workspace_bytes.argtypes = [gp, szp, szp]
+        L.ct_group_norm.argtypes = [gp, P, P, P, f64, u64, u64, P, P, P, P, P, P]
+        L.ct_group_norm_backward.argtypes = [gp, P, P, P, P, P, P, f64, u64, u64, P, P, P, P, P, P]
         L.ct_status_string.argtypes = [ctypes.c_int]
         L.ct_status_string.restype = ctypes.c_char_p
         for name in ("ct_output_shape", "ct_plan", "ct_plan_launches", "ct_prepacked_weight_bytes",
                      "ct_workspace_bytes", "ct_prepack_weights", "ct_run", "ct_run_parts",
-                     "ct_run_noalloc", "ct_take_device_error", "ct_selftest_wait_timeout"):
+                     "ct_run_noalloc", "ct_take_device_error", "ct_selftest_wait_timeout",
+                     "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
+                     "ct_group_norm_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -209,6 +226,8 @@ def ct_plan_destroy(plan):
 # ---- descriptor construction ----------------------------------------------
 
 ACTIVATION = {"identity": 0, "relu": 1}
+NORM_ACTIVATION = {"identity": 0, "relu": 1, "silu": 2, "gelu": 3}
+NORM_DTYPE = {torch.float32: CT_F32, torch.float16: CT_F16, torch.bfloat16: CT_BF16}
 
 
 def make_desc(x_shape, w_shape, *, dtype, layout="nchw", strides=None, dilations=None,
@@ -378,3 +397,218 @@ def conv_transpose_nhwc(x, w, bias=None, *, stride, padding, output_padding, gro
                        dilations=dilation, pads=pads, output_padding=output_padding,
                        group=groups, algo=algo, activation=activation)
     return op(x)
+
+
+# ---- group norm and dropout ---------------------------------------------------
+
+def _overlap(a, b):
+    """Whether two contiguous tensors share memory."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    return (a0 < b0 + b.numel() * b.element_size() and b0 < a0 + a.numel() * a.element_size())
+
+
+def check_like(t, name, x):
+    """Refuse a tensor that has not X's shape, dtype and device."""
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError("%s must be a %s tensor of shape %s on %s"
+                         % (name, x.dtype, list(x.shape), x.device))
+
+
+def check_out(out, x, inputs, in_place=False):
+    """Refuse an output that the kernels could not fill: not like X, not dense,
+    or over an input (`in_place`: exactly on one of them is fine)."""
+    check_like(out, "out", x)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    for t in inputs:
+        if t is not None and _overlap(out, t) and not (in_place and out.data_ptr() == t.data_ptr()
+                                                       and t.is_contiguous()):
+            raise ValueError("out overlaps an input")
+
+
+def check_random(p, seed, offset, rng, device):
+    """Refuse a drop probability outside [0, 1], a seed or offset outside
+    64 bits, and an rng that is not two int64 words on X's device."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError("p must be in [0, 1]")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be in [0, 2^64)")
+    if rng is not None and (rng.dtype != torch.int64 or rng.device != device or rng.dim() != 1
+                            or rng.numel() != 2 or not rng.is_contiguous()):
+        raise ValueError("rng must be an int64 tensor [seed, offset] on %s" % (device,))
+
+
+def check_norm(x, groups, weight, bias, activation):
+    """Refuse arguments that the group norm cannot take."""
+    if x.dtype not in NORM_DTYPE:
+        raise ValueError("X must be float32, float16 or bfloat16, not %s" % x.dtype)
+    if x.dim() < 2:
+        raise ValueError("X must be [N, D.., C], it has shape %s" % list(x.shape))
+    c = x.shape[-1]
+    if groups < 1 or c < 1 or c % groups != 0:
+        raise ValueError("%d channels cannot be split into %d groups" % (c, groups))
+    if activation not in NORM_ACTIVATION:
+        raise ValueError("activation must be one of %s, not %r" % (sorted(NORM_ACTIVATION), activation))
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if t.dtype != torch.float32 and t.dtype != x.dtype:
+            raise ValueError("%s must be float32 or X's %s, not %s" % (name, x.dtype, t.dtype))
+        if t.dim() != 1 or t.numel() != c or t.device != x.device:
+            raise ValueError("%s must have shape [%d] on %s" % (name, c, x.device))
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+
+
+def _check_cuda(x, *leaves):
+    """The operators run on CUDA tensors only and record no autograd graph: a
+    call that would drop a gradient silently is refused."""
+    if not x.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x,) + leaves):
+        raise ValueError("an input requires a gradient, and this call records none: call it under "
+                         "torch.no_grad() and use the _backward function")
+
+
+@contextlib.contextmanager
+def _other_place(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _place(device, stream):
+    """Context in which tensors are allocated and kernels launched: X's device
+    and the given stream (the device's current one by default)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is on %s, X on %s" % (stream.device, device))
+    return _other_place(device, stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_desc(n, s, c, groups, dtype, param_dtype, activation, eps):
+    """A group norm's descriptor and its two workspace sizes: sizes only, no
+    device memory."""
+    d = ct_group_norm_desc(NORM_DTYPE[dtype], NORM_DTYPE[param_dtype], NORM_ACTIVATION[activation], 0,
+                           n, s, c, groups, eps)
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    st = lib().ct_group_norm_workspace_bytes(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b))
+    if st != CT_OK:
+        raise CtError(st, "ct_group_norm_workspace_bytes")
+    return d, f.value, b.value
+
+
+def _norm_desc_of(x, groups, weight, bias, activation, eps):
+    n, c = x.shape[0], x.shape[-1]
+    s = 1
+    for v in x.shape[1:-1]:
+        s *= v
+    one = weight if weight is not None else bias
+    return _norm_desc(n, s, c, groups, x.dtype, torch.float32 if one is None else one.dtype, activation,
+                      float(eps))
+
+
+def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="identity", p=0.0,
+                    seed=0, offset=0, rng=None, out=None, return_stats=False, stream=None):
+    """Group norm of channels-last X[N, D.., C] (what conv_transpose_nhwc
+    returns), then the activation (identity, relu, silu or gelu), then dropout
+    with probability p (see dropout for seed, offset and rng): float32,
+    float16 or bfloat16, weight and bias [C] in X's dtype or float32.
+
+    Returns Y, or (Y, mean, rstd) with ``return_stats``: mean and rstd are
+    float32 [N, groups], what group_norm_nhwc_backward takes."""
+    check_norm(x, groups, weight, bias, activation)
+    if p:
+        check_random(p, seed, offset, rng, x.device)
+    if out is not None:
+        check_out(out, x, (x,))
+    _check_cuda(x, weight, bias)
+    desc, ws_bytes, _ = _norm_desc_of(x, groups, weight, bias, activation, eps)
+    dev = x.device
+    with _place(dev, stream):
+        x = x.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        y = torch.empty_like(x) if out is None else out
+        stats = torch.empty((2, desc.N, groups), dtype=torch.float32, device=dev) if return_stats else None
+        mean, rstd = stats.unbind(0) if return_stats else (None, None)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        st = lib().ct_group_norm(desc, x.data_ptr(), _addr(weight), _addr(bias), p, seed, offset,
+                                 _addr(rng), y.data_ptr(), _addr(mean), _addr(rstd), ws.data_ptr(),
+                                 torch.cuda.current_stream().cuda_stream)
+    if st != CT_OK:
+        raise CtError(st, "ct_group_norm")
+    return (y, mean, rstd) if return_stats else y
+
+
+def group_norm_nhwc_backward(dy, x, mean, rstd, groups, weight=None, bias=None, *, activation="identity",
+                             p=0.0, seed=0, offset=0, rng=None, need_x_grad=True, stream=None):
+    """Gradients (dx, dweight, dbias) of group_norm_nhwc at dy, from the X,
+    mean and rstd, the weight and bias and the p, seed, offset and rng of the
+    forward call.  None for dx without ``need_x_grad``, and for the gradient
+    of a weight or bias that is None."""
+    check_norm(x, groups, weight, bias, activation)
+    check_like(dy, "dy", x)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (x.shape[0], groups) or t.device != x.device:
+            raise ValueError("%s must be a float32 tensor of shape %s on %s"
+                             % (name, [x.shape[0], groups], x.device))
+    if p:
+        check_random(p, seed, offset, rng, x.device)
+    _check_cuda(x, dy, weight, bias)
+    desc, _, ws_bytes = _norm_desc_of(x, groups, weight, bias, activation, 0.0)
+    dev = x.device
+    with _place(dev, stream):
+        x, dy, mean, rstd = x.contiguous(), dy.contiguous(), mean.contiguous(), rstd.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        bias = None if bias is None else bias.contiguous()
+        dx = torch.empty_like(x) if need_x_grad else None
+        dweight = None if weight is None else torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        st = lib().ct_group_norm_backward(desc, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
+                                          rstd.data_ptr(), _addr(weight), _addr(bias), p, seed, offset,
+                                          _addr(rng), _addr(dx), _addr(dweight), _addr(dbias),
+                                          ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    if st != CT_OK:
+        raise CtError(st, "ct_group_norm_backward")
+    return dx, dweight, dbias
+
+
+def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream=None):
+    """Dropout of X with probability p (in steps of 2^-16), plus an optional
+    residual: kept elements are scaled so that the expectation is X.
+
+    Which elements stay is a function of their index, seed and offset alone
+    (Philox4x32-10), so no mask is stored: give dropout_backward the same
+    numbers.  ``rng``, an int64 CUDA tensor [seed, offset], is read on the
+    device in their place: a captured graph then draws a new mask at each
+    replay once the tensor is changed.  ``out`` may be X or the residual."""
+    if x.dtype not in NORM_DTYPE:
+        raise ValueError("X must be float32, float16 or bfloat16, not %s" % x.dtype)
+    check_random(p, seed, offset, rng, x.device)
+    if residual is not None:
+        check_like(residual, "residual", x)
+    if out is not None:
+        check_out(out, x, (x, residual), in_place=True)
+    _check_cuda(x, residual)
+    with _place(x.device, stream):
+        x = x.contiguous()
+        residual = None if residual is None else residual.contiguous()
+        y = torch.empty_like(x) if out is None else out
+        st = lib().ct_dropout(NORM_DTYPE[x.dtype], x.numel(), x.data_ptr(), _addr(residual), p, seed,
+                              offset, _addr(rng), y.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    if st != CT_OK:
+        raise CtError(st, "ct_dropout")
+    return y
+
+
+def dropout_backward(dy, p, *, seed=0, offset=0, rng=None, out=None, stream=None):
+    """The gradient of dropout in X at dy, for the p, seed, offset and rng of
+    the forward call (the residual's gradient is dy itself)."""
+    return dropout(dy, p, seed=seed, offset=offset, rng=rng, out=out, stream=stream)
