@@ -229,7 +229,8 @@ def test_backward_does_not_write_around_dx():
     x, w, b, dy = (v.cuda() for v in inputs(shape, t, 310))
     _, mean, rstd = ct.group_norm_nhwc(x, groups, w, b, return_stats=True)
     want = ct.group_norm_nhwc_backward(dy, x, mean, rstd, groups, w, b)
-    desc, _, nb = ct._norm_desc_of(x, groups, w, b, "identity", 0.0)
+    norm = ct._norm_of(x, groups, w, b, "identity", 0.0)
+    desc, nb = norm.desc, norm.backward_bytes
     ws = torch.full((nb + 256,), 0xFF, dtype=torch.uint8, device="cuda")   # a workspace of NaNs
     for off in (0, 3):
         dx, xbuf = guarded(shape, t, off)

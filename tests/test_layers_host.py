@@ -90,7 +90,11 @@ def test_group_norm_desc_refusals(over, status):
 def test_group_norm_null_and_workspace():
     assert _ws_status(None) == 6
     L = ct.lib()
-    d = ctypes.byref(_desc())
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    big = _desc(S=1 << 20)         # long images: both directions need a workspace
+    assert L.ct_group_norm_workspace_bytes(ctypes.byref(big), ctypes.byref(f), ctypes.byref(b)) == 0
+    assert f.value > 0 and b.value > 0
+    d = ctypes.byref(big)
     a = 1 << 20          # an aligned address that is never followed: every call is refused before a launch
     args = [d, a, a, a, 0.1, 1, 2, None, a, None, None, a, None]
     def fwd(**over):
@@ -216,10 +220,26 @@ def test_checks_of_overlap_and_gradients():
 
 
 def test_descriptor_follows_sizes():
-    a = ct._norm_desc_of(torch.zeros(2, 3, 5, 8, dtype=torch.float16), 4, None, None, "silu", 1e-5)
-    assert (a[0].N, a[0].S, a[0].C, a[0].groups) == (2, 15, 8, 4)
-    assert (a[0].dtype, a[0].param_dtype, a[0].activation) == (1, 0, 2)
-    b = ct._norm_desc_of(torch.zeros(2, 8, dtype=torch.bfloat16), 4, None,
-                         torch.zeros(8, dtype=torch.bfloat16), "gelu", 0)
-    assert (b[0].S, b[0].dtype, b[0].param_dtype, b[0].activation) == (1, 2, 2, 3)
-    assert a[1] > 0 and a[2] > 0
+    a = ct._norm_of(torch.zeros(2, 3, 5, 8, dtype=torch.float16), 4, None, None, "silu", 1e-5)
+    assert (a.desc.N, a.desc.S, a.desc.C, a.desc.groups) == (2, 15, 8, 4)
+    assert (a.desc.dtype, a.desc.param_dtype, a.desc.activation) == (1, 0, 2)
+    b = ct._norm_of(torch.zeros(2, 8, dtype=torch.bfloat16), 4, None, torch.zeros(8, dtype=torch.bfloat16),
+                    "gelu", 0)
+    assert (b.desc.S, b.desc.dtype, b.desc.param_dtype, b.desc.activation) == (1, 2, 2, 3)
+    assert a.stats == (2, 4) and a.forward_bytes >= 0 and a.backward_bytes > 0
+
+
+def test_checks_hold_on_sizes_seen_before():
+    """The checks by size are made once; those of the parameters every time."""
+    x, w = torch.zeros(2, 3, 24), torch.zeros(24)
+    for _ in range(2):
+        ct._norm_of(x, 4, w, w, "silu", 1e-5)
+        for bad in (w[:23], w.half(), w.to("meta"), w.view(4, 6)):
+            with pytest.raises(ValueError):
+                ct._norm_of(x, 4, w, bad, "silu", 1e-5)
+            with pytest.raises(ValueError):
+                ct._norm_of(x, 4, bad, w, "silu", 1e-5)
+        with pytest.raises(ValueError):
+            ct._norm_of(x, 5, w, w, "silu", 1e-5)
+        with pytest.raises(ct.CtError):
+            ct._norm_of(x, 4, w, w, "silu", -1.0)

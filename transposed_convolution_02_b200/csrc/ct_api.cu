@@ -243,7 +243,7 @@ ct_status resolve_rng(double p, uint64_t seed, uint64_t offset, const void *rng,
 
 constexpr int64_t kMaxNormChannels = int64_t(1) << 24;
 
-ct_status resolve_norm(const ct_group_norm_desc *d, GnGeom *g) {
+ct_status resolve_norm(const ct_group_norm_desc *d, int tensors, GnGeom *g) {
     if (!d) return CT_ERR_NULL;
     if (!known_dtype(d->dtype)) return CT_ERR_DTYPE;
     if (d->param_dtype != CT_F32 && d->param_dtype != d->dtype) return CT_ERR_DTYPE;
@@ -254,7 +254,7 @@ ct_status resolve_norm(const ct_group_norm_desc *d, GnGeom *g) {
     if (d->groups < 1 || d->C % d->groups != 0) return CT_ERR_CHANNELS;
     if (mul_capped(mul_capped(d->N, d->S), d->C) < 0) return CT_ERR_ATTR;
     if (mul_capped(d->S, d->C) < 0) return CT_ERR_ATTR;
-    *g = gn_geom(d->N, d->S, d->C, d->groups);
+    *g = gn_geom(d->N, d->S, d->C, d->groups, d->dtype, tensors);
     return CT_OK;
 }
 
@@ -450,9 +450,10 @@ ct_status ct_group_norm_workspace_bytes(const ct_group_norm_desc *desc, size_t *
                                         size_t *backward_bytes) {
     if (!forward_bytes || !backward_bytes) return CT_ERR_NULL;
     GnGeom g;
-    ct_status st = resolve_norm(desc, &g);
+    ct_status st = resolve_norm(desc, 1, &g);
     if (st != CT_OK) return st;
     *forward_bytes = gn_forward_ws(g);
+    resolve_norm(desc, 2, &g);
     *backward_bytes = gn_backward_ws(g);
     return CT_OK;
 }
@@ -461,7 +462,7 @@ ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, const voi
                         double p, uint64_t seed, uint64_t offset, const void *rng, void *y, float *mean,
                         float *rstd, void *workspace, void *stream) {
     GnGeom g;
-    ct_status st = resolve_norm(desc, &g);
+    ct_status st = resolve_norm(desc, 1, &g);
     if (st != CT_OK) return st;
     if (g.N == 0) return CT_OK;
     GnArgs a;
@@ -484,7 +485,7 @@ ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const void *dy,
                                  uint64_t seed, uint64_t offset, const void *rng, void *dx, void *dweight,
                                  void *dbias, void *workspace, void *stream) {
     GnGeom g;
-    ct_status st = resolve_norm(desc, &g);
+    ct_status st = resolve_norm(desc, 2, &g);
     if (st != CT_OK) return st;
     GnArgs a;
     st = norm_args(desc, g, weight, bias, p, seed, offset, rng, workspace, gn_backward_ws(g), &a);

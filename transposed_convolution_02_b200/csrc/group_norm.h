@@ -2,33 +2,84 @@
 // the kernels.
 //
 // The elements of image n are one contiguous run of S*C; kernels read it as
-// aligned vectors of eight elements counted from the run's start rounded down
-// to a multiple of eight (`head` elements before it belong to the previous
-// image).  A "row" is the shortest run of whole pixels that is a multiple of
-// eight elements: L = C * 8 / gcd(C, 8), so a thread that keeps its column
-// and walks the rows always meets the same eight channels, for any C, and
-// holds its channels' coefficients and sums in registers.
+// aligned vectors of 16 bytes (V elements: 8 of a 16-bit type, 4 of fp32)
+// counted from the run's start rounded down to a multiple of V (`head`
+// elements before it belong to the previous image).  A "row" is the shortest
+// run of whole pixels that is a multiple of V elements, L = C * V / gcd(C, V):
+// a thread that keeps its column and walks the rows always meets the same V
+// channels, for any C, and holds its channels' coefficients and sums in
+// registers.  Rows wider than a block's threads are cut into column tiles; a
+// tile of an image is a "strip", and every strip is cut into `chunks` runs of
+// `rpc` rows, one to a block.  The blocks of a cluster work on neighbouring
+// chunks of one strip.  Divisions by these sizes are multiplications by
+// host-made factors: a block's fixed work counts where images are small.
 #pragma once
 
 #include <stdint.h>
 
+#include "ct_divmagic.h"
 #include "ct_internal.h"
 #include "philox.cuh"
 
 namespace ct {
 
+#ifndef CT_GN_WAVE
+#define CT_GN_WAVE (40ll << 20)
+#endif
+#ifndef CT_GN_FU
+#define CT_GN_FU 4
+#endif
+#ifndef CT_GN_BU
+#define CT_GN_BU 2
+#endif
+#ifndef CT_GN_MIN
+#define CT_GN_MIN 4
+#endif
+#ifndef CT_GN_BMIN
+#define CT_GN_BMIN 3
+#endif
+#ifndef CT_GN_APPLY
+#define CT_GN_APPLY 1
+#endif
+#ifndef CT_GN_CL
+#define CT_GN_CL 4
+#endif
+#ifndef CT_GN_FCL
+#define CT_GN_FCL 8
+#endif
+constexpr int kThreads = 256;
+constexpr int kForwardBlocks = CT_GN_MIN, kBackwardBlocks = CT_GN_BMIN;   // per SM
+constexpr int kForwardUnroll = CT_GN_FU, kBackwardUnroll = CT_GN_BU;     // vectors in flight per thread and tensor
+constexpr int64_t kWaveBytes = CT_GN_WAVE;
+constexpr int kMaxColumns = 256;                                         // vectors across a column tile
+constexpr int kMaxPushed = 1024;                                         // group sums that a block takes from its cluster
+
 struct GnGeom {
     int64_t N, S, E;       // images, pixels per image, elements per image (S*C)
-    int32_t C, G, Cg;
+    int32_t C, G, Cg, V;
     int32_t wraps;         // pixels per row, L / C
-    int32_t LV;            // vectors per row, L / 8
+    int32_t LV;            // vectors per row, L / V
+    int64_t full_rows;     // rows of E / V vectors that are whole
+    int32_t full_rest;     // and the vectors beyond them
     int64_t rows;          // rows that cover any image, head included
     int32_t bx, by;        // a block's threads: columns x rows
     int32_t ctiles;        // column tiles per row
-    int64_t rpc;           // rows per chunk
-    int32_t chunks;        // chunks per image
-    int64_t items;         // N * chunks * ctiles
+    int32_t rpc, chunks;   // rows per chunk; chunks per strip
+    int32_t apply_rpc, apply_chunks;   // the same of the launch that applies
+    int32_t cluster;       // blocks per cluster
+    int32_t parts;         // clusters per strip, the parts of its sums
+    bool fused;            // one cluster per strip: both passes in one launch
+    int64_t wave;          // images per wave
+    DivMagic by_bx, by_by, by_cg;   // divisors bx, by, Cg
 };
+
+// Groups that a column tile can meet.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int groups_max(const GnGeom &g) {
+    return g.G < g.bx * g.V + 1 ? g.G : g.bx * g.V + 1;
+}
 
 struct GnArgs {
     int dtype, param_dtype, act;
@@ -41,11 +92,18 @@ struct GnArgs {
     float *ws;
 };
 
-GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G);
+// `tensors`: how many tensors of x's size a wave's second pass reads (from L2).
+GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensors);
 size_t gn_forward_ws(const GnGeom &g);
 size_t gn_backward_ws(const GnGeom &g);
 ct_status gn_forward(const GnGeom &g, const GnArgs &a, cudaStream_t st);
 ct_status gn_backward(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_forward_f32(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_forward_f16(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_forward_bf16(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_backward_f32(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_backward_f16(const GnGeom &g, const GnArgs &a, cudaStream_t st);
+ct_status gn_backward_bf16(const GnGeom &g, const GnArgs &a, cudaStream_t st);
 
 ct_status dropout_run(int dtype, const void *x, const void *residual, void *y, int64_t n, const RngArgs &rng,
                       cudaStream_t st);

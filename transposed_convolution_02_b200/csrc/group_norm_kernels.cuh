@@ -1,0 +1,1218 @@
+// Channels-last group norm with its activation and dropout, forward and
+// backward.
+//
+// Per image n and group g (C/G channels, all S pixels, M = S*C/G values):
+//   mean = sum x / M,  var = sum (x - mean)^2 / M,  rstd = (var + eps)^-1/2,
+//   h = (x - mean) rstd,  a = h w + b,  y = drop(act(a)).
+// With da = drop(dy) act'(a) and dh = da w:
+//   dw = sum da h,  db = sum da  (over images and pixels),
+//   dx = rstd (dh - mean(dh) - h mean(dh h))  (means over the group).
+//
+// Bound: HBM.  Forward must read x and write y, backward read x and dy and
+// write dx.  Both need a whole group's sums before the first output, so there
+// are two passes, and the second is to find its inputs in L2.
+//   Fused: one cluster works on a strip of an image, joins its blocks' sums
+// through distributed shared memory and goes on to the second pass in the same
+// launch.  For images small enough that those under work at a time fit in L2,
+// and enough of them to fill the GPU (or too little work for that to matter).
+//   Two launches else: images are taken in waves of at most kWaveBytes, each
+// summed (a cluster joins its blocks' sums and writes one part) and then
+// applied (the parts joined again by each block).  A launch starts while the
+// one before it ends (programmatic dependent launch) and waits for it only
+// where it needs its sums or ends itself.
+//
+// Statistics: a thread sums x - k and (x - k)^2 of its few values per
+// channel, k being the first of them, then everything is merged as (count,
+// mean, M2) with M2 the sum of squared distances from the mean.  As k is one
+// of the n values summed, sum (x - k)^2 <= n M2, so the subtraction that
+// gives M2 loses at most a factor of the thread's n, however far the mean is
+// from 0.
+#pragma once
+
+#include <string.h>
+
+#include "ct_cuda_util.h"
+#include "group_norm.h"
+#include "sm100.cuh"
+#include "vec16.cuh"
+
+namespace ct {
+
+namespace {
+
+using sm100::cluster_ctarank;
+using sm100::cluster_sync;
+using sm100::griddep_launch_dependents;
+using sm100::griddep_wait;
+
+struct Params {      // kernel arguments besides the geometry
+    const void *x, *dy, *weight, *bias;
+    void *y, *dx, *dweight, *dbias;
+    float *mean, *rstd;
+    float4 *part;    // forward, per strip, part and group: (count, mean, M2, -)
+    float2 *sums;    // backward, per strip, part and group: (sum dh, sum dh h)
+    float2 *chan;    // backward, per strip, chunk and channel: (sum da, sum da h)
+    float eps;
+    int param_dtype;
+    bool vec;
+    RngArgs rng;
+    int64_t strip0;  // this launch's strips: strip0 .. strip0 + strips - 1
+    int64_t strips;
+    int rpc;         // rows of a strip to a block
+};
+
+__device__ __forceinline__ float param(const void *p, int c, int dtype, float none) {
+    if (!p) return none;
+    if (dtype == CT_F32) return ((const float *)p)[c];
+    if (dtype == CT_F16) return __half2float(((const __half *)p)[c]);
+    return __bfloat162float(((const __nv_bfloat16 *)p)[c]);
+}
+
+__device__ __forceinline__ void put_param(void *p, int64_t i, int dtype, float v) {
+    if (dtype == CT_F32) ((float *)p)[i] = v;
+    else if (dtype == CT_F16) ((__half *)p)[i] = __float2half_rn(v);
+    else ((__nv_bfloat16 *)p)[i] = __float2bfloat16_rn(v);
+}
+
+// Two neighbours at a time: the packed fp32 instructions of sm_100 do two
+// additions, products or multiply-adds per issue slot.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+__device__ __forceinline__ float2 sigmoid2(float2 a) {
+    const float2 e = mul2(a, both(-1.44269504f));
+    float2 d;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d.y) : "f"(e.y));
+    d = add2(d, both(1.f));
+    float2 s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+    return s;
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value(float2 a) {
+    if (ACT == CT_ACT_RELU) return make_float2(a.x < 0.f ? 0.f : a.x, a.y < 0.f ? 0.f : a.y);
+    if (ACT == CT_ACT_SILU) return mul2(a, sigmoid2(a));
+    if (ACT == CT_ACT_GELU)
+        return make_float2(0.5f * a.x * (1.f + erff(a.x * 0.70710678f)),
+                           0.5f * a.y * (1.f + erff(a.y * 0.70710678f)));
+    return a;
+}
+
+__device__ __forceinline__ float gelu_slope(float a) {
+    return 0.5f * (1.f + erff(a * 0.70710678f)) + a * __expf(-0.5f * a * a) * 0.39894228f;
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_slope(float2 a) {
+    if (ACT == CT_ACT_RELU) return make_float2(a.x > 0.f ? 1.f : 0.f, a.y > 0.f ? 1.f : 0.f);
+    if (ACT == CT_ACT_SILU) {
+        const float2 s = sigmoid2(a);
+        return fma2(s, fma2(neg2(s), a, a), s);   // s + s a (1 - s)
+    }
+    if (ACT == CT_ACT_GELU) return make_float2(gelu_slope(a.x), gelu_slope(a.y));
+    return both(1.f);
+}
+
+// One block's chunk of a strip, and the strip's place: all fields are the
+// same in every thread but the last ones.
+struct Share {
+    int64_t strip, n;      // strip; image
+    int64_t e0;            // the image's first element
+    int head;
+    int p0, p1;            // the tile's positions within a row
+    int first_group, groups;   // the groups that they meet, counted modulo G
+    // this thread's column and row (-1: it has none), its vectors that no end
+    // of the image cuts, and those that one cuts
+    int col, ty;
+    int first, last;                 // whole vectors: rows ty + i * by of the chunk, first <= i < last
+    int64_t e, cut_head, cut_tail;   // elements (of i = 0), -1 where there is none
+    int64_t r0;                      // the chunk's first row
+    int rows;
+    int64_t whole_rows;              // the image's vectors that its end does not cut: rows, and those beyond
+    int rest;
+};
+
+// A block's share of strip p.strip0 + `local`: its chunk is blockIdx.x.  PLAIN:
+// a pixel is a whole number of vectors, one column tile, aligned tensors; then
+// nothing is cut, a position is its channel and a row a pixel.
+template <bool PLAIN>
+struct Shares {
+    const GnGeom &g;
+    const Params &p;
+    int tx, ty;
+
+    __device__ __forceinline__ Shares(const GnGeom &geom, const Params &par) : g(geom), p(par) {
+        ty = divq(threadIdx.x, g.by_bx);
+        tx = threadIdx.x - ty * g.bx;
+    }
+    __device__ __forceinline__ void get(int64_t local, Share &t) {
+        t.strip = p.strip0 + local;
+        if (PLAIN) {
+            t.n = t.strip;
+            t.e0 = t.n * g.E;
+            t.head = t.p0 = t.first_group = t.first = 0;
+            t.p1 = g.C;
+            t.groups = g.G;
+            t.col = tx;
+            t.ty = ty < g.by ? ty : -1;
+            t.cut_head = t.cut_tail = -1;
+            t.r0 = (int64_t)blockIdx.x * p.rpc;
+            t.rows = g.S - t.r0 < p.rpc ? (int)(g.S - t.r0) : p.rpc;   // S may be 0, where g.rows is 1
+            if (t.rows < 0) t.rows = 0;
+            t.e = t.e0 + (t.r0 + ty) * g.C + tx * g.V;
+            t.last = t.ty >= 0 && t.rows > ty ? divq(t.rows - ty + g.by - 1, g.by_by) : 0;
+            t.whole_rows = g.S;
+            t.rest = 0;
+            return;
+        }
+        int ct = 0;
+        t.n = t.strip;
+        if (g.ctiles > 1) {
+            t.n = t.strip / g.ctiles;
+            ct = (int)(t.strip - t.n * g.ctiles);
+        }
+        t.e0 = t.n * g.E;
+        t.head = (int)t.e0 & (g.V - 1);
+        t.p0 = ct * g.bx * g.V;
+        t.p1 = (ct + 1) * g.bx < g.LV ? t.p0 + g.bx * g.V : g.LV * g.V;
+        const int c = channel(t, t.p0);
+        t.first_group = divq(c, g.by_cg);
+        t.groups = divq(t.p1 - t.p0 - 1 + (c - t.first_group * g.Cg), g.by_cg) + 1;
+        if (t.groups > g.G) t.groups = g.G;
+        t.col = ct * g.bx + tx;
+        t.ty = ty < g.by && t.col < g.LV ? ty : -1;
+        t.first = t.last = 0;
+        t.cut_head = t.cut_tail = -1;
+        // the image's vectors that its end does not cut: t.whole_rows rows and t.rest vectors
+        t.whole_rows = g.full_rows;
+        t.rest = g.full_rest;
+        const int over = ((int)g.E & (g.V - 1)) + t.head;
+        if (over >= g.V && ++t.rest == g.LV) {
+            t.rest = 0;
+            ++t.whole_rows;
+        }
+        t.r0 = (int64_t)blockIdx.x * p.rpc;
+        t.rows = g.rows - t.r0 < p.rpc ? (int)(g.rows - t.r0) : p.rpc;
+        if (t.rows < 0) t.rows = 0;
+        t.e = t.e0 - t.head + g.V * ((t.r0 + ty) * g.LV + t.col);
+        if (t.ty < 0) return;
+        if (t.head != 0 && t.r0 + ty == 0 && t.col == 0 && t.rows > 0) {
+            t.cut_head = t.e;
+            t.first = 1;
+        }
+        const int64_t whole = t.whole_rows + (t.col < t.rest ? 1 : 0) - t.r0;
+        const int end = whole < t.rows ? (int)whole : t.rows;
+        if (end > ty) t.last = divq(end - ty + g.by - 1, g.by_by);
+        if (t.last < t.first) t.last = t.first;
+        const int r = ty + t.last * g.by;   // the row after the whole ones
+        if ((over & (g.V - 1)) != 0 && r < t.rows && t.r0 + r == t.whole_rows && t.col == t.rest)
+            t.cut_tail = t.e + (int64_t)t.last * g.V * g.LV * g.by;
+    }
+    // the channel at position `pos` of a row
+    __device__ __forceinline__ int channel(const Share &t, int pos) const {
+        if (PLAIN || g.wraps == 1) return pos;
+        const int c = (pos - t.head) % g.C;
+        return c < 0 ? c + g.C : c;
+    }
+};
+
+// The elements of a cut vector that are the image's.
+__device__ __forceinline__ uint32_t cut_bits(const GnGeom &g, const Share &t, int64_t e) {
+    uint32_t m = 0;
+    for (int k = 0; k < g.V; ++k)
+        if (e + k >= t.e0 && e + k < t.e0 + g.E) m |= 1u << k;
+    return m;
+}
+
+__device__ __forceinline__ float &lane_of(float2 &v, int k) { return k & 1 ? v.y : v.x; }
+
+// The cluster's barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// f(element, pairs of each of N tensors, bits) for a thread's vectors: the
+// whole ones with U in flight, then those that an end of the image cuts (the
+// elements outside `bits` read as 0); on unaligned tensors all one by one.
+// pre() runs before the first of them, while the first loads are in flight.
+// BACK: the whole ones from the last to the first, so that a second pass over
+// a chunk begins with what the first one left in L2.
+template <typename T, bool PLAIN, bool BACK, int N, int U, typename Pre, typename F>
+__device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T *const (&src)[N], bool vec, Pre pre,
+                                       F f) {
+    constexpr int V = kVec<T>, P = V / 2;
+    const int64_t row = (int64_t)V * g.LV * g.by, step = BACK ? -row : row;
+    if (PLAIN || vec) {
+        int left = t.last - (PLAIN ? 0 : t.first);
+        int64_t e = t.e + (BACK ? t.last - 1 : PLAIN ? 0 : t.first) * row;
+        uint4 w[U][N];
+        auto load = [&](int u) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) w[u][j] = __ldg(reinterpret_cast<const uint4 *>(src[j] + e + u * step));
+        };
+        auto use = [&](int u) {
+            float2 v[N][P];
+#pragma unroll
+            for (int j = 0; j < N; ++j) unpack(w[u][j], v[j], T());
+            f(e + u * step, v, ~0u);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < left) load(u);
+        pre();
+        while (left > 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < left) use(u);
+            e += U * step;
+            left -= U;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < left) load(u);
+        }
+        if (PLAIN || (t.cut_head < 0 && t.cut_tail < 0)) return;
+    } else {
+        pre();
+    }
+#pragma unroll 1
+    for (int i = vec ? t.last : t.first; i < t.last + 2; ++i) {
+        const int64_t e = i < t.last ? t.e + i * row : i == t.last ? t.cut_head : t.cut_tail;
+        if (e < 0) continue;
+        const uint32_t bits = i < t.last ? ~0u : cut_bits(g, t, e);
+        float2 v[N][P];
+#pragma unroll
+        for (int j = 0; j < N; ++j) load_some(src[j] + e, bits, v[j]);
+        f(e, v, bits);
+    }
+}
+
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2)
+        if (o < lanes) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// log2 of the lanes that share one of `n` things: a power of two up to 32.
+__device__ __forceinline__ int log_lanes_for(int n) {
+    return n >= kThreads ? 0 : min(5, 31 - __clz(kThreads / n));
+}
+
+__device__ __forceinline__ int wrap_group(const GnGeom &g, int gi) { return gi >= g.G ? gi - g.G : gi; }
+
+// Store to shared address `p` of the cluster's block `rank`.
+__device__ __forceinline__ void push(float4 *p, int rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     sm100::mapa_shared(sm100::smem_u32(p), rank)),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// A computing thread's V values of a per-position array.
+template <int V>
+__device__ __forceinline__ void own(const float *at, const Share &t, float2 (&v)[V / 2]) {
+    const float4 *q = reinterpret_cast<const float4 *>(at + (t.col * V - t.p0));
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+        const float4 w = q[j];
+        v[2 * j] = make_float2(w.x, w.y);
+        v[2 * j + 1] = make_float2(w.z, w.w);
+    }
+}
+template <int V>
+__device__ __forceinline__ void put_own(float *at, const float2 (&v)[V / 2]) {
+    float4 *q = reinterpret_cast<float4 *>(at + threadIdx.x * V);
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) q[j] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+}
+
+// f(position in the tile, channel, group, the tile's number of the group)
+template <bool PLAIN, typename F>
+__device__ __forceinline__ void each_position(const GnGeom &g, const Shares<PLAIN> &shares, const Share &t, F f) {
+    for (int pos = threadIdx.x; pos < t.p1 - t.p0; pos += kThreads) {
+        if (PLAIN) {
+            const int gi = divq(pos, g.by_cg);
+            f(pos, pos, gi, gi);
+            continue;
+        }
+        const int c = shares.channel(t, t.p0 + pos), gi = divq(c, g.by_cg);
+        f(pos, c, gi, gi >= t.first_group ? gi - t.first_group : gi - t.first_group + g.G);
+    }
+}
+
+// f(position in the tile) for lane `lane` of `lanes` over the positions of a
+// group (or, with count 1, of a channel): channels c .. c + count - 1.
+template <bool PLAIN, typename F>
+__device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t, int c, int count, int lane, int lanes,
+                                                F f) {
+    for (int j = lane; j < count; j += lanes) {
+        if (PLAIN) {
+            f(c + j);
+            continue;
+        }
+        int pos = c + j + t.head;
+        if (pos >= g.C) pos -= g.C;
+        for (pos -= t.p0; pos < t.p1 - t.p0; pos += g.C)
+            if (pos >= 0) f(pos);
+    }
+}
+
+// Sums over the thread rows: ARRAYS arrays [by][bx * V], kThreads * V apart.
+// Every array's rows are cut into a few runs; run s is summed into row s, and
+// at(k, pos) adds the runs of array k.
+struct Columns {
+    const float *sums;
+    int width, apart, segs;
+    __device__ __forceinline__ float at(int k, int pos) const {
+        const float *a = sums + k * apart + pos;
+        float v = a[0];
+        for (int s = 1; s < segs; ++s) v += a[s * width];
+        return v;
+    }
+};
+template <int ARRAYS>
+__device__ __forceinline__ Columns column_sums(const GnGeom &g, float *sums) {
+    Columns c = {sums, g.bx * g.V, kThreads * g.V, 1};
+    while (c.segs * 2 * ARRAYS * c.width <= kThreads && c.segs * 4 <= g.by) c.segs *= 2;
+    __syncthreads();
+    const int runs = c.segs * c.width;   // of an array; consecutive threads take consecutive positions
+    if (g.by > 1)
+        for (int i = threadIdx.x; i < ARRAYS * runs; i += kThreads) {
+            int k = 0, j = i;
+#pragma unroll
+            for (int m = 1; m < ARRAYS; ++m)
+                if (j >= runs) {
+                    j -= runs;
+                    ++k;
+                }
+            float *a = sums + k * c.apart + j;   // row s, position pos of run s: this thread's own
+            const int stride = runs, rows = g.by * c.width - j;
+            float v = 0.f;
+#pragma unroll 8
+            for (int y = 0; y < rows; y += stride) v += a[y];
+            a[0] = v;
+        }
+    __syncthreads();
+    return c;
+}
+
+// ---- forward ----------------------------------------------------------------
+
+// Dynamic shared memory of the forward kernels.
+struct FwdShared {
+    float *nmean, *mul, *add;   // per position of the tile: a = (x + nmean) mul + add
+    float *sums;                // the threads' sums of x - k, of its square, and counts
+    float4 *pushed;             // [2][cluster][groups]: the cluster's (count, mean, M2), taking turns by strip
+    float2 *stat;               // (mean, rstd) of the groups
+    int groups;
+    __device__ __forceinline__ FwdShared(const GnGeom &g) {
+        extern __shared__ float4 dynamic[];
+        const int width = g.bx * g.V;
+        groups = groups_max(g);
+        nmean = (float *)dynamic;
+        mul = nmean + width;
+        add = mul + width;
+        sums = add + width;
+        pushed = (float4 *)(sums + kThreads * g.V * (g.wraps > 1 ? 3 : 2));
+        stat = (float2 *)(pushed + 2 * g.cluster * groups);
+    }
+};
+size_t forward_smem(const GnGeom &g) {
+    return (size_t)g.bx * g.V * 12 + (size_t)kThreads * g.V * (g.wraps > 1 ? 12 : 8) +
+           (size_t)groups_max(g) * (32 * g.cluster + 8);
+}
+
+// The shift of a thread's channels, the same in every thread of a column: the
+// mean of up to four rows of the chunk, or where no row of it is whole the
+// image's first pixel.
+template <typename T, bool PLAIN>
+__device__ __forceinline__ void shift(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                      float2 (&k)[kVec<T> / 2]) {
+    constexpr int V = kVec<T>, P = V / 2;
+    const T *x = (const T *)p.x;
+#pragma unroll
+    for (int j = 0; j < P; ++j) k[j] = both(0.f);
+    const int64_t step = (int64_t)V * g.LV * g.by, top = t.e - (int64_t)V * g.LV * t.ty;   // the column's first row
+    const int64_t whole = t.whole_rows + (t.col < t.rest ? 1 : 0) - t.r0;
+    const int rows = whole < t.rows ? (int)whole : t.rows;
+    const int skip = t.head != 0 && t.r0 == 0 && t.col == 0 ? 1 : 0;
+    int n = 0;
+    uint4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i >= skip && i * g.by < rows) {
+            const T *q = x + top + i * step;
+            w[i] = PLAIN || p.vec ? *reinterpret_cast<const uint4 *>(q) : gather(q);
+            ++n;
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i >= skip && i * g.by < rows) {
+            float2 v[P];
+            unpack(w[i], v, T());
+#pragma unroll
+            for (int j = 0; j < P; ++j) k[j] = add2(k[j], v[j]);
+        }
+    if (n > 0) {
+        const float inv = n == 1 ? 1.f : n == 2 ? 0.5f : n == 3 ? 1.f / 3.f : 0.25f;
+#pragma unroll
+        for (int j = 0; j < P; ++j) k[j] = mul2(k[j], both(inv));
+    } else if (!PLAIN) {
+        int c = shares.channel(t, V * t.col);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (g.E > 0) lane_of(k[i / 2], i) = to_f<T>(x[t.e0 + c]);
+            if (++c == g.C) c = 0;
+        }
+    }
+}
+
+// This block's statistics into the cluster's blocks 0 .. to-1.
+template <typename T, bool PLAIN>
+__device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                            const FwdShared &sh, float4 *pushed, int to, bool first) {
+    constexpr int V = kVec<T>, P = V / 2;
+    {
+        float2 nk[P], s[P], q[P];
+        float n[V];
+#pragma unroll
+        for (int j = 0; j < P; ++j) s[j] = q[j] = both(0.f);
+        const float whole = (float)(t.last - t.first);
+#pragma unroll
+        for (int k = 0; k < V; ++k) n[k] = whole;
+        const T *const x[1] = {(const T *)p.x};
+        auto pre = [&] {
+            shift<T, PLAIN>(g, p, shares, t, nk);
+            if (threadIdx.x < g.bx) put_own<V>(sh.nmean, nk);   // the block's shifts, for the merge
+#pragma unroll
+            for (int j = 0; j < P; ++j) nk[j] = neg2(nk[j]);
+        };
+        if (t.ty >= 0)
+            stream<T, PLAIN, false, 1, kForwardUnroll>(g, t, x, p.vec, pre, [&](int64_t, const float2 (&v)[1][P], uint32_t bits) {
+            if (bits == ~0u) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const float2 d = add2(v[0][j], nk[j]);
+                    s[j] = add2(s[j], d);
+                    q[j] = fma2(d, d, q[j]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if ((bits >> k) & 1u) {
+                        const float d = (k & 1 ? v[0][k / 2].y : v[0][k / 2].x) + lane_of(nk[k / 2], k);
+                        lane_of(s[k / 2], k) += d;
+                        lane_of(q[k / 2], k) += d * d;
+                        n[k] += 1.f;
+                    }
+            }
+        });
+        if (t.ty >= 0) {
+            put_own<V>(sh.sums, s);
+            put_own<V>(sh.sums + kThreads * V, q);
+            if (!PLAIN && g.wraps > 1) {
+                float2 c[P];
+#pragma unroll
+                for (int j = 0; j < P; ++j) c[j] = make_float2(n[2 * j], n[2 * j + 1]);
+                put_own<V>(sh.sums + 2 * kThreads * V, c);
+            }
+        }
+    }
+    const bool counted = !PLAIN && g.wraps > 1;   // counts differ by position
+    Columns cols;
+    if (counted) cols = column_sums<3>(g, sh.sums);
+    else cols = column_sums<2>(g, sh.sums);
+    // per group: its positions' means, then the distances from their mean
+    const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
+    const int rank = cluster_ctarank();
+    if (first) cluster_wait();
+    const float rows = (float)t.rows, by_rows = t.rows > 0 ? __fdividef(1.f, rows) : 0.f;
+    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
+        const int lg = gb + (threadIdx.x >> log);
+        const int c = wrap_group(g, t.first_group + lg) * g.Cg, many = lg < t.groups ? g.Cg : 0;
+        float sn = 0.f, sm = 0.f, sq = 0.f;
+        group_positions<PLAIN>(g, t, c, many, lane, lanes, [&](int pos) {
+            const float n = counted ? cols.at(2, pos) : rows;
+            sn += n;
+            sm += n * sh.nmean[pos] + cols.at(0, pos);
+        });
+        sn = group_sum(sn, lanes);
+        sm = group_sum(sm, lanes);
+        const float m = sn > 0.f ? __fdividef(sm, sn) : 0.f;
+        group_positions<PLAIN>(g, t, c, many, lane, lanes, [&](int pos) {
+            const float n = counted ? cols.at(2, pos) : rows;
+            const float inv = counted ? (n > 0.f ? __fdividef(1.f, n) : 0.f) : by_rows;
+            const float s = cols.at(0, pos), d = sh.nmean[pos] + s * inv - m;
+            sq += fmaxf(cols.at(1, pos) - s * s * inv, 0.f) + n * d * d;
+        });
+        sq = group_sum(sq, lanes);
+        if (lg < t.groups)
+            for (int i = lane; i < to; i += lanes)
+                push(pushed + rank * sh.groups + lg, i, make_float4(sn, m, sq, 0.f));
+    }
+}
+
+// The running join of (count, mean, M2) triples about a reference r, the mean
+// of one of them: sum n (m - r) and sum M2 + n (m - r)^2.  As r is the mean of
+// part of the values, the distance that the second carries is at most their M2
+// times the number of parts of that size.
+struct Joined {
+    float n, s, q, r;
+    __device__ __forceinline__ void add(float4 v) {
+        if (v.x > 0.f) {
+            const float d = v.y - r, w = v.x * d;
+            n += v.x;
+            s += w;
+            q += v.z + w * d;
+        }
+    }
+    __device__ __forceinline__ float4 triple() const {
+        const float m = n > 0.f ? s / n : 0.f;
+        return make_float4(n, r + m, fmaxf(q - s * m, 0.f), 0.f);
+    }
+};
+
+// The triples that the cluster's blocks pushed, joined: one thread per group.
+__device__ __forceinline__ float4 join_pushed(const FwdShared &sh, const float4 *pushed, int cluster, int lg) {
+    Joined j = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < cluster; ++i) {
+        const float4 v = pushed[i * sh.groups + lg];
+        if (j.n == 0.f) j.r = v.y;
+        j.add(v);
+    }
+    return j.triple();
+}
+
+// (mean, rstd) of a group from its joined sums, kept and written.
+__device__ __forceinline__ void put_stat(const GnGeom &g, const Params &p, const Share &t, const FwdShared &sh, int lg,
+                                         float4 v) {
+    const float rstd = 1.f / sqrtf(__fdividef(v.z, fmaxf(v.x, 1.f)) + p.eps);
+    sh.stat[lg] = make_float2(v.y, rstd);
+    if (blockIdx.x == 0) {   // tiles that share a group write the same
+        const int64_t at = t.n * g.G + wrap_group(g, t.first_group + lg);
+        if (p.mean) p.mean[at] = v.y;
+        if (p.rstd) p.rstd[at] = rstd;
+    }
+}
+
+// The parameters of the tile's positions, before their statistics are known.
+template <bool PLAIN>
+__device__ __forceinline__ void stage_params(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                             const FwdShared &sh) {
+    each_position(g, shares, t, [&](int pos, int c, int, int) {
+        sh.mul[pos] = param(p.weight, c, p.param_dtype, 1.f);
+        sh.add[pos] = param(p.bias, c, p.param_dtype, 0.f);
+    });
+}
+
+// y of this block's rows from sh.stat.
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                           const FwdShared &sh, const Philox &philox) {
+    constexpr int V = kVec<T>, P = V / 2;
+    __syncthreads();
+    each_position(g, shares, t, [&](int pos, int, int, int lg) {
+        const float2 s = sh.stat[lg];
+        sh.nmean[pos] = -s.x;
+        sh.mul[pos] *= s.y;
+    });
+    __syncthreads();
+    float2 nmean[P], mul[P], add[P];
+    own<V>(sh.nmean, t, nmean);
+    own<V>(sh.mul, t, mul);
+    own<V>(sh.add, t, add);
+    const T *const x[1] = {(const T *)p.x};
+    T *y = (T *)p.y;
+    const uint32_t limit = drop_limit(p.rng.threshold);
+    if (t.ty >= 0)
+        stream<T, PLAIN, true, 1, kForwardUnroll>(g, t, x, p.vec, [] {}, [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
+        uint32_t w[P];
+        if (DROP) draw(philox, (uint64_t)e, w);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            v[0][j] = act_value<ACT>(fma2(add2(v[0][j], nmean[j]), mul[j], add[j]));
+            if (DROP) v[0][j] = drop_pair(w[j], limit, p.rng.scale, v[0][j]);
+        }
+        if (PLAIN) store_vec(y + e, true, v[0]);
+        else if (bits == ~0u) store_vec(y + e, p.vec, v[0]);
+        else store_some(y + e, bits, v[0]);
+    });
+    __syncthreads();
+}
+
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const FwdShared sh(g);
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    int turn = 0;
+    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const Philox philox(p.rng);
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
+        turn ^= 1;
+        stage_params(g, p, shares, t, sh);
+        block_stats<T, PLAIN>(g, p, shares, t, sh, pushed, g.cluster, s == blockIdx.y);
+        cluster_sync();
+        for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
+            put_stat(g, p, t, sh, lg, join_pushed(sh, pushed, g.cluster, lg));
+        apply_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, sh, philox);
+    }
+}
+
+template <typename T, bool PLAIN>
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_stats_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const FwdShared sh(g);
+    griddep_launch_dependents();
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    int turn = 0;
+    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const int rank = cluster_ctarank();
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
+        turn ^= 1;
+        block_stats<T, PLAIN>(g, p, shares, t, sh, pushed, 1, s == blockIdx.y);
+        cluster_sync();
+        if (rank == 0) {
+            float4 *out = p.part + (t.strip * g.parts + blockIdx.x / g.cluster) * g.G;
+            for (int lg = threadIdx.x; lg < g.G; lg += kThreads)   // a count of 0 for groups of other tiles
+                out[wrap_group(g, t.first_group + lg)] =
+                    lg < t.groups ? join_pushed(sh, pushed, g.cluster, lg) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncthreads();
+    }
+    griddep_wait();
+}
+
+// f(group of the tile, triple) with an image's parts joined: a thread takes
+// every `slices`-th part of a group, neighbours neighbouring groups.
+template <typename F>
+__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const FwdShared &sh, const float4 *in,
+                                           int parts, F f) {
+    float *acc = sh.sums;   // three arrays of kThreads
+    const int log = log_lanes_for(t.groups);   // at most 32 slices
+    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
+        const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;   // groups of this round
+        const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;
+        Joined j = {0.f, 0.f, 0.f, 0.f};
+        if (slice < slices) {
+            const int gi = wrap_group(g, t.first_group + lg);
+            const float4 *q = in + gi;
+            // a part that surely has values: the first of the tile that the group's first channel is in
+            const int first = g.ctiles == 1 ? 0 : (gi * g.Cg + t.head) / (g.bx * g.V) * g.parts;
+            j.r = q[(int64_t)first * g.G].y;
+#pragma unroll 8
+            for (int i = slice; i < parts; i += slices) j.add(q[(int64_t)i * g.G]);
+            acc[threadIdx.x] = j.n;
+            acc[kThreads + threadIdx.x] = j.s;
+            acc[2 * kThreads + threadIdx.x] = j.q;
+        }
+        __syncthreads();
+        if (threadIdx.x < here) {
+            Joined a = j;
+            for (int i = 1; i < slices; ++i) {
+                a.n += acc[i * here + threadIdx.x];
+                a.s += acc[kThreads + i * here + threadIdx.x];
+                a.q += acc[2 * kThreads + i * here + threadIdx.x];
+            }
+            f(lg, a.triple());
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const FwdShared sh(g);
+    griddep_launch_dependents();
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    const Philox philox(p.rng);
+    const int parts = g.ctiles * g.parts;   // an image's strips and parts follow each other
+    bool waited = false;
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        stage_params(g, p, shares, t, sh);
+        if (!waited) griddep_wait();
+        waited = true;
+        join_parts(g, t, sh, p.part + t.n * parts * g.G, parts, [&](int lg, float4 v) { put_stat(g, p, t, sh, lg, v); });
+        apply_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, sh, philox);
+    }
+    if (!waited) griddep_wait();
+}
+
+// ---- backward ---------------------------------------------------------------
+
+// Dynamic shared memory of the backward kernels.
+struct BwdShared {
+    float *nmean, *mul, *add;   // per position of the tile: a = (x + nmean) mul + add
+    float *weight, *rstd;       // per position
+    float *sums;                // the threads' sums of da and of da (x - mean); row 0 the block's per position
+    float4 *pushed;             // [2][cluster][groups]: the cluster's (sum dh, sum dh h), taking turns by strip
+    float2 *stat;               // the groups' means of both
+    int groups;
+    __device__ __forceinline__ BwdShared(const GnGeom &g) {
+        extern __shared__ float4 dynamic[];
+        const int width = g.bx * g.V;
+        groups = groups_max(g);
+        nmean = (float *)dynamic;
+        mul = nmean + width;
+        add = mul + width;
+        weight = add + width;
+        rstd = weight + width;
+        sums = rstd + width;
+        pushed = (float4 *)(sums + kThreads * g.V * 2);
+        stat = (float2 *)(pushed + 2 * g.cluster * groups);
+    }
+};
+size_t backward_smem(const GnGeom &g) {
+    return (size_t)g.bx * g.V * 20 + (size_t)kThreads * g.V * 8 + (size_t)groups_max(g) * (32 * g.cluster + 8);
+}
+
+// The coefficients of the tile's positions, and this thread's.
+template <int V>
+struct Coef {
+    float2 nmean[V / 2], mul[V / 2], add[V / 2];
+    template <bool PLAIN>
+    __device__ __forceinline__ Coef(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                    const BwdShared &sh) {
+        const float *mean = p.mean + t.n * g.G, *rstd = p.rstd + t.n * g.G;
+        each_position(g, shares, t, [&](int pos, int c, int gi, int) {
+            const float w = param(p.weight, c, p.param_dtype, 1.f), r = rstd[gi];
+            sh.nmean[pos] = -mean[gi];
+            sh.mul[pos] = r * w;
+            sh.add[pos] = param(p.bias, c, p.param_dtype, 0.f);
+            sh.weight[pos] = w;
+            sh.rstd[pos] = r;
+        });
+        __syncthreads();
+        own<V>(sh.nmean, t, nmean);
+        own<V>(sh.mul, t, mul);
+        own<V>(sh.add, t, add);
+    }
+};
+
+// da of a pair; v becomes x - mean
+template <int ACT, bool DROP>
+__device__ __forceinline__ float2 grad_a(float2 &v, float2 d, float2 nmean, float2 mul, float2 add, uint32_t word,
+                                         uint32_t limit, float scale) {
+    v = add2(v, nmean);
+    if (DROP) d = drop_pair(word, limit, scale, d);
+    if (ACT == CT_ACT_IDENTITY) return d;
+    return mul2(d, act_slope<ACT>(fma2(v, mul, add)));
+}
+
+// This block's sums: per channel to p.chan, per group into the cluster's
+// blocks 0 .. to-1.
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, const Share &t, const Coef<kVec<T>> &f,
+                                           const BwdShared &sh, const Philox &philox, float4 *pushed, int to, bool first) {
+    constexpr int V = kVec<T>, P = V / 2;
+    {
+        const uint32_t limit = drop_limit(p.rng.threshold);
+        float2 u[P], w[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) u[j] = w[j] = both(0.f);
+        const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
+        if (t.ty >= 0)
+            stream<T, PLAIN, false, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+            uint32_t r[P];
+            if (DROP) draw(philox, (uint64_t)e, r);
+            if (bits != ~0u) {   // outside the image x is the mean and dy is 0: nothing is added
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    if (!((bits >> (2 * j)) & 1u)) v[0][j].x = -f.nmean[j].x;
+                    if (!((bits >> (2 * j + 1)) & 1u)) v[0][j].y = -f.nmean[j].y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float2 da = grad_a<ACT, DROP>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], DROP ? r[j] : 0,
+                                                    limit, p.rng.scale);
+                u[j] = add2(u[j], da);
+                w[j] = fma2(da, v[0][j], w[j]);
+            }
+        });
+        if (t.ty >= 0) {
+            put_own<V>(sh.sums, u);
+            put_own<V>(sh.sums + kThreads * V, w);
+        }
+    }
+    const Columns cols = column_sums<2>(g, sh.sums);
+    if (p.chan) {
+        float2 *out = p.chan + (t.strip * g.chunks + blockIdx.x) * g.C;
+        for (int c = threadIdx.x; c < g.C; c += kThreads) {   // 0 for other tiles' channels
+            float2 s = both(0.f);
+            group_positions<PLAIN>(g, t, c, 1, 0, 1, [&](int pos) {
+                s = add2(s, make_float2(cols.at(0, pos), cols.at(1, pos) * sh.rstd[pos]));
+            });
+            out[c] = s;
+        }
+    }
+    const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
+    const int rank = cluster_ctarank();
+    if (first) cluster_wait();
+    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
+        const int lg = gb + (threadIdx.x >> log);
+        float2 s = both(0.f);
+        group_positions<PLAIN>(g, t, wrap_group(g, t.first_group + lg) * g.Cg, lg < t.groups ? g.Cg : 0, lane, lanes,
+                               [&](int pos) {
+                                   const float w = sh.weight[pos];
+                                   s = add2(s, make_float2(w * cols.at(0, pos), w * sh.rstd[pos] * cols.at(1, pos)));
+                               });
+        s.x = group_sum(s.x, lanes);
+        s.y = group_sum(s.y, lanes);
+        if (lg < t.groups)
+            for (int i = lane; i < to; i += lanes) push(pushed + rank * sh.groups + lg, i, make_float4(s.x, s.y, 0.f, 0.f));
+    }
+}
+
+__device__ __forceinline__ float2 join_pushed(const BwdShared &sh, const float4 *pushed, int cluster, int lg) {
+    float2 s = both(0.f);
+    for (int i = 0; i < cluster; ++i) {
+        const float4 v = pushed[i * sh.groups + lg];
+        s = add2(s, make_float2(v.x, v.y));
+    }
+    return s;
+}
+
+// dx of this block's rows from sh.stat.
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
+                                          const Coef<kVec<T>> &f, const BwdShared &sh, const Philox &philox) {
+    constexpr int V = kVec<T>, P = V / 2;
+    __syncthreads();
+    float *m0 = sh.sums, *m1 = sh.sums + g.bx * V;   // per position: -rstd mean(dh), -rstd^2 mean(dh h)
+    each_position(g, shares, t, [&](int pos, int, int, int lg) {
+        const float2 s = sh.stat[lg];
+        const float r = sh.rstd[pos];
+        m0[pos] = -r * s.x;
+        m1[pos] = -r * r * s.y;
+    });
+    __syncthreads();
+    float2 a[P], b[P];
+    own<V>(m0, t, a);
+    own<V>(m1, t, b);
+    const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
+    T *dx = (T *)p.dx;
+    const uint32_t limit = drop_limit(p.rng.threshold);
+    if (t.ty >= 0)
+        stream<T, PLAIN, true, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+        uint32_t r[P];
+        if (DROP) draw(philox, (uint64_t)e, r);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            const float2 da = grad_a<ACT, DROP>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], DROP ? r[j] : 0, limit,
+                                                p.rng.scale);
+            v[0][j] = fma2(v[0][j], b[j], fma2(da, f.mul[j], a[j]));
+        }
+        if (PLAIN) store_vec(dx + e, true, v[0]);
+        else if (bits == ~0u) store_vec(dx + e, p.vec, v[0]);
+        else store_some(dx + e, bits, v[0]);
+    });
+    __syncthreads();
+}
+
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const BwdShared sh(g);
+    griddep_launch_dependents();
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    int turn = 0;
+    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const Philox philox(p.rng);
+    const float inv = (float)(1.0 / ((double)g.S * g.Cg));
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
+        turn ^= 1;
+        const Coef<kVec<T>> f(g, p, shares, t, sh);
+        block_sums<T, PLAIN, ACT, DROP>(g, p, t, f, sh, philox, pushed, g.cluster, s == blockIdx.y);
+        cluster_sync();
+        for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
+            sh.stat[lg] = mul2(join_pushed(sh, pushed, g.cluster, lg), both(inv));
+        if (p.dx) grad_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, f, sh, philox);
+        else __syncthreads();
+    }
+}
+
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_sums_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const BwdShared sh(g);
+    griddep_launch_dependents();
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    int turn = 0;
+    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const Philox philox(p.rng);
+    const int rank = cluster_ctarank();
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
+        turn ^= 1;
+        const Coef<kVec<T>> f(g, p, shares, t, sh);
+        block_sums<T, PLAIN, ACT, DROP>(g, p, t, f, sh, philox, pushed, 1, s == blockIdx.y);
+        cluster_sync();
+        if (rank == 0) {
+            float2 *out = p.sums + (t.strip * g.parts + blockIdx.x / g.cluster) * g.G;
+            for (int lg = threadIdx.x; lg < g.G; lg += kThreads)   // 0 for groups of other tiles
+                out[wrap_group(g, t.first_group + lg)] =
+                    lg < t.groups ? join_pushed(sh, pushed, g.cluster, lg) : both(0.f);
+        }
+        __syncthreads();
+    }
+    griddep_wait();
+}
+
+// f(group of the tile, sums) with an image's parts joined.
+template <typename F>
+__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const BwdShared &sh, const float2 *in,
+                                           int parts, F f) {
+    float2 *acc = (float2 *)sh.sums;
+    const int log = log_lanes_for(t.groups);
+    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
+        const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;
+        const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;
+        float2 s = both(0.f);
+        if (slice < slices) {
+            const float2 *q = in + wrap_group(g, t.first_group + lg);
+#pragma unroll 8
+            for (int i = slice; i < parts; i += slices) s = add2(s, q[(int64_t)i * g.G]);
+            acc[threadIdx.x] = s;
+        }
+        __syncthreads();
+        if (threadIdx.x < here) {
+            for (int i = 1; i < slices; ++i) s = add2(s, acc[i * here + threadIdx.x]);
+            f(lg, s);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, bool PLAIN, int ACT, bool DROP>
+__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    const BwdShared sh(g);
+    griddep_launch_dependents();
+    Shares<PLAIN> shares(g, p);
+    Share t;
+    const Philox philox(p.rng);
+    const int parts = g.ctiles * g.parts;   // an image's strips and parts follow each other
+    const float inv = (float)(1.0 / ((double)g.S * g.Cg));
+    bool waited = false;
+    for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
+        shares.get(s, t);
+        const Coef<kVec<T>> f(g, p, shares, t, sh);
+        if (!waited) griddep_wait();
+        waited = true;
+        join_parts(g, t, sh, p.sums + t.n * parts * g.G, parts,
+                   [&](int lg, float2 v) { sh.stat[lg] = mul2(v, both(inv)); });
+        grad_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, f, sh, philox);
+    }
+    if (!waited) griddep_wait();
+}
+
+// dw and db: the strips' parts joined, 16 channels to a block, its threads 64
+// rows of them.
+constexpr int kParamThreads = 1024, kParamChannels = 16;
+__global__ void __launch_bounds__(kParamThreads) gn_back_params_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+    __shared__ float2 sums[kParamThreads];
+    griddep_wait();
+    const int in = threadIdx.x % kParamChannels, row = threadIdx.x / kParamChannels;
+    const int64_t rows = g.N * g.ctiles * g.chunks;
+    for (int64_t c0 = (int64_t)blockIdx.x * kParamChannels; c0 < g.C; c0 += (int64_t)gridDim.x * kParamChannels) {
+        const int64_t c = c0 + in;
+        float2 s = both(0.f);
+        if (c < g.C) {
+#pragma unroll 8
+            for (int64_t r = row; r < rows; r += kParamThreads / kParamChannels) s = add2(s, p.chan[r * g.C + c]);
+        }
+        sums[threadIdx.x] = s;
+        __syncthreads();
+        if (threadIdx.x < 32 * kParamChannels) {   // one warp per channel, two rows to a lane
+            const int ch = threadIdx.x / 32, lane = threadIdx.x % 32;
+            s = add2(sums[lane * kParamChannels + ch], sums[(lane + 32) * kParamChannels + ch]);
+            s.x = group_sum(s.x, 32);
+            s.y = group_sum(s.y, 32);
+            if (lane == 0 && c0 + ch < g.C) {
+                if (p.dbias) put_param(p.dbias, c0 + ch, p.param_dtype, s.x);
+                if (p.dweight) put_param(p.dweight, c0 + ch, p.param_dtype, s.y);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- host -------------------------------------------------------------------
+
+template <int V>
+struct Int {
+    static constexpr int value = V;
+};
+
+// f(activation, dropout, plain) with each as a type.
+template <typename F>
+ct_status by_act(int act, bool drop, bool plain, F g) {
+    auto f = [&](auto a, auto d) { return plain ? g(a, d, Int<1>()) : g(a, d, Int<0>()); };
+    if (drop) {
+        if (act == CT_ACT_RELU) return f(Int<CT_ACT_RELU>(), Int<1>());
+        if (act == CT_ACT_SILU) return f(Int<CT_ACT_SILU>(), Int<1>());
+        if (act == CT_ACT_GELU) return f(Int<CT_ACT_GELU>(), Int<1>());
+        return f(Int<CT_ACT_IDENTITY>(), Int<1>());
+    }
+    if (act == CT_ACT_RELU) return f(Int<CT_ACT_RELU>(), Int<0>());
+    if (act == CT_ACT_SILU) return f(Int<CT_ACT_SILU>(), Int<0>());
+    if (act == CT_ACT_GELU) return f(Int<CT_ACT_GELU>(), Int<0>());
+    return f(Int<CT_ACT_IDENTITY>(), Int<0>());
+}
+
+Params params_of(const GnArgs &a) {
+    Params p = {};
+    p.x = a.x; p.dy = a.dy; p.weight = a.weight; p.bias = a.bias;
+    p.y = a.y; p.dx = a.dx; p.dweight = a.dweight; p.dbias = a.dbias;
+    p.mean = a.mean; p.rstd = a.rstd;
+    p.eps = a.eps;
+    p.param_dtype = a.param_dtype;
+    p.rng = a.rng;
+    p.vec = (((uintptr_t)a.x | (uintptr_t)a.dy | (uintptr_t)a.y | (uintptr_t)a.dx) & 15) == 0;
+    return p;
+}
+
+// Once per kernel and device: as much shared memory and as large a cluster as
+// any geometry asks for.
+template <typename K>
+bool allow(K kernel, std::atomic<int> *flags) {
+    const int dev = current_device();
+    if (dev < 0 || dev >= 64) return false;
+    if (flags[dev].load()) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    flags[dev].store(1);
+    return true;
+}
+
+// Launch with clusters along x; `follows`: it may start while the launch
+// before it, of the same call, still runs.
+template <typename K>
+ct_status launch(K kernel, const GnGeom &g, const Params &p, dim3 grid, int threads, int cluster, size_t smem,
+                 bool follows, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {};
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    if (follows) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    if (cudaLaunchKernelEx(&cfg, kernel, g, p) != cudaSuccess) {
+        cudaGetLastError();
+        return CT_ERR_DEVICE;
+    }
+    return CT_OK;
+}
+
+// The strips of the wave that starts at image n into p, and their grid for the
+// launch that sums or the one that applies.
+dim3 wave_grid(const GnGeom &g, int64_t n, bool apply, Params &p) {
+    p.strip0 = n * g.ctiles;
+    p.strips = (g.N - n < g.wave ? g.N - n : g.wave) * g.ctiles;
+    p.rpc = apply ? g.apply_rpc : g.rpc;
+    return dim3((unsigned)(apply ? g.apply_chunks : g.chunks), (unsigned)(p.strips < 65535 ? p.strips : 65535));
+}
+
+template <typename T>
+ct_status forward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
+    Params p = params_of(a);
+    p.part = (float4 *)a.ws;
+    const size_t smem = forward_smem(g);
+    return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
+        constexpr int kAct = decltype(act)::value;
+        constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
+        static std::atomic<int> ready[3][64];
+        ct_status s = CT_OK;
+        if (g.fused) {
+            auto fused = gn_fused_kernel<T, kPlain, kAct, kDrop>;
+            if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
+            const dim3 grid = wave_grid(g, 0, false, p);
+            return launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
+        }
+        auto apply = gn_apply_kernel<T, kPlain, kAct, kDrop>;
+        auto stats = gn_stats_kernel<T, kPlain>;
+        if (!allow(stats, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
+        for (int64_t n = 0; s == CT_OK && n < g.N; n += g.wave) {
+            const dim3 sum_grid = wave_grid(g, n, false, p);
+            s = launch(stats, g, p, sum_grid, kThreads, g.cluster, smem, n > 0, st);
+            const dim3 grid = wave_grid(g, n, true, p);
+            if (s == CT_OK) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
+        }
+        return s;
+    });
+}
+
+template <typename T>
+ct_status backward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
+    Params p = params_of(a);
+    p.sums = (float2 *)a.ws;
+    const bool params = a.dweight || a.dbias;
+    if (params) p.chan = p.sums + g.N * g.ctiles * g.parts * g.G;
+    const size_t smem = backward_smem(g);
+    return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
+        constexpr int kAct = decltype(act)::value;
+        constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
+        static std::atomic<int> ready[3][64];
+        ct_status s = CT_OK;
+        if (g.fused) {
+            auto fused = gn_back_fused_kernel<T, kPlain, kAct, kDrop>;
+            if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
+            const dim3 grid = wave_grid(g, 0, false, p);
+            if (g.N > 0) s = launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
+        } else {
+            auto sums = gn_back_sums_kernel<T, kPlain, kAct, kDrop>;
+            auto apply = gn_back_apply_kernel<T, kPlain, kAct, kDrop>;
+            if (!allow(sums, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
+            for (int64_t n = 0; s == CT_OK && n < g.N; n += g.wave) {
+                const dim3 sum_grid = wave_grid(g, n, false, p);
+                s = launch(sums, g, p, sum_grid, kThreads, g.cluster, smem, n > 0, st);
+                const dim3 grid = wave_grid(g, n, true, p);
+                if (s == CT_OK && a.dx) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
+            }
+        }
+        if (s == CT_OK && params) {
+            const int64_t blocks = ceil_div(g.C, kParamChannels);
+            s = launch(gn_back_params_kernel, g, p, dim3(blocks < 2048 ? (unsigned)blocks : 2048u), kParamThreads, 1, 0,
+                       g.N > 0, st);
+        }
+        return s;
+    });
+}
+
+}  // namespace
+}  // namespace ct

@@ -51,16 +51,27 @@ struct Philox {
     }
 };
 
-// Bit k: element k of the block is kept.
-__device__ __forceinline__ uint32_t keep_bits(uint4 r, uint32_t threshold) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        m |= (uint32_t)((w[j] & 0xFFFFu) >= threshold) << (2 * j);
-        m |= (uint32_t)((w[j] >> 16) >= threshold) << (2 * j + 1);
+// Dropout of pair j (elements 2j and 2j + 1) of a block.  A 16-bit value h is
+// at least t where h << 16, whatever lies below it, is above (t << 16) - 1;
+// t = 2^16 keeps nothing.  The launch has t >= 1.
+__device__ __forceinline__ float2 drop_pair(uint32_t word, uint32_t limit, float scale, float2 v) {
+    v = __fmul2_rn(v, make_float2(scale, scale));
+    return make_float2((word << 16) > limit ? v.x : 0.f, word > limit ? v.y : 0.f);
+}
+__device__ __forceinline__ uint32_t drop_limit(uint32_t threshold) { return (threshold << 16) - 1u; }
+
+// The words for the pairs of a vector of P pairs at element e (a multiple of
+// 2 P): a whole block of the generator, or one half of it.
+template <int P>
+__device__ __forceinline__ void draw(const Philox &philox, uint64_t e, uint32_t (&w)[P]) {
+    const uint4 r = philox(e >> 3);
+    if constexpr (P == 4) {
+        w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+    } else {
+        const bool high = (e >> 2) & 1;
+        w[0] = high ? r.z : r.x;
+        w[1] = high ? r.w : r.y;
     }
-    return m;
 }
 
 #endif

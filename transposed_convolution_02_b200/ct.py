@@ -12,7 +12,6 @@ Attribute names follow the ai.onnx.ConvTranspose README ("Attributes");
 weight [C_in, K.., O/groups], padding as (lo, hi) per spatial dim).
 """
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -465,52 +464,83 @@ def _check_cuda(x, *leaves):
     call that would drop a gradient silently is refused."""
     if not x.is_cuda:
         raise ValueError("X must be a CUDA tensor")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x,) + leaves):
+    if not torch.is_grad_enabled():
+        return
+    for t in (x,) + leaves:
+        if t is None or not t.requires_grad:
+            continue
         raise ValueError("an input requires a gradient, and this call records none: call it under "
                          "torch.no_grad() and use the _backward function")
 
 
-@contextlib.contextmanager
-def _other_place(device, stream):
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield
+def _elsewhere(call, x, stream):
+    """`call(raw stream)` where tensors are allocated and kernels launched for
+    X: on its device, on the given stream (the device's current one by
+    default)."""
+    dev = x.device
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream is on %s, X on %s" % (stream.device, dev))
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
-def _place(device, stream):
-    """Context in which tensors are allocated and kernels launched: X's device
-    and the given stream (the device's current one by default)."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream is on %s, X on %s" % (stream.device, device))
-    return _other_place(device, stream)
+def _run_on(call, x, stream):
+    index = x.get_device()
+    if stream is None and index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    return _elsewhere(call, x, stream)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-@functools.lru_cache(maxsize=1024)
-def _norm_desc(n, s, c, groups, dtype, param_dtype, activation, eps):
-    """A group norm's descriptor and its two workspace sizes: sizes only, no
-    device memory."""
-    d = ct_group_norm_desc(NORM_DTYPE[dtype], NORM_DTYPE[param_dtype], NORM_ACTIVATION[activation], 0,
-                           n, s, c, groups, eps)
-    f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    st = lib().ct_group_norm_workspace_bytes(ctypes.byref(d), ctypes.byref(f), ctypes.byref(b))
-    if st != CT_OK:
-        raise CtError(st, "ct_group_norm_workspace_bytes")
-    return d, f.value, b.value
+class _Norm:
+    """A group norm's descriptor and workspace sizes: sizes only, no memory."""
+
+    def __init__(self, shape, dtype, groups, param_dtype, activation, eps):
+        s = 1
+        for v in shape[1:-1]:
+            s *= v
+        self.shape, self.dtype = shape, dtype
+        self.stats = (shape[0], groups)
+        self.desc = ct_group_norm_desc(NORM_DTYPE[dtype], NORM_DTYPE[param_dtype],
+                                       NORM_ACTIVATION[activation], 0, shape[0], s, shape[-1], groups, eps)
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        st = lib().ct_group_norm_workspace_bytes(ctypes.byref(self.desc), ctypes.byref(f), ctypes.byref(b))
+        if st != CT_OK:
+            raise CtError(st, "ct_group_norm_workspace_bytes")
+        self.forward_bytes, self.backward_bytes = f.value, b.value
 
 
-def _norm_desc_of(x, groups, weight, bias, activation, eps):
-    n, c = x.shape[0], x.shape[-1]
-    s = 1
-    for v in x.shape[1:-1]:
-        s *= v
+_norm = functools.lru_cache(maxsize=1024)(_Norm)
+
+
+def _norm_of(x, groups, weight, bias, activation, eps):
+    """The checked arguments' _Norm (the checks by size and type are made once
+    per size and type)."""
     one = weight if weight is not None else bias
-    return _norm_desc(n, s, c, groups, x.dtype, torch.float32 if one is None else one.dtype, activation,
-                      float(eps))
+    pd = torch.float32 if one is None else one.dtype
+    try:
+        n = _NORMS[x.shape, x.dtype, groups, pd, activation, eps]
+    except (KeyError, TypeError):
+        check_norm(x, groups, weight, bias, activation)
+        n = _norm(x.shape, x.dtype, int(groups), pd, activation, float(eps))
+        if len(_NORMS) >= 1024:
+            _NORMS.clear()
+        _NORMS[x.shape, x.dtype, groups, pd, activation, eps] = n
+        return n
+    dev = x.device
+    for t in (weight, bias):
+        if t is not None and (t.dtype != pd or t.device != dev or t.dim() != 1 or t.numel() != n.shape[-1]):
+            check_norm(x, groups, weight, bias, activation)
+    return n
+
+
+_NORMS = {}
 
 
 def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="identity", p=0.0,
@@ -522,28 +552,33 @@ def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="
 
     Returns Y, or (Y, mean, rstd) with ``return_stats``: mean and rstd are
     float32 [N, groups], what group_norm_nhwc_backward takes."""
-    check_norm(x, groups, weight, bias, activation)
+    norm = _norm_of(x, groups, weight, bias, activation, eps)
     if p:
         check_random(p, seed, offset, rng, x.device)
     if out is not None:
         check_out(out, x, (x,))
     _check_cuda(x, weight, bias)
-    desc, ws_bytes, _ = _norm_desc_of(x, groups, weight, bias, activation, eps)
-    dev = x.device
-    with _place(dev, stream):
-        x = x.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        bias = None if bias is None else bias.contiguous()
-        y = torch.empty_like(x) if out is None else out
-        stats = torch.empty((2, desc.N, groups), dtype=torch.float32, device=dev) if return_stats else None
-        mean, rstd = stats.unbind(0) if return_stats else (None, None)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        st = lib().ct_group_norm(desc, x.data_ptr(), _addr(weight), _addr(bias), p, seed, offset,
-                                 _addr(rng), y.data_ptr(), _addr(mean), _addr(rstd), ws.data_ptr(),
-                                 torch.cuda.current_stream().cuda_stream)
-    if st != CT_OK:
-        raise CtError(st, "ct_group_norm")
-    return (y, mean, rstd) if return_stats else y
+
+    def call(raw):
+        xc = x.contiguous()
+        w = None if weight is None else weight.contiguous()
+        b = None if bias is None else bias.contiguous()
+        y = torch.empty_like(xc) if out is None else out
+        if return_stats:
+            n, g = norm.stats
+            mean, rstd = torch.empty_strided((2, n, g), (n * g, g, 1), dtype=torch.float32,
+                                             device=xc.device).unbind()
+        else:
+            mean = rstd = None
+        ws = (torch.empty(norm.forward_bytes, dtype=torch.uint8, device=xc.device) if norm.forward_bytes
+              else None)
+        st = lib().ct_group_norm(norm.desc, xc.data_ptr(), _addr(w), _addr(b), p, seed, offset,
+                                 _addr(rng), y.data_ptr(), _addr(mean), _addr(rstd), _addr(ws), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_group_norm")
+        return (y, mean, rstd) if return_stats else y
+
+    return _run_on(call, x, stream)
 
 
 def group_norm_nhwc_backward(dy, x, mean, rstd, groups, weight=None, bias=None, *, activation="identity",
@@ -552,32 +587,33 @@ def group_norm_nhwc_backward(dy, x, mean, rstd, groups, weight=None, bias=None, 
     mean and rstd, the weight and bias and the p, seed, offset and rng of the
     forward call.  None for dx without ``need_x_grad``, and for the gradient
     of a weight or bias that is None."""
-    check_norm(x, groups, weight, bias, activation)
+    norm = _norm_of(x, groups, weight, bias, activation, 0.0)
     check_like(dy, "dy", x)
     for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or tuple(t.shape) != (x.shape[0], groups) or t.device != x.device:
+        if t.dtype != torch.float32 or t.shape != norm.stats or t.device != x.device:
             raise ValueError("%s must be a float32 tensor of shape %s on %s"
-                             % (name, [x.shape[0], groups], x.device))
+                             % (name, list(norm.stats), x.device))
     if p:
         check_random(p, seed, offset, rng, x.device)
     _check_cuda(x, dy, weight, bias)
-    desc, _, ws_bytes = _norm_desc_of(x, groups, weight, bias, activation, 0.0)
-    dev = x.device
-    with _place(dev, stream):
-        x, dy, mean, rstd = x.contiguous(), dy.contiguous(), mean.contiguous(), rstd.contiguous()
-        weight = None if weight is None else weight.contiguous()
-        bias = None if bias is None else bias.contiguous()
-        dx = torch.empty_like(x) if need_x_grad else None
-        dweight = None if weight is None else torch.empty_like(weight)
-        dbias = None if bias is None else torch.empty_like(bias)
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-        st = lib().ct_group_norm_backward(desc, dy.data_ptr(), x.data_ptr(), mean.data_ptr(),
-                                          rstd.data_ptr(), _addr(weight), _addr(bias), p, seed, offset,
-                                          _addr(rng), _addr(dx), _addr(dweight), _addr(dbias),
-                                          ws.data_ptr(), torch.cuda.current_stream().cuda_stream)
-    if st != CT_OK:
-        raise CtError(st, "ct_group_norm_backward")
-    return dx, dweight, dbias
+
+    def call(raw):
+        xc, dyc, m, r = x.contiguous(), dy.contiguous(), mean.contiguous(), rstd.contiguous()
+        w = None if weight is None else weight.contiguous()
+        b = None if bias is None else bias.contiguous()
+        dx = torch.empty_like(xc) if need_x_grad else None
+        dweight = None if w is None else torch.empty_like(w)
+        dbias = None if b is None else torch.empty_like(b)
+        ws = (torch.empty(norm.backward_bytes, dtype=torch.uint8, device=xc.device)
+              if norm.backward_bytes else None)
+        st = lib().ct_group_norm_backward(norm.desc, dyc.data_ptr(), xc.data_ptr(), m.data_ptr(),
+                                          r.data_ptr(), _addr(w), _addr(b), p, seed, offset, _addr(rng),
+                                          _addr(dx), _addr(dweight), _addr(dbias), _addr(ws), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_group_norm_backward")
+        return dx, dweight, dbias
+
+    return _run_on(call, x, stream)
 
 
 def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream=None):
@@ -597,15 +633,18 @@ def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream
     if out is not None:
         check_out(out, x, (x, residual), in_place=True)
     _check_cuda(x, residual)
-    with _place(x.device, stream):
-        x = x.contiguous()
-        residual = None if residual is None else residual.contiguous()
-        y = torch.empty_like(x) if out is None else out
-        st = lib().ct_dropout(NORM_DTYPE[x.dtype], x.numel(), x.data_ptr(), _addr(residual), p, seed,
-                              offset, _addr(rng), y.data_ptr(), torch.cuda.current_stream().cuda_stream)
-    if st != CT_OK:
-        raise CtError(st, "ct_dropout")
-    return y
+
+    def call(raw):
+        xc = x.contiguous()
+        r = None if residual is None else residual.contiguous()
+        y = torch.empty_like(xc) if out is None else out
+        st = lib().ct_dropout(NORM_DTYPE[xc.dtype], xc.numel(), xc.data_ptr(), _addr(r), p, seed, offset,
+                              _addr(rng), y.data_ptr(), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_dropout")
+        return y
+
+    return _run_on(call, x, stream)
 
 
 def dropout_backward(dy, p, *, seed=0, offset=0, rng=None, out=None, stream=None):
