@@ -10,8 +10,7 @@
 // channels, for any C, and holds its channels' coefficients and sums in
 // registers.  Rows wider than a block's threads are cut into column tiles; a
 // tile of an image is a "strip", and every strip is cut into `chunks` runs of
-// `rpc` rows, one to a block.  The blocks of a cluster work on neighbouring
-// chunks of one strip.  Divisions by these sizes are multiplications by
+// `rpc` rows, one to a block.  Divisions by these sizes are multiplications by
 // host-made factors: a block's fixed work counts where images are small.
 #pragma once
 
@@ -23,36 +22,28 @@
 
 namespace ct {
 
-#ifndef CT_GN_WAVE
-#define CT_GN_WAVE (40ll << 20)
-#endif
 #ifndef CT_GN_FU
-#define CT_GN_FU 4
+#define CT_GN_FU 8
 #endif
 #ifndef CT_GN_BU
-#define CT_GN_BU 2
+#define CT_GN_BU 4
 #endif
 #ifndef CT_GN_MIN
-#define CT_GN_MIN 4
+#define CT_GN_MIN 2
 #endif
 #ifndef CT_GN_BMIN
-#define CT_GN_BMIN 3
+#define CT_GN_BMIN 2
 #endif
-#ifndef CT_GN_APPLY
-#define CT_GN_APPLY 1
-#endif
-#ifndef CT_GN_CL
-#define CT_GN_CL 4
-#endif
-#ifndef CT_GN_FCL
-#define CT_GN_FCL 8
+#ifndef CT_GN_CB
+#define CT_GN_CB (1 << 20)
 #endif
 constexpr int kThreads = 256;
 constexpr int kForwardBlocks = CT_GN_MIN, kBackwardBlocks = CT_GN_BMIN;   // per SM
-constexpr int kForwardUnroll = CT_GN_FU, kBackwardUnroll = CT_GN_BU;     // vectors in flight per thread and tensor
-constexpr int64_t kWaveBytes = CT_GN_WAVE;
-constexpr int kMaxColumns = 256;                                         // vectors across a column tile
-constexpr int kMaxPushed = 1024;                                         // group sums that a block takes from its cluster
+constexpr int kForwardUnroll = CT_GN_FU, kBackwardUnroll = CT_GN_BU;      // vectors in flight per thread and tensor
+constexpr int kMaxColumns = 256;           // vectors across a column tile
+constexpr int kMaxPushed = 1024;           // group sums that a block takes from its cluster
+constexpr int64_t kSmallBytes = 4 << 20;   // of a tensor (two for the backward) that any cluster may take
+constexpr int64_t kClusterBytes = CT_GN_CB;   // of an image per block of its cluster
 
 struct GnGeom {
     int64_t N, S, E;       // images, pixels per image, elements per image (S*C)
@@ -65,11 +56,7 @@ struct GnGeom {
     int32_t bx, by;        // a block's threads: columns x rows
     int32_t ctiles;        // column tiles per row
     int32_t rpc, chunks;   // rows per chunk; chunks per strip
-    int32_t apply_rpc, apply_chunks;   // the same of the launch that applies
-    int32_t cluster;       // blocks per cluster
-    int32_t parts;         // clusters per strip, the parts of its sums
-    bool fused;            // one cluster per strip: both passes in one launch
-    int64_t wave;          // images per wave
+    int32_t cluster;       // one launch, a cluster of that many blocks per strip; 0: two launches
     DivMagic by_bx, by_by, by_cg;   // divisors bx, by, Cg
 };
 
@@ -92,8 +79,9 @@ struct GnArgs {
     float *ws;
 };
 
-// `tensors`: how many tensors of x's size a wave's second pass reads (from L2).
+// `tensors`: how many tensors of x's size a pass reads: 1 forward, 2 backward.
 GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensors);
+int64_t gn_sums(const GnGeom &g);   // group sums in the workspace, before a backward's channel sums
 size_t gn_forward_ws(const GnGeom &g);
 size_t gn_backward_ws(const GnGeom &g);
 ct_status gn_forward(const GnGeom &g, const GnArgs &a, cudaStream_t st);

@@ -56,9 +56,7 @@ struct Params {      // kernel arguments besides the geometry
     int param_dtype;
     bool vec;
     RngArgs rng;
-    int64_t strip0;  // this launch's strips: strip0 .. strip0 + strips - 1
     int64_t strips;
-    int rpc;         // rows of a strip to a block
 };
 
 __device__ __forceinline__ float param(const void *p, int c, int dtype, float none) {
@@ -138,7 +136,7 @@ struct Share {
     int rest;
 };
 
-// A block's share of strip p.strip0 + `local`: its chunk is blockIdx.x.  PLAIN:
+// A block's share of a strip: its chunk is blockIdx.x.  PLAIN:
 // a pixel is a whole number of vectors, one column tile, aligned tensors; then
 // nothing is cut, a position is its channel and a row a pixel.
 template <bool PLAIN>
@@ -152,7 +150,7 @@ struct Shares {
         tx = threadIdx.x - ty * g.bx;
     }
     __device__ __forceinline__ void get(int64_t local, Share &t) {
-        t.strip = p.strip0 + local;
+        t.strip = local;
         if (PLAIN) {
             t.n = t.strip;
             t.e0 = t.n * g.E;
@@ -162,8 +160,8 @@ struct Shares {
             t.col = tx;
             t.ty = ty < g.by ? ty : -1;
             t.cut_head = t.cut_tail = -1;
-            t.r0 = (int64_t)blockIdx.x * p.rpc;
-            t.rows = g.S - t.r0 < p.rpc ? (int)(g.S - t.r0) : p.rpc;   // S may be 0, where g.rows is 1
+            t.r0 = (int64_t)blockIdx.x * g.rpc;
+            t.rows = g.S - t.r0 < g.rpc ? (int)(g.S - t.r0) : g.rpc;   // S may be 0, where g.rows is 1
             if (t.rows < 0) t.rows = 0;
             t.e = t.e0 + (t.r0 + ty) * g.C + tx * g.V;
             t.last = t.ty >= 0 && t.rows > ty ? divq(t.rows - ty + g.by - 1, g.by_by) : 0;
@@ -197,8 +195,8 @@ struct Shares {
             t.rest = 0;
             ++t.whole_rows;
         }
-        t.r0 = (int64_t)blockIdx.x * p.rpc;
-        t.rows = g.rows - t.r0 < p.rpc ? (int)(g.rows - t.r0) : p.rpc;
+        t.r0 = (int64_t)blockIdx.x * g.rpc;
+        t.rows = g.rows - t.r0 < g.rpc ? (int)(g.rows - t.r0) : g.rpc;
         if (t.rows < 0) t.rows = 0;
         t.e = t.e0 - t.head + g.V * ((t.r0 + ty) * g.LV + t.col);
         if (t.ty < 0) return;
@@ -478,10 +476,11 @@ __device__ __forceinline__ void shift(const GnGeom &g, const Params &p, const Sh
     }
 }
 
-// This block's statistics into the cluster's blocks 0 .. to-1.
-template <typename T, bool PLAIN>
+// This block's statistics: ready(), then emit(group of the tile, lane, lanes,
+// triple) for each group, its lanes together.
+template <typename T, bool PLAIN, typename Ready, typename Emit>
 __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                            const FwdShared &sh, float4 *pushed, int to, bool first) {
+                                            const FwdShared &sh, Ready ready, Emit emit) {
     constexpr int V = kVec<T>, P = V / 2;
     {
         float2 nk[P], s[P], q[P];
@@ -535,8 +534,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
     else cols = column_sums<2>(g, sh.sums);
     // per group: its positions' means, then the distances from their mean
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
-    const int rank = cluster_ctarank();
-    if (first) cluster_wait();
+    ready();
     const float rows = (float)t.rows, by_rows = t.rows > 0 ? __fdividef(1.f, rows) : 0.f;
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
         const int lg = gb + (threadIdx.x >> log);
@@ -557,9 +555,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
             sq += fmaxf(cols.at(1, pos) - s * s * inv, 0.f) + n * d * d;
         });
         sq = group_sum(sq, lanes);
-        if (lg < t.groups)
-            for (int i = lane; i < to; i += lanes)
-                push(pushed + rank * sh.groups + lg, i, make_float4(sn, m, sq, 0.f));
+        if (lg < t.groups) emit(lg, lane, lanes, make_float4(sn, m, sq, 0.f));
     }
 }
 
@@ -658,13 +654,21 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_fused_kernel(cons
     Share t;
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const int rank = cluster_ctarank();
     const Philox philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
         turn ^= 1;
         stage_params(g, p, shares, t, sh);
-        block_stats<T, PLAIN>(g, p, shares, t, sh, pushed, g.cluster, s == blockIdx.y);
+        block_stats<T, PLAIN>(
+            g, p, shares, t, sh,
+            [&] {
+                if (s == blockIdx.y) cluster_wait();
+            },
+            [&](int lg, int lane, int lanes, float4 v) {
+                for (int i = lane; i < g.cluster; i += lanes) push(pushed + rank * sh.groups + lg, i, v);
+            });
         cluster_sync();
         for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
             put_stat(g, p, t, sh, lg, join_pushed(sh, pushed, g.cluster, lg));
@@ -678,24 +682,18 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_stats_kernel(cons
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    int turn = 0;
-    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
-    const int rank = cluster_ctarank();
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
-        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
-        turn ^= 1;
-        block_stats<T, PLAIN>(g, p, shares, t, sh, pushed, 1, s == blockIdx.y);
-        cluster_sync();
-        if (rank == 0) {
-            float4 *out = p.part + (t.strip * g.parts + blockIdx.x / g.cluster) * g.G;
-            for (int lg = threadIdx.x; lg < g.G; lg += kThreads)   // a count of 0 for groups of other tiles
-                out[wrap_group(g, t.first_group + lg)] =
-                    lg < t.groups ? join_pushed(sh, pushed, g.cluster, lg) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        float4 *out = p.part + (t.strip * g.chunks + blockIdx.x) * g.G;
+        block_stats<T, PLAIN>(
+            g, p, shares, t, sh, [] {},
+            [&](int lg, int lane, int, float4 v) {
+                if (lane == 0) out[wrap_group(g, t.first_group + lg)] = v;
+            });
+        for (int lg = t.groups + threadIdx.x; lg < g.G; lg += kThreads)   // a count of 0 for groups of other tiles
+            out[wrap_group(g, t.first_group + lg)] = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
     }
-    griddep_wait();
 }
 
 // f(group of the tile, triple) with an image's parts joined: a thread takes
@@ -713,7 +711,7 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
             const int gi = wrap_group(g, t.first_group + lg);
             const float4 *q = in + gi;
             // a part that surely has values: the first of the tile that the group's first channel is in
-            const int first = g.ctiles == 1 ? 0 : (gi * g.Cg + t.head) / (g.bx * g.V) * g.parts;
+            const int first = g.ctiles == 1 ? 0 : (gi * g.Cg + t.head) / (g.bx * g.V) * g.chunks;
             j.r = q[(int64_t)first * g.G].y;
 #pragma unroll 8
             for (int i = slice; i < parts; i += slices) j.add(q[(int64_t)i * g.G]);
@@ -742,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_apply_kernel(cons
     Shares<PLAIN> shares(g, p);
     Share t;
     const Philox philox(p.rng);
-    const int parts = g.ctiles * g.parts;   // an image's strips and parts follow each other
+    const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
@@ -816,11 +814,11 @@ __device__ __forceinline__ float2 grad_a(float2 &v, float2 d, float2 nmean, floa
     return mul2(d, act_slope<ACT>(fma2(v, mul, add)));
 }
 
-// This block's sums: per channel to p.chan, per group into the cluster's
-// blocks 0 .. to-1.
-template <typename T, bool PLAIN, int ACT, bool DROP>
+// This block's sums: per channel to p.chan; ready(), then emit(group of the
+// tile, lane, lanes, sums) for each group, its lanes together.
+template <typename T, bool PLAIN, int ACT, bool DROP, typename Ready, typename Emit>
 __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, const Share &t, const Coef<kVec<T>> &f,
-                                           const BwdShared &sh, const Philox &philox, float4 *pushed, int to, bool first) {
+                                           const BwdShared &sh, const Philox &philox, Ready ready, Emit emit) {
     constexpr int V = kVec<T>, P = V / 2;
     {
         const uint32_t limit = drop_limit(p.rng.threshold);
@@ -864,8 +862,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         }
     }
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
-    const int rank = cluster_ctarank();
-    if (first) cluster_wait();
+    ready();
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
         const int lg = gb + (threadIdx.x >> log);
         float2 s = both(0.f);
@@ -876,8 +873,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
                                });
         s.x = group_sum(s.x, lanes);
         s.y = group_sum(s.y, lanes);
-        if (lg < t.groups)
-            for (int i = lane; i < to; i += lanes) push(pushed + rank * sh.groups + lg, i, make_float4(s.x, s.y, 0.f, 0.f));
+        if (lg < t.groups) emit(lg, lane, lanes, s);
     }
 }
 
@@ -935,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kerne
     Share t;
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
+    const int rank = cluster_ctarank();
     const Philox philox(p.rng);
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
@@ -942,7 +939,15 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kerne
         float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
         turn ^= 1;
         const Coef<kVec<T>> f(g, p, shares, t, sh);
-        block_sums<T, PLAIN, ACT, DROP>(g, p, t, f, sh, philox, pushed, g.cluster, s == blockIdx.y);
+        block_sums<T, PLAIN, ACT, DROP>(
+            g, p, t, f, sh, philox,
+            [&] {
+                if (s == blockIdx.y) cluster_wait();
+            },
+            [&](int lg, int lane, int lanes, float2 v) {
+                for (int i = lane; i < g.cluster; i += lanes)
+                    push(pushed + rank * sh.groups + lg, i, make_float4(v.x, v.y, 0.f, 0.f));
+            });
         cluster_sync();
         for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
             sh.stat[lg] = mul2(join_pushed(sh, pushed, g.cluster, lg), both(inv));
@@ -957,26 +962,20 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_sums_kernel
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    int turn = 0;
-    cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
     const Philox philox(p.rng);
-    const int rank = cluster_ctarank();
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
-        float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
-        turn ^= 1;
+        float2 *out = p.sums + (t.strip * g.chunks + blockIdx.x) * g.G;
         const Coef<kVec<T>> f(g, p, shares, t, sh);
-        block_sums<T, PLAIN, ACT, DROP>(g, p, t, f, sh, philox, pushed, 1, s == blockIdx.y);
-        cluster_sync();
-        if (rank == 0) {
-            float2 *out = p.sums + (t.strip * g.parts + blockIdx.x / g.cluster) * g.G;
-            for (int lg = threadIdx.x; lg < g.G; lg += kThreads)   // 0 for groups of other tiles
-                out[wrap_group(g, t.first_group + lg)] =
-                    lg < t.groups ? join_pushed(sh, pushed, g.cluster, lg) : both(0.f);
-        }
+        block_sums<T, PLAIN, ACT, DROP>(
+            g, p, t, f, sh, philox, [] {},
+            [&](int lg, int lane, int, float2 v) {
+                if (lane == 0) out[wrap_group(g, t.first_group + lg)] = v;
+            });
+        for (int lg = t.groups + threadIdx.x; lg < g.G; lg += kThreads)   // 0 for groups of other tiles
+            out[wrap_group(g, t.first_group + lg)] = both(0.f);
         __syncthreads();
     }
-    griddep_wait();
 }
 
 // f(group of the tile, sums) with an image's parts joined.
@@ -1011,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_apply_kerne
     Shares<PLAIN> shares(g, p);
     Share t;
     const Philox philox(p.rng);
-    const int parts = g.ctiles * g.parts;   // an image's strips and parts follow each other
+    const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
@@ -1080,7 +1079,7 @@ ct_status by_act(int act, bool drop, bool plain, F g) {
     return f(Int<CT_ACT_IDENTITY>(), Int<0>());
 }
 
-Params params_of(const GnArgs &a) {
+Params params_of(const GnGeom &g, const GnArgs &a) {
     Params p = {};
     p.x = a.x; p.dy = a.dy; p.weight = a.weight; p.bias = a.bias;
     p.y = a.y; p.dx = a.dx; p.dweight = a.dweight; p.dbias = a.dbias;
@@ -1088,6 +1087,7 @@ Params params_of(const GnArgs &a) {
     p.eps = a.eps;
     p.param_dtype = a.param_dtype;
     p.rng = a.rng;
+    p.strips = g.N * g.ctiles;
     p.vec = (((uintptr_t)a.x | (uintptr_t)a.dy | (uintptr_t)a.y | (uintptr_t)a.dx) & 15) == 0;
     return p;
 }
@@ -1139,71 +1139,59 @@ ct_status launch(K kernel, const GnGeom &g, const Params &p, dim3 grid, int thre
     return CT_OK;
 }
 
-// The strips of the wave that starts at image n into p, and their grid for the
-// launch that sums or the one that applies.
-dim3 wave_grid(const GnGeom &g, int64_t n, bool apply, Params &p) {
-    p.strip0 = n * g.ctiles;
-    p.strips = (g.N - n < g.wave ? g.N - n : g.wave) * g.ctiles;
-    p.rpc = apply ? g.apply_rpc : g.rpc;
-    return dim3((unsigned)(apply ? g.apply_chunks : g.chunks), (unsigned)(p.strips < 65535 ? p.strips : 65535));
+dim3 grid_of(const GnGeom &g) {
+    const int64_t strips = g.N * g.ctiles;
+    return dim3((unsigned)g.chunks, (unsigned)(strips < 65535 ? strips : 65535));
 }
 
 template <typename T>
 ct_status forward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
-    Params p = params_of(a);
+    Params p = params_of(g, a);
     p.part = (float4 *)a.ws;
+    const dim3 grid = grid_of(g);
     const size_t smem = forward_smem(g);
     return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
         constexpr int kAct = decltype(act)::value;
         constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
         static std::atomic<int> ready[3][64];
-        ct_status s = CT_OK;
-        if (g.fused) {
+        if (g.cluster > 0) {
             auto fused = gn_fused_kernel<T, kPlain, kAct, kDrop>;
             if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
-            const dim3 grid = wave_grid(g, 0, false, p);
             return launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
         }
-        auto apply = gn_apply_kernel<T, kPlain, kAct, kDrop>;
         auto stats = gn_stats_kernel<T, kPlain>;
+        auto apply = gn_apply_kernel<T, kPlain, kAct, kDrop>;
         if (!allow(stats, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
-        for (int64_t n = 0; s == CT_OK && n < g.N; n += g.wave) {
-            const dim3 sum_grid = wave_grid(g, n, false, p);
-            s = launch(stats, g, p, sum_grid, kThreads, g.cluster, smem, n > 0, st);
-            const dim3 grid = wave_grid(g, n, true, p);
-            if (s == CT_OK) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
-        }
-        return s;
+        const ct_status s = launch(stats, g, p, grid, kThreads, 1, smem, false, st);
+        return s == CT_OK ? launch(apply, g, p, grid, kThreads, 1, smem, true, st) : s;
     });
 }
 
 template <typename T>
 ct_status backward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
-    Params p = params_of(a);
-    p.sums = (float2 *)a.ws;
+    Params p = params_of(g, a);
     const bool params = a.dweight || a.dbias;
-    if (params) p.chan = p.sums + g.N * g.ctiles * g.parts * g.G;
+    p.sums = (float2 *)a.ws;
+    if (params) p.chan = p.sums + gn_sums(g);
+    const dim3 grid = grid_of(g);
     const size_t smem = backward_smem(g);
     return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
         constexpr int kAct = decltype(act)::value;
         constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
         static std::atomic<int> ready[3][64];
         ct_status s = CT_OK;
-        if (g.fused) {
+        if (g.N == 0) {
+            // nothing to sum: the parameters' gradients are 0
+        } else if (g.cluster > 0) {
             auto fused = gn_back_fused_kernel<T, kPlain, kAct, kDrop>;
             if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
-            const dim3 grid = wave_grid(g, 0, false, p);
-            if (g.N > 0) s = launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
+            s = launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
         } else {
             auto sums = gn_back_sums_kernel<T, kPlain, kAct, kDrop>;
             auto apply = gn_back_apply_kernel<T, kPlain, kAct, kDrop>;
             if (!allow(sums, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
-            for (int64_t n = 0; s == CT_OK && n < g.N; n += g.wave) {
-                const dim3 sum_grid = wave_grid(g, n, false, p);
-                s = launch(sums, g, p, sum_grid, kThreads, g.cluster, smem, n > 0, st);
-                const dim3 grid = wave_grid(g, n, true, p);
-                if (s == CT_OK && a.dx) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
-            }
+            s = launch(sums, g, p, grid, kThreads, 1, smem, false, st);
+            if (s == CT_OK && a.dx) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
         }
         if (s == CT_OK && params) {
             const int64_t blocks = ceil_div(g.C, kParamChannels);

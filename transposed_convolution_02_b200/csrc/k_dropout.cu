@@ -10,12 +10,22 @@ namespace ct {
 
 namespace {
 
+#ifndef CT_DROP_U
+#define CT_DROP_U 4
+#endif
+#ifndef CT_DROP_B
+#define CT_DROP_B 4
+#endif
+#ifndef CT_DROP_G
+#define CT_DROP_G (1 << 20)
+#endif
 constexpr int kThreads = 256;
+constexpr int kUnroll = CT_DROP_U;   // blocks of the generator that a thread has in flight
 
 // A thread takes eight elements, one block of the generator, at a time.
 template <typename T, bool RES>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *residual, T *y, int64_t n,
-                                                           RngArgs rng, bool vec) {
+__global__ void __launch_bounds__(kThreads, CT_DROP_B) dropout_kernel(const T *x, const T *residual, T *y, int64_t n,
+                                                                      const __grid_constant__ RngArgs rng, bool vec) {
     constexpr int V = kVec<T>, P = V / 2, Q = 8 / V;   // vectors of P pairs, Q to a block
     const Philox philox(rng);
     const uint32_t limit = drop_limit(rng.threshold);
@@ -29,22 +39,51 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *
     };
     const int64_t blocks = n / 8, stride = (int64_t)gridDim.x * kThreads;
     int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    for (; i < blocks; i += stride) {
-        float2 v[Q][P], r[Q][P] = {};
+    if (vec) {
+        for (; i < blocks; i += kUnroll * stride) {
+            uint4 a[kUnroll][Q], b[kUnroll][Q];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            load_vec(x + 8 * i + q * V, vec, v[q]);
-            if (RES) load_vec(residual + 8 * i + q * V, vec, r[q]);
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * stride < blocks)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        a[u][q] = *reinterpret_cast<const uint4 *>(x + 8 * (i + u * stride) + q * V);
+                        if (RES) b[u][q] = *reinterpret_cast<const uint4 *>(residual + 8 * (i + u * stride) + q * V);
+                    }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * stride < blocks) {
+                    const uint4 d = philox((uint64_t)(i + u * stride));
+                    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        float2 v[P], r[P] = {};
+                        unpack(a[u][q], v, T());
+                        if (RES) unpack(b[u][q], r, T());
+                        one(v, w + q * P, r);
+                        *reinterpret_cast<uint4 *>(y + 8 * (i + u * stride) + q * V) = pack(v, T());
+                    }
+                }
         }
-        const uint4 d = philox((uint64_t)i);
-        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+    } else {
+        for (; i < blocks; i += stride) {
+            const uint4 d = philox((uint64_t)i);
+            const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+            float2 v[Q][P], r[Q][P] = {};
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            one(v[q], w + q * P, r[q]);
-            store_vec(y + 8 * i + q * V, vec, v[q]);
+            for (int q = 0; q < Q; ++q) {
+                unpack(gather(x + 8 * i + q * V), v[q], T());
+                if (RES) unpack(gather(residual + 8 * i + q * V), r[q], T());
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                one(v[q], w + q * P, r[q]);
+                store_some(y + 8 * i + q * V, ~0u, v[q]);
+            }
         }
     }
-    if (i == blocks && (n & 7)) {   // the last elements
+    if ((n & 7) != 0 && blockIdx.x == 0 && threadIdx.x == 0) {   // the last elements
+        i = blocks;
         const uint4 d = philox((uint64_t)i);
         const uint32_t w[4] = {d.x, d.y, d.z, d.w};
         const uint32_t bits = (1u << (n & 7)) - 1u;
@@ -62,8 +101,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T *x, const T *
 template <typename T>
 ct_status run(const void *x, const void *residual, void *y, int64_t n, const RngArgs &rng, cudaStream_t st) {
     const bool vec = (((uintptr_t)x | (uintptr_t)residual | (uintptr_t)y) & 15) == 0;
-    const int64_t want = ceil_div(ceil_div(n, 8), kThreads);
-    const int grid = (int)(want < 148 * 8 ? want : 148 * 8);
+    const int64_t want = ceil_div(ceil_div(n, 8), (int64_t)kThreads * kUnroll);
+    const int grid = (int)(want < 1 ? 1 : want < CT_DROP_G ? want : CT_DROP_G);
     if (residual)
         dropout_kernel<T, true><<<grid, kThreads, 0, st>>>((const T *)x, (const T *)residual, (T *)y, n, rng, vec);
     else

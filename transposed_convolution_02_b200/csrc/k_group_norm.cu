@@ -31,56 +31,38 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
     g.by_by = make_magic((uint32_t)g.by);
     g.by_cg = make_magic((uint32_t)g.Cg);
 
-    // Fused: as many blocks to a cluster as fill the GPU, up to 16, each thread
-    // with a row or more.  Not where a group spans column tiles, where the
-    // images under work at a time would not stay in L2, or where the clusters
-    // would leave much of the GPU idle with long work to do.
+    // One launch: a cluster of up to 8 blocks per strip, where that fills half
+    // of the GPU or the tensor is small, and no group spans column tiles.
+    // (Clusters of 16 are placed so slowly that [16,32x32,512] bf16 took 33 us
+    // in place of 22.)
     const int64_t strips = N * g.ctiles;
+    const bool whole = g.ctiles == 1 || (g.wraps == 1 && g.bx * g.V % g.Cg == 0);
     int64_t cluster = 1;
-    while (cluster < CT_GN_FCL && cluster * 2 * strips <= slots && cluster * 2 * by <= g.rows &&
+    while (cluster < 8 && cluster * 2 * strips <= slots && cluster * 2 * by <= g.rows &&
            cluster * 2 * groups_max(g) <= kMaxPushed)
         cluster *= 2;
-    const int64_t at_once = strips < slots / cluster ? strips : slots / cluster;
-    const bool whole = g.ctiles == 1 || (g.wraps == 1 && g.bx * g.V % g.Cg == 0);
-    if (whole && at_once * image / g.ctiles <= kWaveBytes && g.rows < (int64_t(1) << 30) &&
-        (2 * cluster * strips >= slots || image * N <= (4 << 20))) {
-        g.fused = true;
-        g.wave = N;
+    if (whole && g.rows < (int64_t(1) << 30) && (N * image <= kSmallBytes || 2 * cluster * strips >= slots) &&
+        image <= cluster * kClusterBytes) {
         g.cluster = (int32_t)cluster;
-        g.rpc = (int32_t)ceil_div(g.rows, cluster);
         g.chunks = g.cluster;
-        g.parts = 1;
+        g.rpc = (int32_t)ceil_div(g.rows, cluster);
         return g;
     }
-    // Two launches: waves of equal size, and one round of resident blocks over
-    // a wave.
-    int64_t wave = image > 0 ? kWaveBytes / image : N;
-    if (wave < 1) wave = 1;
-    g.wave = N > 0 ? ceil_div(N, ceil_div(N, wave)) : 1;
-    int64_t chunks = g.wave * g.ctiles < slots ? slots / (g.wave * g.ctiles) : 1;
+    // Two launches, of one round of resident blocks.
+    int64_t chunks = strips < slots ? slots / (strips < 1 ? 1 : strips) : 1;
     const int64_t useful = ceil_div(g.rows, by * 2), least = ceil_div(g.rows, int64_t(1) << 30);
     if (chunks > useful) chunks = useful;
     if (chunks < least) chunks = least;
-    g.cluster = 1;
-    while (g.cluster < CT_GN_CL && g.cluster * 2 <= chunks && g.cluster * 2 * groups_max(g) <= kMaxPushed) g.cluster *= 2;
-    g.chunks = (int32_t)(chunks / g.cluster * g.cluster);
-    g.rpc = (int32_t)ceil_div(g.rows, (int64_t)g.chunks);
-    g.parts = g.chunks / g.cluster;
-    int64_t finer = chunks * CT_GN_APPLY;
-    if (finer > useful) finer = useful;
-    if (finer < chunks) finer = chunks;
-    g.apply_rpc = (int32_t)ceil_div(g.rows, finer);
-    g.apply_chunks = (int32_t)ceil_div(g.rows, (int64_t)g.apply_rpc);
+    g.rpc = (int32_t)ceil_div(g.rows, chunks);
+    g.chunks = (int32_t)ceil_div(g.rows, (int64_t)g.rpc);
     return g;
 }
 
-size_t gn_forward_ws(const GnGeom &g) {
-    return g.fused ? 0 : (size_t)(g.N * g.ctiles * g.parts * g.G) * sizeof(float4);
-}
+int64_t gn_sums(const GnGeom &g) { return g.cluster > 0 ? 0 : g.N * g.ctiles * g.chunks * g.G; }
 
-size_t gn_backward_ws(const GnGeom &g) {
-    return (size_t)(g.N * g.ctiles * ((int64_t)g.parts * g.G + (int64_t)g.chunks * g.C)) * sizeof(float2);
-}
+size_t gn_forward_ws(const GnGeom &g) { return (size_t)gn_sums(g) * 16; }
+
+size_t gn_backward_ws(const GnGeom &g) { return (size_t)(gn_sums(g) + g.N * g.ctiles * g.chunks * g.C) * 8; }
 
 ct_status gn_forward(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
     if (a.dtype == CT_F32) return gn_forward_f32(g, a, st);
