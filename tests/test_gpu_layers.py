@@ -156,6 +156,7 @@ def test_not_finite_stays_in_its_group():
         ok[0, :, 8:16] = 0
         ok[1, :, 16:] = 0
         assert bool(ok.isfinite().all())
+    assert math.isnan(float(rstd[0, 1])) and math.isnan(float(rstd[1, 2])) and int(rstd.isnan().sum()) == 2
     assert torch.equal(y[0, :, :8], clean[0, :, :8]) and torch.equal(y[1, :, :16], clean[1, :, :16])
 
 

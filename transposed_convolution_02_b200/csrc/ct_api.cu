@@ -235,6 +235,7 @@ ct_status resolve_rng(double p, uint64_t seed, uint64_t offset, const void *rng,
     out->seed = seed;
     out->offset = offset;
     out->dev = (const uint64_t *)rng;
+    set_keys(*out);
     out->threshold = (uint32_t)floor(p * 65536.0 + 0.5);
     out->scale = out->threshold < 65536 ? (float)(65536.0 / (65536.0 - out->threshold)) : 0.f;
     if (out->threshold == 0) out->dev = nullptr;   // nothing is drawn

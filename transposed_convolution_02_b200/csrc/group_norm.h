@@ -22,28 +22,15 @@
 
 namespace ct {
 
-#ifndef CT_GN_FU
-#define CT_GN_FU 8
-#endif
-#ifndef CT_GN_BU
-#define CT_GN_BU 4
-#endif
-#ifndef CT_GN_MIN
-#define CT_GN_MIN 2
-#endif
-#ifndef CT_GN_BMIN
-#define CT_GN_BMIN 2
-#endif
-#ifndef CT_GN_CB
-#define CT_GN_CB (1 << 20)
-#endif
 constexpr int kThreads = 256;
-constexpr int kForwardBlocks = CT_GN_MIN, kBackwardBlocks = CT_GN_BMIN;   // per SM
-constexpr int kForwardUnroll = CT_GN_FU, kBackwardUnroll = CT_GN_BU;      // vectors in flight per thread and tensor
+constexpr int kBlocksPerSm = 2;
+constexpr int kForwardUnroll = 8, kBackwardUnroll = 4;   // vectors in flight per thread and tensor
 constexpr int kMaxColumns = 256;           // vectors across a column tile
 constexpr int kMaxPushed = 1024;           // group sums that a block takes from its cluster
-constexpr int64_t kSmallBytes = 4 << 20;   // of a tensor (two for the backward) that any cluster may take
-constexpr int64_t kClusterBytes = CT_GN_CB;   // of an image per block of its cluster
+constexpr int kMaxSmem = 144 * 1024;       // of any geometry: 2048 positions, 2049 groups
+constexpr int64_t kSmallBytes = 4 << 20;   // of the tensors read, that a cluster per strip may always take
+constexpr int64_t kClusterBytes = 1 << 20; // of an image per block of its cluster
+constexpr int64_t kMaxRows = 1024;         // vectors that a thread sums one after the other
 
 struct GnGeom {
     int64_t N, S, E;       // images, pixels per image, elements per image (S*C)

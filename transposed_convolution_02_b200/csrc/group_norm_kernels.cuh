@@ -9,24 +9,41 @@
 //   dx = rstd (dh - mean(dh) - h mean(dh h))  (means over the group).
 //
 // Bound: HBM.  Forward must read x and write y, backward read x and dy and
-// write dx.  Both need a whole group's sums before the first output, so there
-// are two passes, and the second is to find its inputs in L2.
-//   Fused: one cluster works on a strip of an image, joins its blocks' sums
-// through distributed shared memory and goes on to the second pass in the same
-// launch.  For images small enough that those under work at a time fit in L2,
-// and enough of them to fill the GPU (or too little work for that to matter).
-//   Two launches else: images are taken in waves of at most kWaveBytes, each
-// summed (a cluster joins its blocks' sums and writes one part) and then
-// applied (the parts joined again by each block).  A launch starts while the
-// one before it ends (programmatic dependent launch) and waits for it only
-// where it needs its sums or ends itself.
+// write dx; both need a whole group's sums before the first output, so there
+// are two passes over the inputs.
+//   One launch: a cluster of blocks works on an image (a strip), joins its
+// blocks' sums through distributed shared memory and goes on to the second
+// pass.  For small tensors, where a launch counts, and where such clusters fill
+// the GPU.
+//   Two launches else: sums, with a part of them from every block in the
+// workspace, and apply, each block joining the parts of its groups.  The
+// second starts while the first one ends (programmatic dependent launch).
+// Inputs of up to about 90 MB are then found in L2.
+// Measured, [8, 128x128, 128] fp16 with SiLU, 33.5 MB in and out: 25.8 us,
+// where reading x alone takes 6.9 and copying it 12.3; of it 8.4 reading, 3.5
+// sums and joining them, 2 between the launches and the parts, 7.2 on average
+// and 10.3 at most writing.  [16, 16384, 256] fp32, 268 MB: 150 us, a read (41)
+// and a copy (87) being the least for tensors that L2 does not hold.
+// Tried and slower: images taken in waves that fit L2 (every wave paid the 10
+// us that do not stream; vocoder size 176 to 230 us), a ring of bulk copies
+// with a copying warp (its hand-overs cost more than the registers it saved),
+// clusters of 8 whole-SM blocks or of 16 (placed slowly), a second pass with
+// rows handed out by a counter (a barrier for each piece; 27.1 us) or in
+// reverse (no change), streaming stores (no change).
 //
-// Statistics: a thread sums x - k and (x - k)^2 of its few values per
-// channel, k being the first of them, then everything is merged as (count,
-// mean, M2) with M2 the sum of squared distances from the mean.  As k is one
-// of the n values summed, sum (x - k)^2 <= n M2, so the subtraction that
-// gives M2 loses at most a factor of the thread's n, however far the mean is
-// from 0.
+// A pass is a loop of whole 16-byte vectors, 8 of them (4 of each tensor
+// backward) in flight per thread at 512 threads an SM: with 4 and 768 or 1024
+// threads the same within 3% where HBM bounds, 10% slower where the fixed work
+// of a thread counts (its column's coefficients, sums and joins take about as
+// many instructions as 25 vectors).  Packed fp32 instructions (two lanes an
+// issue slot) carry the arithmetic.
+//
+// Statistics: every thread of a column sums x - k and (x - k)^2 with one k, the
+// mean of up to four rows of the chunk, so a block's sums are plain sums; they
+// are then joined as (count, mean, M2) with M2 the sum of squared distances
+// from the mean.  As k is the mean of m of the n values summed, m (k - mean)^2
+// <= M2, so sum (x - k)^2 <= (1 + n/m) M2, and the subtraction that gives M2
+// loses at most that factor however far the mean is from 0.
 #pragma once
 
 #include <string.h>
@@ -244,16 +261,14 @@ __device__ __forceinline__ void cluster_wait() {
 // whole ones with U in flight, then those that an end of the image cuts (the
 // elements outside `bits` read as 0); on unaligned tensors all one by one.
 // pre() runs before the first of them, while the first loads are in flight.
-// BACK: the whole ones from the last to the first, so that a second pass over
-// a chunk begins with what the first one left in L2.
-template <typename T, bool PLAIN, bool BACK, int N, int U, typename Pre, typename F>
+template <typename T, bool PLAIN, int N, int U, typename Pre, typename F>
 __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T *const (&src)[N], bool vec, Pre pre,
                                        F f) {
     constexpr int V = kVec<T>, P = V / 2;
-    const int64_t row = (int64_t)V * g.LV * g.by, step = BACK ? -row : row;
+    const int64_t step = (int64_t)V * g.LV * g.by;
     if (PLAIN || vec) {
         int left = t.last - (PLAIN ? 0 : t.first);
-        int64_t e = t.e + (BACK ? t.last - 1 : PLAIN ? 0 : t.first) * row;
+        int64_t e = t.e + (PLAIN ? 0 : t.first) * step;
         uint4 w[U][N];
         auto load = [&](int u) {
 #pragma unroll
@@ -285,7 +300,7 @@ __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T 
     }
 #pragma unroll 1
     for (int i = vec ? t.last : t.first; i < t.last + 2; ++i) {
-        const int64_t e = i < t.last ? t.e + i * row : i == t.last ? t.cut_head : t.cut_tail;
+        const int64_t e = i < t.last ? t.e + i * step : i == t.last ? t.cut_head : t.cut_tail;
         if (e < 0) continue;
         const uint32_t bits = i < t.last ? ~0u : cut_bits(g, t, e);
         float2 v[N][P];
@@ -294,6 +309,8 @@ __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T 
         f(e, v, bits);
     }
 }
+
+__device__ __forceinline__ float at_least_0(float v) { return v < 0.f ? 0.f : v; }   // NaN stays
 
 __device__ __forceinline__ float group_sum(float v, int lanes) {
 #pragma unroll
@@ -431,7 +448,7 @@ size_t forward_smem(const GnGeom &g) {
            (size_t)groups_max(g) * (32 * g.cluster + 8);
 }
 
-// The shift of a thread's channels, the same in every thread of a column: the
+// The shift k of a thread's channels, the same in every thread of a column: the
 // mean of up to four rows of the chunk, or where no row of it is whole the
 // image's first pixel.
 template <typename T, bool PLAIN>
@@ -498,7 +515,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
             for (int j = 0; j < P; ++j) nk[j] = neg2(nk[j]);
         };
         if (t.ty >= 0)
-            stream<T, PLAIN, false, 1, kForwardUnroll>(g, t, x, p.vec, pre, [&](int64_t, const float2 (&v)[1][P], uint32_t bits) {
+            stream<T, PLAIN, 1, kForwardUnroll>(g, t, x, p.vec, pre, [&](int64_t, const float2 (&v)[1][P], uint32_t bits) {
             if (bits == ~0u) {
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -552,7 +569,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
             const float n = counted ? cols.at(2, pos) : rows;
             const float inv = counted ? (n > 0.f ? __fdividef(1.f, n) : 0.f) : by_rows;
             const float s = cols.at(0, pos), d = sh.nmean[pos] + s * inv - m;
-            sq += fmaxf(cols.at(1, pos) - s * s * inv, 0.f) + n * d * d;
+            sq += at_least_0(cols.at(1, pos) - s * s * inv) + n * d * d;
         });
         sq = group_sum(sq, lanes);
         if (lg < t.groups) emit(lg, lane, lanes, make_float4(sn, m, sq, 0.f));
@@ -575,7 +592,7 @@ struct Joined {
     }
     __device__ __forceinline__ float4 triple() const {
         const float m = n > 0.f ? s / n : 0.f;
-        return make_float4(n, r + m, fmaxf(q - s * m, 0.f), 0.f);
+        return make_float4(n, r + m, at_least_0(q - s * m), 0.f);
     }
 };
 
@@ -615,7 +632,7 @@ __device__ __forceinline__ void stage_params(const GnGeom &g, const Params &p, c
 // y of this block's rows from sh.stat.
 template <typename T, bool PLAIN, int ACT, bool DROP>
 __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                           const FwdShared &sh, const Philox &philox) {
+                                           const FwdShared &sh, const Philox<false> &philox) {
     constexpr int V = kVec<T>, P = V / 2;
     __syncthreads();
     each_position(g, shares, t, [&](int pos, int, int, int lg) {
@@ -632,7 +649,7 @@ __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, con
     T *y = (T *)p.y;
     const uint32_t limit = drop_limit(p.rng.threshold);
     if (t.ty >= 0)
-        stream<T, PLAIN, true, 1, kForwardUnroll>(g, t, x, p.vec, [] {}, [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
+        stream<T, PLAIN, 1, kForwardUnroll>(g, t, x, p.vec, [] {}, [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
         uint32_t w[P];
         if (DROP) draw(philox, (uint64_t)e, w);
 #pragma unroll
@@ -648,14 +665,15 @@ __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, con
 }
 
 template <typename T, bool PLAIN, int ACT, bool DROP>
-__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const FwdShared sh(g);
     Shares<PLAIN> shares(g, p);
     Share t;
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
     const int rank = cluster_ctarank();
-    const Philox philox(p.rng);
+    const Philox<false> philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
@@ -677,7 +695,8 @@ __global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_fused_kernel(cons
 }
 
 template <typename T, bool PLAIN>
-__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_stats_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_stats_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const FwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
@@ -734,12 +753,13 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
 }
 
 template <typename T, bool PLAIN, int ACT, bool DROP>
-__global__ void __launch_bounds__(kThreads, kForwardBlocks) gn_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const FwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox philox(p.rng);
+    const Philox<false> philox(p.rng);
     const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
@@ -818,7 +838,7 @@ __device__ __forceinline__ float2 grad_a(float2 &v, float2 d, float2 nmean, floa
 // tile, lane, lanes, sums) for each group, its lanes together.
 template <typename T, bool PLAIN, int ACT, bool DROP, typename Ready, typename Emit>
 __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, const Share &t, const Coef<kVec<T>> &f,
-                                           const BwdShared &sh, const Philox &philox, Ready ready, Emit emit) {
+                                           const BwdShared &sh, const Philox<false> &philox, Ready ready, Emit emit) {
     constexpr int V = kVec<T>, P = V / 2;
     {
         const uint32_t limit = drop_limit(p.rng.threshold);
@@ -827,7 +847,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         for (int j = 0; j < P; ++j) u[j] = w[j] = both(0.f);
         const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
         if (t.ty >= 0)
-            stream<T, PLAIN, false, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+            stream<T, PLAIN, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
             uint32_t r[P];
             if (DROP) draw(philox, (uint64_t)e, r);
             if (bits != ~0u) {   // outside the image x is the mean and dy is 0: nothing is added
@@ -889,7 +909,7 @@ __device__ __forceinline__ float2 join_pushed(const BwdShared &sh, const float4 
 // dx of this block's rows from sh.stat.
 template <typename T, bool PLAIN, int ACT, bool DROP>
 __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                          const Coef<kVec<T>> &f, const BwdShared &sh, const Philox &philox) {
+                                          const Coef<kVec<T>> &f, const BwdShared &sh, const Philox<false> &philox) {
     constexpr int V = kVec<T>, P = V / 2;
     __syncthreads();
     float *m0 = sh.sums, *m1 = sh.sums + g.bx * V;   // per position: -rstd mean(dh), -rstd^2 mean(dh h)
@@ -907,7 +927,7 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
     T *dx = (T *)p.dx;
     const uint32_t limit = drop_limit(p.rng.threshold);
     if (t.ty >= 0)
-        stream<T, PLAIN, true, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+        stream<T, PLAIN, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
         uint32_t r[P];
         if (DROP) draw(philox, (uint64_t)e, r);
 #pragma unroll
@@ -924,7 +944,8 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
 }
 
 template <typename T, bool PLAIN, int ACT, bool DROP>
-__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_back_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
@@ -932,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kerne
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
     const int rank = cluster_ctarank();
-    const Philox philox(p.rng);
+    const Philox<false> philox(p.rng);
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
@@ -957,12 +978,13 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_fused_kerne
 }
 
 template <typename T, bool PLAIN, int ACT, bool DROP>
-__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_sums_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_back_sums_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox philox(p.rng);
+    const Philox<false> philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         float2 *out = p.sums + (t.strip * g.chunks + blockIdx.x) * g.G;
@@ -1004,12 +1026,13 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
 }
 
 template <typename T, bool PLAIN, int ACT, bool DROP>
-__global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    gn_back_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox philox(p.rng);
+    const Philox<false> philox(p.rng);
     const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     bool waited = false;
@@ -1028,7 +1051,8 @@ __global__ void __launch_bounds__(kThreads, kBackwardBlocks) gn_back_apply_kerne
 // dw and db: the strips' parts joined, 16 channels to a block, its threads 64
 // rows of them.
 constexpr int kParamThreads = 1024, kParamChannels = 16;
-__global__ void __launch_bounds__(kParamThreads) gn_back_params_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kParamThreads)
+    gn_back_params_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     __shared__ float2 sums[kParamThreads];
     griddep_wait();
     const int in = threadIdx.x % kParamChannels, row = threadIdx.x / kParamChannels;
@@ -1092,22 +1116,6 @@ Params params_of(const GnGeom &g, const GnArgs &a) {
     return p;
 }
 
-// Once per kernel and device: as much shared memory and as large a cluster as
-// any geometry asks for.
-template <typename K>
-bool allow(K kernel, std::atomic<int> *flags) {
-    const int dev = current_device();
-    if (dev < 0 || dev >= 64) return false;
-    if (flags[dev].load()) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    flags[dev].store(1);
-    return true;
-}
-
 // Launch with clusters along x; `follows`: it may start while the launch
 // before it, of the same call, still runs.
 template <typename K>
@@ -1156,12 +1164,12 @@ ct_status forward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
         static std::atomic<int> ready[3][64];
         if (g.cluster > 0) {
             auto fused = gn_fused_kernel<T, kPlain, kAct, kDrop>;
-            if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
+            if (!allow_smem(fused, ready[0], kMaxSmem)) return CT_ERR_DEVICE;
             return launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
         }
         auto stats = gn_stats_kernel<T, kPlain>;
         auto apply = gn_apply_kernel<T, kPlain, kAct, kDrop>;
-        if (!allow(stats, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
+        if (!allow_smem(stats, ready[1], kMaxSmem) || !allow_smem(apply, ready[2], kMaxSmem)) return CT_ERR_DEVICE;
         const ct_status s = launch(stats, g, p, grid, kThreads, 1, smem, false, st);
         return s == CT_OK ? launch(apply, g, p, grid, kThreads, 1, smem, true, st) : s;
     });
@@ -1184,12 +1192,12 @@ ct_status backward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
             // nothing to sum: the parameters' gradients are 0
         } else if (g.cluster > 0) {
             auto fused = gn_back_fused_kernel<T, kPlain, kAct, kDrop>;
-            if (!allow(fused, ready[0])) return CT_ERR_DEVICE;
+            if (!allow_smem(fused, ready[0], kMaxSmem)) return CT_ERR_DEVICE;
             s = launch(fused, g, p, grid, kThreads, g.cluster, smem, false, st);
         } else {
             auto sums = gn_back_sums_kernel<T, kPlain, kAct, kDrop>;
             auto apply = gn_back_apply_kernel<T, kPlain, kAct, kDrop>;
-            if (!allow(sums, ready[1]) || !allow(apply, ready[2])) return CT_ERR_DEVICE;
+            if (!allow_smem(sums, ready[1], kMaxSmem) || !allow_smem(apply, ready[2], kMaxSmem)) return CT_ERR_DEVICE;
             s = launch(sums, g, p, grid, kThreads, 1, smem, false, st);
             if (s == CT_OK && a.dx) s = launch(apply, g, p, grid, kThreads, 1, smem, true, st);
         }

@@ -1,4 +1,4 @@
-// The group norm's geometry: how images are cut into waves, strips and chunks.
+// The group norm's geometry: how images are cut into strips and chunks.
 #include "group_norm.h"
 
 namespace ct {
@@ -6,7 +6,7 @@ namespace ct {
 GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensors) {
     GnGeom g = {};
     const int size = dtype == CT_F32 ? 4 : 2;
-    const int64_t slots = 148 * (tensors == 1 ? kForwardBlocks : kBackwardBlocks);
+    const int64_t slots = 148 * kBlocksPerSm;   // resident blocks
     g.V = 16 / size;
     g.N = N; g.S = S; g.E = S * C;
     g.C = (int32_t)C; g.G = (int32_t)G; g.Cg = (int32_t)(C / G);
@@ -48,11 +48,13 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
         g.rpc = (int32_t)ceil_div(g.rows, cluster);
         return g;
     }
-    // Two launches, of one round of resident blocks.
+    // Two launches, of one round of resident blocks; more where a thread would
+    // sum too many rows one after the other, fewer where it had less than two.
     int64_t chunks = strips < slots ? slots / (strips < 1 ? 1 : strips) : 1;
-    const int64_t useful = ceil_div(g.rows, by * 2), least = ceil_div(g.rows, int64_t(1) << 30);
+    const int64_t useful = ceil_div(g.rows, by * 2), least = ceil_div(g.rows, by * kMaxRows);
     if (chunks > useful) chunks = useful;
     if (chunks < least) chunks = least;
+    if (chunks > int64_t(1) << 30) chunks = int64_t(1) << 30;
     g.rpc = (int32_t)ceil_div(g.rows, chunks);
     g.chunks = (int32_t)ceil_div(g.rows, (int64_t)g.rpc);
     return g;
