@@ -88,7 +88,10 @@ SHAPES = [
     ([2, 40, 515], 5), ([2, 33, 2056], 8), ([1, 5, 4099], 1), ([2, 3, 2050], 41),   # rows wider than a block
     ([1, 4099, 16], 2), ([1, 50000, 8], 4), ([1, 20011, 3], 3),                     # one long image
     ([2, 64, 64, 128], 32), ([16, 8, 8, 512], 32), ([1, 8, 8, 256], 32), ([3, 100, 1024], 16),
+    ([16, 35, 2], 2), ([5, 33, 3], 3), ([4, 13, 5], 1), ([3, 77, 1], 1), ([40, 9, 3], 1), ([3, 41, 6], 2),   # below a vector
     ([70, 4, 16], 4), ([2, 57, 91, 30], 5), ([1, 31, 2048], 2048), ([6, 300, 96], 96),
+    ([2, 40, 4096], 32), ([1, 3000, 4096], 16), ([2, 700, 4104], 27), ([2, 5, 8192], 8192),  # column tiles of whole groups
+    ([700, 33, 64], 8), ([70000, 1, 8], 2), ([5, 20000, 56], 7), ([1, 30001, 70], 14),       # many images, long ones
 ]
 
 

@@ -376,8 +376,7 @@ __device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t,
             f(c + j);
             continue;
         }
-        int pos = c + j + t.head;
-        if (pos >= g.C) pos -= g.C;
+        int pos = (c + j + t.head) % g.C;   // C may be below the head
         for (pos -= t.p0; pos < t.p1 - t.p0; pos += g.C)
             if (pos >= 0) f(pos);
     }
