@@ -284,7 +284,8 @@ typedef struct ct_group_norm_desc {
 } ct_group_norm_desc;
 
 /* Bytes of device workspace (256-byte aligned) of one forward and one
- * backward call.  Its contents need not be set before a call and mean
+ * backward call; 0 where small images need none, the workspace pointer may
+ * then be NULL.  Its contents need not be set before a call and mean
  * nothing after it; calls that may run at the same time need one each. */
 CT_API ct_status ct_group_norm_workspace_bytes(const ct_group_norm_desc *desc, size_t *forward_bytes,
                                                size_t *backward_bytes);

@@ -291,7 +291,7 @@ __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T 
             e += U * step;
             left -= U;
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)   // together: one by one as registers free took 254 us in place of 150
                 if (u < left) load(u);
         }
         if (PLAIN || (t.cut_head < 0 && t.cut_tail < 0)) return;
@@ -334,7 +334,7 @@ __device__ __forceinline__ void push(float4 *p, int rank, float4 v) {
                  : "memory");
 }
 
-// A computing thread's V values of a per-position array.
+// A thread's V values of a per-position array.
 template <int V>
 __device__ __forceinline__ void own(const float *at, const Share &t, float2 (&v)[V / 2]) {
     const float4 *q = reinterpret_cast<const float4 *>(at + (t.col * V - t.p0));
@@ -629,9 +629,9 @@ __device__ __forceinline__ void stage_params(const GnGeom &g, const Params &p, c
 }
 
 // y of this block's rows from sh.stat.
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                           const FwdShared &sh, const Philox<false> &philox) {
+                                           const FwdShared &sh, const Philox<DROP == 1> &philox) {
     constexpr int V = kVec<T>, P = V / 2;
     __syncthreads();
     each_position(g, shares, t, [&](int pos, int, int, int lg) {
@@ -647,14 +647,15 @@ __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, con
     const T *const x[1] = {(const T *)p.x};
     T *y = (T *)p.y;
     const uint32_t limit = drop_limit(p.rng.threshold);
+    constexpr bool on = DROP != 0;
     if (t.ty >= 0)
         stream<T, PLAIN, 1, kForwardUnroll>(g, t, x, p.vec, [] {}, [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
         uint32_t w[P];
-        if (DROP) draw(philox, (uint64_t)e, w);
+        if (on) draw(philox, (uint64_t)e, w);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
             v[0][j] = act_value<ACT>(fma2(add2(v[0][j], nmean[j]), mul[j], add[j]));
-            if (DROP) v[0][j] = drop_pair(w[j], limit, p.rng.scale, v[0][j]);
+            if (on) v[0][j] = drop_pair(w[j], limit, p.rng.scale, v[0][j]);
         }
         if (PLAIN) store_vec(y + e, true, v[0]);
         else if (bits == ~0u) store_vec(y + e, p.vec, v[0]);
@@ -663,7 +664,7 @@ __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, con
     __syncthreads();
 }
 
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     gn_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const FwdShared sh(g);
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
     const int rank = cluster_ctarank();
-    const Philox<false> philox(p.rng);
+    const Philox<DROP == 1> philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         float4 *pushed = sh.pushed + turn * g.cluster * sh.groups;
@@ -751,14 +752,14 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
     }
 }
 
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     gn_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const FwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox<false> philox(p.rng);
+    const Philox<DROP == 1> philox(p.rng);
     const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
@@ -824,31 +825,32 @@ struct Coef {
 };
 
 // da of a pair; v becomes x - mean
-template <int ACT, bool DROP>
-__device__ __forceinline__ float2 grad_a(float2 &v, float2 d, float2 nmean, float2 mul, float2 add, uint32_t word,
-                                         uint32_t limit, float scale) {
+template <int ACT>
+__device__ __forceinline__ float2 grad_a(float2 &v, float2 d, float2 nmean, float2 mul, float2 add, bool on,
+                                         uint32_t word, uint32_t limit, float scale) {
     v = add2(v, nmean);
-    if (DROP) d = drop_pair(word, limit, scale, d);
+    if (on) d = drop_pair(word, limit, scale, d);
     if (ACT == CT_ACT_IDENTITY) return d;
     return mul2(d, act_slope<ACT>(fma2(v, mul, add)));
 }
 
 // This block's sums: per channel to p.chan; ready(), then emit(group of the
 // tile, lane, lanes, sums) for each group, its lanes together.
-template <typename T, bool PLAIN, int ACT, bool DROP, typename Ready, typename Emit>
+template <typename T, bool PLAIN, int ACT, int DROP, typename Ready, typename Emit>
 __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, const Share &t, const Coef<kVec<T>> &f,
-                                           const BwdShared &sh, const Philox<false> &philox, Ready ready, Emit emit) {
+                                           const BwdShared &sh, const Philox<DROP == 1> &philox, Ready ready, Emit emit) {
     constexpr int V = kVec<T>, P = V / 2;
     {
         const uint32_t limit = drop_limit(p.rng.threshold);
+        constexpr bool on = DROP != 0;
         float2 u[P], w[P];
 #pragma unroll
         for (int j = 0; j < P; ++j) u[j] = w[j] = both(0.f);
         const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
         if (t.ty >= 0)
-            stream<T, PLAIN, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+            stream<T, PLAIN, 2, DROP ? kMaskedUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
             uint32_t r[P];
-            if (DROP) draw(philox, (uint64_t)e, r);
+            if (on) draw(philox, (uint64_t)e, r);
             if (bits != ~0u) {   // outside the image x is the mean and dy is 0: nothing is added
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
@@ -858,8 +860,8 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
             }
 #pragma unroll
             for (int j = 0; j < P; ++j) {
-                const float2 da = grad_a<ACT, DROP>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], DROP ? r[j] : 0,
-                                                    limit, p.rng.scale);
+                const float2 da = grad_a<ACT>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], on, on ? r[j] : 0,
+                                               limit, p.rng.scale);
                 u[j] = add2(u[j], da);
                 w[j] = fma2(da, v[0][j], w[j]);
             }
@@ -906,9 +908,9 @@ __device__ __forceinline__ float2 join_pushed(const BwdShared &sh, const float4 
 }
 
 // dx of this block's rows from sh.stat.
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                          const Coef<kVec<T>> &f, const BwdShared &sh, const Philox<false> &philox) {
+                                          const Coef<kVec<T>> &f, const BwdShared &sh, const Philox<DROP == 1> &philox) {
     constexpr int V = kVec<T>, P = V / 2;
     __syncthreads();
     float *m0 = sh.sums, *m1 = sh.sums + g.bx * V;   // per position: -rstd mean(dh), -rstd^2 mean(dh h)
@@ -925,14 +927,15 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
     const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
     T *dx = (T *)p.dx;
     const uint32_t limit = drop_limit(p.rng.threshold);
+    constexpr bool on = DROP != 0;
     if (t.ty >= 0)
-        stream<T, PLAIN, 2, kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+        stream<T, PLAIN, 2, DROP ? kMaskedUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
         uint32_t r[P];
-        if (DROP) draw(philox, (uint64_t)e, r);
+        if (on) draw(philox, (uint64_t)e, r);
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-            const float2 da = grad_a<ACT, DROP>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], DROP ? r[j] : 0, limit,
-                                                p.rng.scale);
+            const float2 da = grad_a<ACT>(v[0][j], v[1][j], f.nmean[j], f.mul[j], f.add[j], on, on ? r[j] : 0,
+                                               limit, p.rng.scale);
             v[0][j] = fma2(v[0][j], b[j], fma2(da, f.mul[j], a[j]));
         }
         if (PLAIN) store_vec(dx + e, true, v[0]);
@@ -942,7 +945,7 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
     __syncthreads();
 }
 
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     gn_back_fused_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     int turn = 0;
     cluster_arrive();   // every block of the cluster runs before any stores to it: its push waits
     const int rank = cluster_ctarank();
-    const Philox<false> philox(p.rng);
+    const Philox<DROP == 1> philox(p.rng);
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
@@ -976,14 +979,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
 }
 
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     gn_back_sums_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox<false> philox(p.rng);
+    const Philox<DROP == 1> philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         float2 *out = p.sums + (t.strip * g.chunks + blockIdx.x) * g.G;
@@ -1024,14 +1027,14 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
     }
 }
 
-template <typename T, bool PLAIN, int ACT, bool DROP>
+template <typename T, bool PLAIN, int ACT, int DROP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     gn_back_apply_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     const BwdShared sh(g);
     griddep_launch_dependents();
     Shares<PLAIN> shares(g, p);
     Share t;
-    const Philox<false> philox(p.rng);
+    const Philox<DROP == 1> philox(p.rng);
     const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     bool waited = false;
@@ -1086,20 +1089,20 @@ struct Int {
     static constexpr int value = V;
 };
 
-// f(activation, dropout, plain) with each as a type.
+// f(activation, dropout, plain) with each as a type; dropout: 0 none, 1 with a
+// seed given, 2 with one that may lie on the device.  (1 makes the training
+// case's two calls 54 us in place of 57; tensors that are not plain do with 2.)
 template <typename F>
-ct_status by_act(int act, bool drop, bool plain, F g) {
-    auto f = [&](auto a, auto d) { return plain ? g(a, d, Int<1>()) : g(a, d, Int<0>()); };
-    if (drop) {
-        if (act == CT_ACT_RELU) return f(Int<CT_ACT_RELU>(), Int<1>());
-        if (act == CT_ACT_SILU) return f(Int<CT_ACT_SILU>(), Int<1>());
-        if (act == CT_ACT_GELU) return f(Int<CT_ACT_GELU>(), Int<1>());
-        return f(Int<CT_ACT_IDENTITY>(), Int<1>());
-    }
-    if (act == CT_ACT_RELU) return f(Int<CT_ACT_RELU>(), Int<0>());
-    if (act == CT_ACT_SILU) return f(Int<CT_ACT_SILU>(), Int<0>());
-    if (act == CT_ACT_GELU) return f(Int<CT_ACT_GELU>(), Int<0>());
-    return f(Int<CT_ACT_IDENTITY>(), Int<0>());
+ct_status by_act(const GnArgs &a, bool plain, F f) {
+    auto by_drop = [&](auto act) {
+        if (!plain) return a.drop ? f(act, Int<2>(), Int<0>()) : f(act, Int<0>(), Int<0>());
+        if (!a.drop) return f(act, Int<0>(), Int<1>());
+        return a.rng.dev ? f(act, Int<2>(), Int<1>()) : f(act, Int<1>(), Int<1>());
+    };
+    if (a.act == CT_ACT_RELU) return by_drop(Int<CT_ACT_RELU>());
+    if (a.act == CT_ACT_SILU) return by_drop(Int<CT_ACT_SILU>());
+    if (a.act == CT_ACT_GELU) return by_drop(Int<CT_ACT_GELU>());
+    return by_drop(Int<CT_ACT_IDENTITY>());
 }
 
 Params params_of(const GnGeom &g, const GnArgs &a) {
@@ -1157,9 +1160,9 @@ ct_status forward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
     p.part = (float4 *)a.ws;
     const dim3 grid = grid_of(g);
     const size_t smem = forward_smem(g);
-    return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
-        constexpr int kAct = decltype(act)::value;
-        constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
+    return by_act(a, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
+        constexpr int kAct = decltype(act)::value, kDrop = decltype(drop)::value;
+        constexpr bool kPlain = decltype(plain)::value != 0;
         static std::atomic<int> ready[3][64];
         if (g.cluster > 0) {
             auto fused = gn_fused_kernel<T, kPlain, kAct, kDrop>;
@@ -1182,9 +1185,9 @@ ct_status backward_t(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
     if (params) p.chan = p.sums + gn_sums(g);
     const dim3 grid = grid_of(g);
     const size_t smem = backward_smem(g);
-    return by_act(a.act, a.drop, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
-        constexpr int kAct = decltype(act)::value;
-        constexpr bool kDrop = decltype(drop)::value != 0, kPlain = decltype(plain)::value != 0;
+    return by_act(a, p.vec && g.wraps == 1 && g.ctiles == 1, [&](auto act, auto drop, auto plain) {
+        constexpr int kAct = decltype(act)::value, kDrop = decltype(drop)::value;
+        constexpr bool kPlain = decltype(plain)::value != 0;
         static std::atomic<int> ready[3][64];
         ct_status s = CT_OK;
         if (g.N == 0) {
