@@ -24,10 +24,11 @@ namespace ct {
 
 constexpr int kThreads = 256;
 constexpr int kBlocksPerSm = 2;
-// vectors in flight per thread and tensor (backward with 6 and a mask to draw:
-// spills, 39 us in place of 34 at [16,32x32,512]; without one 4: 198 in place
-// of 186 at [16,112x112,512])
-constexpr int kForwardUnroll = 8, kBackwardUnroll = 6, kMaskedUnroll = 4;
+// Vectors in flight per thread and tensor.  Backward, plain kernels without a
+// mask take 6 (186 us in place of 198 at [16,112x112,512] fp16), the others 4
+// (with a mask 6 spill: 39 us in place of 34 at [16,32x32,512] bf16; general
+// kernels grow: 14.5 us in place of 11.8 at [2,13x17,65] fp32).
+constexpr int kForwardUnroll = 8, kBackwardUnroll = 6, kFewerUnroll = 4;
 constexpr int kMaxColumns = 256;           // vectors across a column tile
 constexpr int kMaxPushed = 1024;           // group sums that a block takes from its cluster
 constexpr int kMaxSmem = 144 * 1024;       // of any geometry: 2048 positions, 2049 groups

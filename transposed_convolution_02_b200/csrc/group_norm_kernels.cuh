@@ -19,10 +19,10 @@
 // workspace, and apply, each block joining the parts of its groups.  The
 // second starts while the first one ends (programmatic dependent launch).
 // Inputs of up to about 90 MB are then found in L2.
-// Measured, [8, 128x128, 128] fp16 with SiLU, 33.5 MB in and out: 25.8 us,
+// Measured, [8, 128x128, 128] fp16 with SiLU, 33.5 MB in and out: 25.6 us,
 // where reading x alone takes 6.9 and copying it 12.3; of it 8.4 reading, 3.5
 // sums and joining them, 2 between the launches and the parts, 7.2 on average
-// and 10.3 at most writing.  [16, 16384, 256] fp32, 268 MB: 150 us, a read (41)
+// and 10.3 at most writing.  [16, 16384, 256] fp32, 268 MB: 151 us, a read (41)
 // and a copy (87) being the least for tensors that L2 does not hold.
 // Tried and slower: images taken in waves that fit L2 (every wave paid the 10
 // us that do not stream; vocoder size 176 to 230 us), a ring of bulk copies
@@ -31,12 +31,13 @@
 // rows handed out by a counter (a barrier for each piece; 27.1 us) or in
 // reverse (no change), streaming stores (no change).
 //
-// A pass is a loop of whole 16-byte vectors, 8 of them (4 of each tensor
-// backward) in flight per thread at 512 threads an SM: with 4 and 768 or 1024
-// threads the same within 3% where HBM bounds, 10% slower where the fixed work
-// of a thread counts (its column's coefficients, sums and joins take about as
-// many instructions as 25 vectors).  Packed fp32 instructions (two lanes an
-// issue slot) carry the arithmetic.
+// A pass is a loop of whole 16-byte vectors, several of them in flight per
+// thread at 512 threads an SM; 768 and 1024 threads with fewer in flight each
+// read as fast, but the fixed work of a thread (its column's coefficients, sums
+// and joins: as many instructions as about 25 vectors) then weighs more (decoder
+// size 27.3 us).  Packed fp32 instructions (two lanes an issue slot) carry the
+// arithmetic; SiLU's exponential and reciprocal take the special-function pipe
+// to half of its rate.
 //
 // Statistics: every thread of a column sums x - k and (x - k)^2 with one k, the
 // mean of up to four rows of the chunk, so a block's sums are plain sums; they
@@ -848,7 +849,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         for (int j = 0; j < P; ++j) u[j] = w[j] = both(0.f);
         const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
         if (t.ty >= 0)
-            stream<T, PLAIN, 2, DROP ? kMaskedUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+            stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
             uint32_t r[P];
             if (on) draw(philox, (uint64_t)e, r);
             if (bits != ~0u) {   // outside the image x is the mean and dy is 0: nothing is added
@@ -929,7 +930,7 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
     const uint32_t limit = drop_limit(p.rng.threshold);
     constexpr bool on = DROP != 0;
     if (t.ty >= 0)
-        stream<T, PLAIN, 2, DROP ? kMaskedUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+        stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
         uint32_t r[P];
         if (on) draw(philox, (uint64_t)e, r);
 #pragma unroll
