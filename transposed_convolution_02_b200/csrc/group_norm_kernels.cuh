@@ -325,6 +325,10 @@ __device__ __forceinline__ int log_lanes_for(int n) {
     return n >= kThreads ? 0 : min(5, 31 - __clz(kThreads / n));
 }
 
+// log2 of the warps that share one of `n` groups: a block's eight among fewer
+// than eight groups.
+__device__ __forceinline__ int log_warps_for(int n) { return n == 1 ? 3 : n == 2 ? 2 : n <= 4 ? 1 : 0; }
+
 __device__ __forceinline__ int wrap_group(const GnGeom &g, int gi) { return gi >= g.G ? gi - g.G : gi; }
 
 // Store to shared address `p` of the cluster's block `rank`.
@@ -377,7 +381,8 @@ __device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t,
             f(c + j);
             continue;
         }
-        int pos = (c + j + t.head) % g.C;   // C may be below the head
+        int pos = c + j + t.head;
+        while (pos >= g.C) pos -= g.C;   // more than once where C is below the head
         for (pos -= t.p0; pos < t.p1 - t.p0; pos += g.C)
             if (pos >= 0) f(pos);
     }
@@ -493,6 +498,26 @@ __device__ __forceinline__ void shift(const GnGeom &g, const Params &p, const Sh
     }
 }
 
+// The running join of (count, mean, M2) triples about a reference r, the mean
+// of one of them: sum n (m - r) and sum M2 + n (m - r)^2.  As r is the mean of
+// part of the values, the distance that the second carries is at most their M2
+// times the number of parts of that size.
+struct Joined {
+    float n, s, q, r;
+    __device__ __forceinline__ void add(float4 v) {
+        if (v.x > 0.f) {
+            const float d = v.y - r, w = v.x * d;
+            n += v.x;
+            s += w;
+            q += v.z + w * d;
+        }
+    }
+    __device__ __forceinline__ float4 triple() const {
+        const float m = n > 0.f ? s / n : 0.f;
+        return make_float4(n, r + m, at_least_0(q - s * m), 0.f);
+    }
+};
+
 // This block's statistics: ready(), then emit(group of the tile, lane, lanes,
 // triple) for each group, its lanes together.
 template <typename T, bool PLAIN, typename Ready, typename Emit>
@@ -551,13 +576,15 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
     else cols = column_sums<2>(g, sh.sums);
     // per group: its positions' means, then the distances from their mean
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
+    const int logw = log_warps_for(t.groups), warps = 1 << logw;
+    __shared__ float4 shares_of_warps[kThreads / 32];
     ready();
     const float rows = (float)t.rows, by_rows = t.rows > 0 ? __fdividef(1.f, rows) : 0.f;
-    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
-        const int lg = gb + (threadIdx.x >> log);
+    for (int gb = 0; gb < t.groups; gb += kThreads >> (log + logw)) {
+        const int lg = gb + (threadIdx.x >> (log + logw)), at = threadIdx.x & ((lanes << logw) - 1);
         const int c = wrap_group(g, t.first_group + lg) * g.Cg, many = lg < t.groups ? g.Cg : 0;
         float sn = 0.f, sm = 0.f, sq = 0.f;
-        group_positions<PLAIN>(g, t, c, many, lane, lanes, [&](int pos) {
+        group_positions<PLAIN>(g, t, c, many, at, lanes << logw, [&](int pos) {
             const float n = counted ? cols.at(2, pos) : rows;
             sn += n;
             sm += n * sh.nmean[pos] + cols.at(0, pos);
@@ -565,36 +592,29 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
         sn = group_sum(sn, lanes);
         sm = group_sum(sm, lanes);
         const float m = sn > 0.f ? __fdividef(sm, sn) : 0.f;
-        group_positions<PLAIN>(g, t, c, many, lane, lanes, [&](int pos) {
+        group_positions<PLAIN>(g, t, c, many, at, lanes << logw, [&](int pos) {
             const float n = counted ? cols.at(2, pos) : rows;
             const float inv = counted ? (n > 0.f ? __fdividef(1.f, n) : 0.f) : by_rows;
             const float s = cols.at(0, pos), d = sh.nmean[pos] + s * inv - m;
             sq += at_least_0(cols.at(1, pos) - s * s * inv) + n * d * d;
         });
         sq = group_sum(sq, lanes);
-        if (lg < t.groups) emit(lg, lane, lanes, make_float4(sn, m, sq, 0.f));
+        float4 v = make_float4(sn, m, sq, 0.f);
+        if (logw > 0) {   // one round: the warps' triples joined
+            if (lane == 0) shares_of_warps[threadIdx.x / 32] = v;
+            __syncthreads();
+            Joined all = {0.f, 0.f, 0.f, 0.f};
+            if (at < 32)
+                for (int i = 0; i < warps; ++i) {
+                    v = shares_of_warps[threadIdx.x / 32 + i];
+                    if (all.n == 0.f) all.r = v.y;
+                    all.add(v);
+                }
+            v = all.triple();
+        }
+        if (lg < t.groups && at < lanes) emit(lg, lane, lanes, v);
     }
 }
-
-// The running join of (count, mean, M2) triples about a reference r, the mean
-// of one of them: sum n (m - r) and sum M2 + n (m - r)^2.  As r is the mean of
-// part of the values, the distance that the second carries is at most their M2
-// times the number of parts of that size.
-struct Joined {
-    float n, s, q, r;
-    __device__ __forceinline__ void add(float4 v) {
-        if (v.x > 0.f) {
-            const float d = v.y - r, w = v.x * d;
-            n += v.x;
-            s += w;
-            q += v.z + w * d;
-        }
-    }
-    __device__ __forceinline__ float4 triple() const {
-        const float m = n > 0.f ? s / n : 0.f;
-        return make_float4(n, r + m, at_least_0(q - s * m), 0.f);
-    }
-};
 
 // The triples that the cluster's blocks pushed, joined: one thread per group.
 __device__ __forceinline__ float4 join_pushed(const FwdShared &sh, const float4 *pushed, int cluster, int lg) {
@@ -884,18 +904,26 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         }
     }
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
+    const int logw = log_warps_for(t.groups), warps = 1 << logw;
+    __shared__ float2 shares_of_warps[kThreads / 32];
     ready();
-    for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
-        const int lg = gb + (threadIdx.x >> log);
+    for (int gb = 0; gb < t.groups; gb += kThreads >> (log + logw)) {
+        const int lg = gb + (threadIdx.x >> (log + logw)), at = threadIdx.x & ((lanes << logw) - 1);
         float2 s = both(0.f);
-        group_positions<PLAIN>(g, t, wrap_group(g, t.first_group + lg) * g.Cg, lg < t.groups ? g.Cg : 0, lane, lanes,
+        group_positions<PLAIN>(g, t, wrap_group(g, t.first_group + lg) * g.Cg, lg < t.groups ? g.Cg : 0, at, lanes << logw,
                                [&](int pos) {
                                    const float w = sh.weight[pos];
                                    s = add2(s, make_float2(w * cols.at(0, pos), w * sh.rstd[pos] * cols.at(1, pos)));
                                });
         s.x = group_sum(s.x, lanes);
         s.y = group_sum(s.y, lanes);
-        if (lg < t.groups) emit(lg, lane, lanes, s);
+        if (logw > 0) {   // one round: the warps' sums joined
+            if (lane == 0) shares_of_warps[threadIdx.x / 32] = s;
+            __syncthreads();
+            if (at < 32)
+                for (int i = 1; i < warps; ++i) s = add2(s, shares_of_warps[threadIdx.x / 32 + i]);
+        }
+        if (lg < t.groups && at < lanes) emit(lg, lane, lanes, s);
     }
 }
 
