@@ -326,7 +326,11 @@ __device__ __forceinline__ int log_lanes_for(int n) {
 }
 
 // log2 of the warps that share one of `n` groups: a block's eight among fewer
-// than eight groups.
+// than eight groups.  The general kernels only ([8, 16383, 127] fp16 in one
+// group 32.4 us in place of 36.5): the plain ones have short sums, and sharing
+// costs them 2% at every size (backward [16, 112x112, 512] fp16 190 us in place
+// of 186, decoder size 26.1 in place of 25.5), more than their one kind of
+// shape that gains is worth ([8, 256, 2048] bf16 in one group 18.5 in place of 24).
 __device__ __forceinline__ int log_warps_for(int n) { return n == 1 ? 3 : n == 2 ? 2 : n <= 4 ? 1 : 0; }
 
 __device__ __forceinline__ int wrap_group(const GnGeom &g, int gi) { return gi >= g.G ? gi - g.G : gi; }
@@ -576,7 +580,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
     else cols = column_sums<2>(g, sh.sums);
     // per group: its positions' means, then the distances from their mean
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
-    const int logw = log_warps_for(t.groups), warps = 1 << logw;
+    const int logw = PLAIN ? 0 : log_warps_for(t.groups), warps = 1 << logw;
     __shared__ float4 shares_of_warps[kThreads / 32];
     ready();
     const float rows = (float)t.rows, by_rows = t.rows > 0 ? __fdividef(1.f, rows) : 0.f;
@@ -600,7 +604,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
         });
         sq = group_sum(sq, lanes);
         float4 v = make_float4(sn, m, sq, 0.f);
-        if (logw > 0) {   // one round: the warps' triples joined
+        if (logw > 0) {   // one step: the warps' triples joined
             if (lane == 0) shares_of_warps[threadIdx.x / 32] = v;
             __syncthreads();
             Joined all = {0.f, 0.f, 0.f, 0.f};
@@ -744,7 +748,7 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
     float *acc = sh.sums;   // three arrays of kThreads
     const int log = log_lanes_for(t.groups);   // at most 32 slices
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
-        const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;   // groups of this round
+        const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;   // groups of this step
         const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;
         Joined j = {0.f, 0.f, 0.f, 0.f};
         if (slice < slices) {
@@ -904,7 +908,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         }
     }
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
-    const int logw = log_warps_for(t.groups), warps = 1 << logw;
+    const int logw = PLAIN ? 0 : log_warps_for(t.groups), warps = 1 << logw;
     __shared__ float2 shares_of_warps[kThreads / 32];
     ready();
     for (int gb = 0; gb < t.groups; gb += kThreads >> (log + logw)) {
@@ -917,7 +921,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
                                });
         s.x = group_sum(s.x, lanes);
         s.y = group_sum(s.y, lanes);
-        if (logw > 0) {   // one round: the warps' sums joined
+        if (logw > 0) {   // one step: the warps' sums joined
             if (lane == 0) shares_of_warps[threadIdx.x / 32] = s;
             __syncthreads();
             if (at < 32)
