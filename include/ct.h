@@ -302,7 +302,7 @@ CT_API ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, co
  * images and pixels), each NULL when it is not wanted.  x, weight, bias,
  * mean, rstd, p, seed, offset and rng as the forward call had and gave them;
  * a is computed again from x.  With S or N of 0 the parameters' gradients
- * are 0.  The same call gives the same bits: no sum's order depends on
+ * are 0, and the other tensors are not read and may be NULL.  The same call gives the same bits: no sum's order depends on
  * timing. */
 CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const void *dy, const void *x,
                                         const float *mean, const float *rstd, const void *weight,

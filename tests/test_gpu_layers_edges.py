@@ -1,0 +1,62 @@
+"""Group norm and dropout on the GPU: the edges of the accepted sizes and
+arguments, against fp64."""
+
+import pytest
+import torch
+
+from transposed_convolution_02_b200 import ct
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    major, _ = torch.cuda.get_device_capability()
+    assert major == 10, "these kernels are built for sm_100a"
+
+
+def raw_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("n,c,groups", [(3, 8, 2), (5, 30, 3), (2, 4099, 1)])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_no_pixels_without_statistics(dtype, n, c, groups):
+    """Images of no pixels through the C entries: no statistics are read or
+    needed, the parameters' gradients are 0."""
+    x = torch.empty(n, 0, c, dtype=TYPES[dtype], device="cuda")
+    norm = ct._norm_of(x, groups, None, None, "silu", EPS)
+    dw, db = (torch.full((c,), 7.25, device="cuda") for _ in range(2))
+    for p in (0.0, 0.5):
+        assert ct.lib().ct_group_norm_backward(norm.desc, None, None, None, None, None, None, p, 1, 2, None, None,
+                                               dw.data_ptr(), db.data_ptr(), None, raw_stream()) == 0
+        torch.cuda.synchronize()
+        assert not dw.any() and not db.any()
+        dw.fill_(7.25), db.fill_(7.25)
+        mean, rstd = (torch.full((n, groups), 7.25, device="cuda") for _ in range(2))
+        assert ct.lib().ct_group_norm(norm.desc, None, None, None, p, 1, 2, None, None, mean.data_ptr(),
+                                      rstd.data_ptr(), None, raw_stream()) == 0
+        assert ct.lib().ct_group_norm(norm.desc, None, None, None, p, 1, 2, None, None, None, None, None,
+                                      raw_stream()) == 0
+        torch.cuda.synchronize()
+        assert not mean.any()
+        # a square root, a quotient and eps itself rounded: half a step each, the root of eps' halved
+        assert bool(((rstd.double() * EPS ** 0.5 - 1).abs() <= 3 * 2.0 ** -24).all())
+
+
+def test_any_number_of_images_of_no_pixels():
+    """The number of empty images is bounded by no memory: no kernel may walk
+    them one by one."""
+    x = torch.empty(1 << 30, 0, 1 << 24, dtype=torch.float16, device="cuda")
+    assert ct.group_norm_nhwc(x, 1, activation="silu").shape == x.shape
+    x = torch.empty(1 << 24, 0, 1 << 22, dtype=torch.float16, device="cuda")
+    y, mean, rstd = ct.group_norm_nhwc(x, 2, return_stats=True)
+    w = torch.ones(1 << 22, device="cuda")
+    dx, dw, db = ct.group_norm_nhwc_backward(x, x, mean, rstd, 2, w, w)
+    torch.cuda.synchronize()
+    assert dx.shape == x.shape and not dw.any() and not db.any() and not mean.any()

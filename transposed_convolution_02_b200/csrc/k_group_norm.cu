@@ -1,7 +1,21 @@
-// The group norm's geometry: how images are cut into strips and chunks.
+// The group norm's geometry: how images are cut into strips and chunks; and
+// what is left of a call on images of no pixels.
+#include "ct_cuda_util.h"
 #include "group_norm.h"
 
 namespace ct {
+
+namespace {
+
+// The statistics of images without pixels.
+__global__ void __launch_bounds__(kThreads) gn_empty_kernel(float *mean, float *rstd, int64_t n, float eps) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+        if (mean) mean[i] = 0.f;
+        if (rstd) rstd[i] = 1.f / sqrtf(eps);
+    }
+}
+
+}  // namespace
 
 GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensors) {
     GnGeom g = {};
@@ -62,17 +76,29 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
 
 int64_t gn_sums(const GnGeom &g) { return g.cluster > 0 ? 0 : g.N * g.ctiles * g.chunks * g.G; }
 
-size_t gn_forward_ws(const GnGeom &g) { return (size_t)gn_sums(g) * 16; }
+size_t gn_forward_ws(const GnGeom &g) { return g.E == 0 ? 0 : (size_t)gn_sums(g) * 16; }
 
-size_t gn_backward_ws(const GnGeom &g) { return (size_t)(gn_sums(g) + g.N * g.ctiles * g.chunks * g.C) * 8; }
+size_t gn_backward_ws(const GnGeom &g) {
+    return g.E == 0 ? 0 : (size_t)(gn_sums(g) + g.N * g.ctiles * g.chunks * g.C) * 8;
+}
 
+// Images without pixels: no kernel walks them (their number is bounded by no
+// memory), and no statistics are read.
 ct_status gn_forward(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
+    if (g.E == 0) {
+        const int64_t n = g.N * g.G, blocks = ceil_div(n, (int64_t)kThreads);
+        if (n == 0 || (!a.mean && !a.rstd)) return CT_OK;
+        gn_empty_kernel<<<(unsigned)(blocks < 4096 ? blocks : 4096), kThreads, 0, st>>>(a.mean, a.rstd, n, a.eps);
+        return launch_status();
+    }
     if (a.dtype == CT_F32) return gn_forward_f32(g, a, st);
     if (a.dtype == CT_F16) return gn_forward_f16(g, a, st);
     return gn_forward_bf16(g, a, st);
 }
 
-ct_status gn_backward(const GnGeom &g, const GnArgs &a, cudaStream_t st) {
+ct_status gn_backward(const GnGeom &geom, const GnArgs &a, cudaStream_t st) {
+    GnGeom g = geom;
+    if (g.E == 0) g.N = 0;
     if (a.dtype == CT_F32) return gn_backward_f32(g, a, st);
     if (a.dtype == CT_F16) return gn_backward_f16(g, a, st);
     return gn_backward_bf16(g, a, st);
