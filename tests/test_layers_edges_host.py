@@ -2,11 +2,14 @@
 arguments."""
 
 import ctypes
+import os
 
 import pytest
 import torch
 
 from transposed_convolution_02_b200 import ct
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(ct.__file__)), "csrc")
 
 
 def workspace(dtype, n, s, c, groups):
@@ -22,3 +25,14 @@ def workspace(dtype, n, s, c, groups):
                                         (1 << 30, 1 << 24, 1 << 24)])
 def test_no_pixels_need_no_workspace(dtype, n, c, groups):
     assert workspace(dtype, n, 0, c, groups) == (0, 0)
+
+
+def test_cluster_barriers_have_their_warp_together():
+    """The aligned forms of the cluster's barrier are undefined where a warp's
+    lanes arrive apart, which no run shows: in the group norm's kernels, which
+    meet it after branches by lane, each stands directly behind a warp barrier."""
+    with open(os.path.join(CSRC, "group_norm_kernels.cuh")) as f:
+        lines = [line.strip() for line in f]
+    at = [i for i, line in enumerate(lines) if "barrier.cluster" in line]
+    assert len(at) == 2 and all(lines[i - 1] == "__syncwarp();" for i in at)
+    assert not any("cluster_sync" in line for line in lines)

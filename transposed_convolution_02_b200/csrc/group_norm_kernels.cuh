@@ -59,7 +59,6 @@ namespace ct {
 namespace {
 
 using sm100::cluster_ctarank;
-using sm100::cluster_sync;
 using sm100::griddep_launch_dependents;
 using sm100::griddep_wait;
 
@@ -248,7 +247,8 @@ __device__ __forceinline__ uint32_t cut_bits(const GnGeom &g, const Share &t, in
 
 __device__ __forceinline__ float &lane_of(float2 &v, int k) { return k & 1 ? v.y : v.x; }
 
-// The cluster's barrier in two halves.
+// The cluster's barrier in two halves. The aligned forms want their warp
+// together, which a branch or a loop by lane just before does not promise.
 __device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -712,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             [&](int lg, int lane, int lanes, float4 v) {
                 for (int i = lane; i < g.cluster; i += lanes) push(pushed + rank * sh.groups + lg, i, v);
             });
-        cluster_sync();
+        cluster_arrive();
+        cluster_wait();
         for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
             put_stat(g, p, t, sh, lg, join_pushed(sh, pushed, g.cluster, lg));
         apply_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, sh, philox);
@@ -1004,7 +1005,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 for (int i = lane; i < g.cluster; i += lanes)
                     push(pushed + rank * sh.groups + lg, i, make_float4(v.x, v.y, 0.f, 0.f));
             });
-        cluster_sync();
+        cluster_arrive();
+        cluster_wait();
         for (int lg = threadIdx.x; lg < t.groups; lg += kThreads)
             sh.stat[lg] = mul2(join_pushed(sh, pushed, g.cluster, lg), both(inv));
         if (p.dx) grad_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, f, sh, philox);
