@@ -4,12 +4,10 @@ arguments, against fp64."""
 import pytest
 import torch
 
+from test_gpu_layers import EPS, TYPES, both_ways
 from transposed_convolution_02_b200 import ct
 
 pytestmark = pytest.mark.gpu
-
-TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
-EPS = 1e-5
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -60,3 +58,21 @@ def test_any_number_of_images_of_no_pixels():
     dx, dw, db = ct.group_norm_nhwc_backward(x, x, mean, rstd, 2, w, w)
     torch.cuda.synchronize()
     assert dx.shape == x.shape and not dw.any() and not db.any() and not mean.any()
+
+
+WIDE = [
+    ([40, 1, 65537], 1), ([9, 1, 4099], 4099), ([3, 2, 100001], 11), ([5, 3, 70004], 2), ([9, 5, 2570], 10),
+    ([2, 9, 4112], 257), ([3, 7, 2052], 1026), ([1, 1, 1 << 20], 1 << 20), ([6, 2, 16388], 17), ([17, 1, 2058], 3),
+    ([1, 1, (1 << 24) - 1], 1), ([1, 2, 1 << 22], 1 << 10), ([2, 500, 4101], 3), ([1, 900, 2316], 193),
+]
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("i", range(len(WIDE)))
+def test_wide_pixels(i, dtype):
+    """Pixels of more channels than one column tile takes: few and many
+    groups, tiles that start and end inside groups, images that start inside a
+    vector, fewer pixels than copies of the channels along a row."""
+    shape, groups = WIDE[i]
+    both_ways(shape, groups, TYPES[dtype], ["silu", "identity", "gelu"][(i + len(dtype)) % 3], [0.0, 0.3][i % 2],
+              seed=2000 + 10 * i, affine=i % 4 != 3)

@@ -36,3 +36,18 @@ def test_cluster_barriers_have_their_warp_together():
     at = [i for i, line in enumerate(lines) if "barrier.cluster" in line]
     assert len(at) == 2 and all(lines[i - 1] == "__syncwarp();" for i in at)
     assert not any("cluster_sync" in line for line in lines)
+
+
+@pytest.mark.parametrize("n,s,c,groups", [
+    (1024, 1, 65537, 1), (1, 1, 1 << 20, 1), (1, 1, 1 << 24, 1 << 24), (1, 1, (1 << 24) - 1, 1),
+    (1, 1, (1 << 24) - 1, (1 << 24) - 1), (1, 1, 100001, 1), (7, 3, 70007, 7), (64, 1, 1 << 20, 32),
+    (3, 5, 4099, 1), (2, 64, 8200, 50), (1 << 10, 1, 1 << 24, 1 << 12)])
+@pytest.mark.parametrize("dtype", [ct.CT_F32, ct.CT_F16, ct.CT_BF16])
+def test_workspace_of_wide_pixels(dtype, n, s, c, groups):
+    """The workspace is a small multiple of X, however many channels a pixel
+    has: 16 bytes for a group and 8 for a group and a channel, at most twice
+    (an image that starts inside a vector reaches into a second copy of the
+    channels) and in every block of the GPU (the constant)."""
+    x = n * s * c * (4 if dtype == ct.CT_F32 else 2)
+    f, b = workspace(dtype, n, s, c, groups)
+    assert f <= 16 * x + (1 << 20) and b <= 16 * x + (1 << 20)

@@ -48,7 +48,12 @@ struct GnGeom {
     int32_t ctiles;        // column tiles per row
     int32_t rpc, chunks;   // rows per chunk; chunks per strip
     int32_t cluster;       // one launch, a cluster of that many blocks per strip; 0: two launches
-    DivMagic by_bx, by_by, by_cg;   // divisors bx, by, Cg
+    // With several column tiles (all 1 with one): copies of the channels along a
+    // row that an image can have values in, and the most tiles that a group's
+    // channels lie in there. The workspace holds a slot per group and tile of
+    // it, and per channel and copy.
+    int32_t copies, slots;
+    DivMagic by_bx, by_by, by_cg, by_tile;   // divisors bx, by, Cg, bx * V
 };
 
 // Groups that a column tile can meet.

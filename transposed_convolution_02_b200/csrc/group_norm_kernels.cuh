@@ -66,9 +66,9 @@ struct Params {      // kernel arguments besides the geometry
     const void *x, *dy, *weight, *bias;
     void *y, *dx, *dweight, *dbias;
     float *mean, *rstd;
-    float4 *part;    // forward, per strip, part and group: (count, mean, M2, -)
-    float2 *sums;    // backward, per strip, part and group: (sum dh, sum dh h)
-    float2 *chan;    // backward, per strip, chunk and channel: (sum da, sum da h)
+    float4 *part;    // forward, per image, slot, chunk and group: (count, mean, M2, -)
+    float2 *sums;    // backward, per image, slot, chunk and group: (sum dh, sum dh h)
+    float2 *chan;    // backward, per image, chunk, copy and channel: (sum da, sum da h)
     float eps;
     int param_dtype;
     bool vec;
@@ -137,7 +137,8 @@ __device__ __forceinline__ float2 act_slope(float2 a) {
 // One block's chunk of a strip, and the strip's place: all fields are the
 // same in every thread but the last ones.
 struct Share {
-    int64_t strip, n;      // strip; image
+    int64_t n;             // image
+    int tile;              // column tile
     int64_t e0;            // the image's first element
     int head;
     int p0, p1;            // the tile's positions within a row
@@ -166,10 +167,10 @@ struct Shares {
         ty = divq(threadIdx.x, g.by_bx);
         tx = threadIdx.x - ty * g.bx;
     }
-    __device__ __forceinline__ void get(int64_t local, Share &t) {
-        t.strip = local;
+    __device__ __forceinline__ void get(int64_t strip, Share &t) {
+        t.n = strip;
+        t.tile = 0;
         if (PLAIN) {
-            t.n = t.strip;
             t.e0 = t.n * g.E;
             t.head = t.p0 = t.first_group = t.first = 0;
             t.p1 = g.C;
@@ -186,21 +187,21 @@ struct Shares {
             t.rest = 0;
             return;
         }
-        int ct = 0;
-        t.n = t.strip;
         if (g.ctiles > 1) {
-            t.n = t.strip / g.ctiles;
-            ct = (int)(t.strip - t.n * g.ctiles);
+            t.n = strip / g.ctiles;
+            t.tile = (int)(strip - t.n * g.ctiles);
         }
         t.e0 = t.n * g.E;
         t.head = (int)t.e0 & (g.V - 1);
-        t.p0 = ct * g.bx * g.V;
-        t.p1 = (ct + 1) * g.bx < g.LV ? t.p0 + g.bx * g.V : g.LV * g.V;
+        t.p0 = t.tile * g.bx * g.V;
+        t.p1 = (t.tile + 1) * g.bx < g.LV ? t.p0 + g.bx * g.V : g.LV * g.V;
+        if (g.ctiles > 1 && t.p1 > g.copies * g.C)   // the positions after these have no values in any image
+            t.p1 = t.p0 < g.copies * g.C ? g.copies * g.C : t.p0;
         const int c = channel(t, t.p0);
         t.first_group = divq(c, g.by_cg);
-        t.groups = divq(t.p1 - t.p0 - 1 + (c - t.first_group * g.Cg), g.by_cg) + 1;
+        t.groups = t.p1 > t.p0 ? divq(t.p1 - t.p0 - 1 + (c - t.first_group * g.Cg), g.by_cg) + 1 : 0;
         if (t.groups > g.G) t.groups = g.G;
-        t.col = ct * g.bx + tx;
+        t.col = t.tile * g.bx + tx;
         t.ty = ty < g.by && t.col < g.LV ? ty : -1;
         t.first = t.last = 0;
         t.cut_head = t.cut_tail = -1;
@@ -236,6 +237,33 @@ struct Shares {
         return c < 0 ? c + g.C : c;
     }
 };
+
+// Of the tiles below `upto`, how many hold channels of group gi in an image
+// whose channels start at position `head` of its rows (tiles run up, so the
+// runs of a group's channels, one to a copy, meet theirs in order).
+__device__ __forceinline__ int tiles_of(const GnGeom &g, int head, int gi, int upto) {
+    const int end = g.copies * g.C;
+    int n = 0, next = 0;
+    for (int a = gi * g.Cg + head - (g.wraps > 1 ? g.C : 0); a < end; a += g.C) {
+        const int lo = max(a, 0), hi = min(a + g.Cg, end) - 1;
+        if (hi < lo) continue;
+        const int last = divq(hi, g.by_tile);
+        n += max(0, min(last + 1, upto) - max(divq(lo, g.by_tile), next));
+        next = last + 1;
+    }
+    return n;
+}
+
+// The image's first slots in the workspace, and group gi's from this block's
+// chunk there on.
+template <bool PLAIN>
+__device__ __forceinline__ int64_t slots_of(const GnGeom &g, const Share &t) {
+    return (PLAIN ? t.n : t.n * g.slots) * g.chunks;
+}
+template <bool PLAIN>
+__device__ __forceinline__ int64_t slot_at(const GnGeom &g, const Share &t, int gi) {
+    return PLAIN || g.ctiles == 1 ? gi : (int64_t)tiles_of(g, t.head, gi, t.tile) * g.chunks * g.G + gi;
+}
 
 // The elements of a cut vector that are the image's.
 __device__ __forceinline__ uint32_t cut_bits(const GnGeom &g, const Share &t, int64_t e) {
@@ -380,6 +408,11 @@ __device__ __forceinline__ void each_position(const GnGeom &g, const Shares<PLAI
 template <bool PLAIN, typename F>
 __device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t, int c, int count, int lane, int lanes,
                                                 F f) {
+    if (!PLAIN && g.ctiles > 1) {   // run by run: the tile may hold few of the group's channels
+        for (int a = c + t.head - t.p0 - (g.wraps > 1 ? g.C : 0); a < t.p1 - t.p0; a += g.C)
+            for (int pos = max(a, 0) + lane; pos < min(a + count, t.p1 - t.p0); pos += lanes) f(pos);
+        return;
+    }
     for (int j = lane; j < count; j += lanes) {
         if (PLAIN) {
             f(c + j);
@@ -387,8 +420,7 @@ __device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t,
         }
         int pos = c + j + t.head;
         while (pos >= g.C) pos -= g.C;   // more than once where C is below the head
-        for (pos -= t.p0; pos < t.p1 - t.p0; pos += g.C)
-            if (pos >= 0) f(pos);
+        for (; pos < t.p1; pos += g.C) f(pos);
     }
 }
 
@@ -729,23 +761,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     Share t;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
-        float4 *out = p.part + (t.strip * g.chunks + blockIdx.x) * g.G;
+        float4 *out = p.part + (slots_of<PLAIN>(g, t) + blockIdx.x) * g.G;
         block_stats<T, PLAIN>(
             g, p, shares, t, sh, [] {},
             [&](int lg, int lane, int, float4 v) {
-                if (lane == 0) out[wrap_group(g, t.first_group + lg)] = v;
+                if (lane == 0) out[slot_at<PLAIN>(g, t, wrap_group(g, t.first_group + lg))] = v;
             });
-        for (int lg = t.groups + threadIdx.x; lg < g.G; lg += kThreads)   // a count of 0 for groups of other tiles
-            out[wrap_group(g, t.first_group + lg)] = make_float4(0.f, 0.f, 0.f, 0.f);
         __syncthreads();
     }
 }
 
+// A group's parts, which follow each other in the workspace, G apart.
+template <bool PLAIN>
+__device__ __forceinline__ int parts_of(const GnGeom &g, const Share &t, int gi) {
+    return (PLAIN || g.ctiles == 1 ? 1 : tiles_of(g, t.head, gi, g.ctiles)) * g.chunks;
+}
+
 // f(group of the tile, triple) with an image's parts joined: a thread takes
 // every `slices`-th part of a group, neighbours neighbouring groups.
-template <typename F>
-__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const FwdShared &sh, const float4 *in,
-                                           int parts, F f) {
+template <bool PLAIN, typename F>
+__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const FwdShared &sh, const float4 *part,
+                                           F f) {
+    const float4 *in = part + slots_of<PLAIN>(g, t) * g.G;
     float *acc = sh.sums;   // three arrays of kThreads
     const int log = log_lanes_for(t.groups);   // at most 32 slices
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
@@ -755,8 +792,11 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
         if (slice < slices) {
             const int gi = wrap_group(g, t.first_group + lg);
             const float4 *q = in + gi;
+            const int parts = parts_of<PLAIN>(g, t, gi);
             // a part that surely has values: the first of the tile that the group's first channel is in
-            const int first = g.ctiles == 1 ? 0 : (gi * g.Cg + t.head) / (g.bx * g.V) * g.chunks;
+            const int first = PLAIN || g.ctiles == 1
+                                  ? 0
+                                  : tiles_of(g, t.head, gi, divq(gi * g.Cg + t.head, g.by_tile)) * g.chunks;
             j.r = q[(int64_t)first * g.G].y;
 #pragma unroll 8
             for (int i = slice; i < parts; i += slices) j.add(q[(int64_t)i * g.G]);
@@ -786,14 +826,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     Shares<PLAIN> shares(g, p);
     Share t;
     const Philox<DROP == 1> philox(p.rng);
-    const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
         stage_params(g, p, shares, t, sh);
         if (!waited) griddep_wait();
         waited = true;
-        join_parts(g, t, sh, p.part + t.n * parts * g.G, parts, [&](int lg, float4 v) { put_stat(g, p, t, sh, lg, v); });
+        join_parts<PLAIN>(g, t, sh, p.part, [&](int lg, float4 v) { put_stat(g, p, t, sh, lg, v); });
         apply_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, sh, philox);
     }
     if (!waited) griddep_wait();
@@ -899,13 +938,18 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
     }
     const Columns cols = column_sums<2>(g, sh.sums);
     if (p.chan) {
-        float2 *out = p.chan + (t.strip * g.chunks + blockIdx.x) * g.C;
-        for (int c = threadIdx.x; c < g.C; c += kThreads) {   // 0 for other tiles' channels
-            float2 s = both(0.f);
-            group_positions<PLAIN>(g, t, c, 1, 0, 1, [&](int pos) {
-                s = add2(s, make_float2(cols.at(0, pos), cols.at(1, pos) * sh.rstd[pos]));
-            });
-            out[c] = s;
+        float2 *out = p.chan + (t.n * g.chunks + blockIdx.x) * g.copies * g.C;
+        if (!PLAIN && g.ctiles > 1) {   // the tile's own, copies apart
+            for (int pos = threadIdx.x; pos < t.p1 - t.p0; pos += kThreads)
+                out[t.p0 + pos] = make_float2(cols.at(0, pos), cols.at(1, pos) * sh.rstd[pos]);
+        } else {
+            for (int c = threadIdx.x; c < g.C; c += kThreads) {
+                float2 s = both(0.f);
+                group_positions<PLAIN>(g, t, c, 1, 0, 1, [&](int pos) {
+                    s = add2(s, make_float2(cols.at(0, pos), cols.at(1, pos) * sh.rstd[pos]));
+                });
+                out[c] = s;
+            }
         }
     }
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
@@ -1024,23 +1068,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const Philox<DROP == 1> philox(p.rng);
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
         shares.get(s, t);
-        float2 *out = p.sums + (t.strip * g.chunks + blockIdx.x) * g.G;
+        float2 *out = p.sums + (slots_of<PLAIN>(g, t) + blockIdx.x) * g.G;
         const Coef<kVec<T>> f(g, p, shares, t, sh);
         block_sums<T, PLAIN, ACT, DROP>(
             g, p, t, f, sh, philox, [] {},
             [&](int lg, int lane, int, float2 v) {
-                if (lane == 0) out[wrap_group(g, t.first_group + lg)] = v;
+                if (lane == 0) out[slot_at<PLAIN>(g, t, wrap_group(g, t.first_group + lg))] = v;
             });
-        for (int lg = t.groups + threadIdx.x; lg < g.G; lg += kThreads)   // 0 for groups of other tiles
-            out[wrap_group(g, t.first_group + lg)] = both(0.f);
         __syncthreads();
     }
 }
 
 // f(group of the tile, sums) with an image's parts joined.
-template <typename F>
-__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const BwdShared &sh, const float2 *in,
-                                           int parts, F f) {
+template <bool PLAIN, typename F>
+__device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const BwdShared &sh, const float2 *sums,
+                                           F f) {
+    const float2 *in = sums + slots_of<PLAIN>(g, t) * g.G;
     float2 *acc = (float2 *)sh.sums;
     const int log = log_lanes_for(t.groups);
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
@@ -1048,7 +1091,8 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
         const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;
         float2 s = both(0.f);
         if (slice < slices) {
-            const float2 *q = in + wrap_group(g, t.first_group + lg);
+            const int gi = wrap_group(g, t.first_group + lg), parts = parts_of<PLAIN>(g, t, gi);
+            const float2 *q = in + gi;
 #pragma unroll 8
             for (int i = slice; i < parts; i += slices) s = add2(s, q[(int64_t)i * g.G]);
             acc[threadIdx.x] = s;
@@ -1070,7 +1114,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     Shares<PLAIN> shares(g, p);
     Share t;
     const Philox<DROP == 1> philox(p.rng);
-    const int parts = g.ctiles * g.chunks;   // an image's strips and chunks follow each other
     const float inv = (float)(1.0 / ((double)g.S * g.Cg));
     bool waited = false;
     for (int64_t s = blockIdx.y; s < p.strips; s += gridDim.y) {
@@ -1078,28 +1121,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const Coef<kVec<T>> f(g, p, shares, t, sh);
         if (!waited) griddep_wait();
         waited = true;
-        join_parts(g, t, sh, p.sums + t.n * parts * g.G, parts,
-                   [&](int lg, float2 v) { sh.stat[lg] = mul2(v, both(inv)); });
+        join_parts<PLAIN>(g, t, sh, p.sums, [&](int lg, float2 v) { sh.stat[lg] = mul2(v, both(inv)); });
         grad_rows<T, PLAIN, ACT, DROP>(g, p, shares, t, f, sh, philox);
     }
     if (!waited) griddep_wait();
 }
 
-// dw and db: the strips' parts joined, 16 channels to a block, its threads 64
-// rows of them.
+// dw and db: the images', chunks' and copies' parts joined, 16 channels to a
+// block, its threads 64 rows of them.
 constexpr int kParamThreads = 1024, kParamChannels = 16;
 __global__ void __launch_bounds__(kParamThreads)
     gn_back_params_kernel(const __grid_constant__ GnGeom g, const __grid_constant__ Params p) {
     __shared__ float2 sums[kParamThreads];
     griddep_wait();
     const int in = threadIdx.x % kParamChannels, row = threadIdx.x / kParamChannels;
-    const int64_t rows = g.N * g.ctiles * g.chunks;
+    const int64_t rows = g.N * g.chunks * g.copies;
     for (int64_t c0 = (int64_t)blockIdx.x * kParamChannels; c0 < g.C; c0 += (int64_t)gridDim.x * kParamChannels) {
         const int64_t c = c0 + in;
         float2 s = both(0.f);
-        if (c < g.C) {
+        if (c < g.C && g.copies == 1) {
 #pragma unroll 8
             for (int64_t r = row; r < rows; r += kParamThreads / kParamChannels) s = add2(s, p.chan[r * g.C + c]);
+        } else if (c < g.C) {   // by position: an image's head moves its channels
+            for (int64_t r = row; r < rows; r += kParamThreads / kParamChannels) {
+                const int64_t at = c + ((r / ((int64_t)g.chunks * g.copies) * g.E) & (g.V - 1));
+                s = add2(s, p.chan[r * g.C + (at < g.C ? at : at - g.C)]);
+            }
         }
         sums[threadIdx.x] = s;
         __syncthreads();

@@ -44,6 +44,19 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
     g.by_bx = make_magic((uint32_t)g.bx);
     g.by_by = make_magic((uint32_t)g.by);
     g.by_cg = make_magic((uint32_t)g.Cg);
+    const int64_t width = (int64_t)g.bx * g.V;   // positions of a tile
+    g.by_tile = make_magic((uint32_t)width);
+    g.copies = g.slots = 1;
+    if (g.ctiles > 1) {
+        // an image's head moves its channels along the row by less than C, so S
+        // pixels take S + 1 copies there; a group that the row's ends cut has a
+        // run more than copies, and a run of Cg positions lies in at most
+        // ceil((Cg - 1) / width) + 1 tiles
+        if (g.wraps > 1) g.copies = (int32_t)(S + 1 < g.wraps ? S + 1 : g.wraps);
+        const int64_t runs = g.wraps > 1 && g.Cg > 1 ? g.copies + 1 : g.copies;
+        const int64_t tiles = runs * (ceil_div((int64_t)g.Cg - 1, width) + 1);
+        g.slots = (int32_t)(tiles < g.ctiles ? tiles : g.ctiles);
+    }
 
     // One launch: a cluster of up to 8 blocks per strip, where that fills half
     // of the GPU or the tensor is small, and no group spans column tiles.
@@ -74,12 +87,15 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
     return g;
 }
 
-int64_t gn_sums(const GnGeom &g) { return g.cluster > 0 ? 0 : g.N * g.ctiles * g.chunks * g.G; }
+// No product here leaves 64 bits: slots * G <= 19 C (a tile has more than 512
+// positions where there are several), N C <= 2^54, N S C <= 2^60, and chunks is
+// at most 592 / (N ctiles) or S / 1024 + 1.
+int64_t gn_sums(const GnGeom &g) { return g.cluster > 0 ? 0 : g.N * g.slots * g.chunks * g.G; }
 
 size_t gn_forward_ws(const GnGeom &g) { return g.E == 0 ? 0 : (size_t)gn_sums(g) * 16; }
 
 size_t gn_backward_ws(const GnGeom &g) {
-    return g.E == 0 ? 0 : (size_t)(gn_sums(g) + g.N * g.ctiles * g.chunks * g.C) * 8;
+    return g.E == 0 ? 0 : (size_t)(gn_sums(g) + g.N * g.chunks * g.copies * g.C) * 8;
 }
 
 // Images without pixels: no kernel walks them (their number is bounded by no
