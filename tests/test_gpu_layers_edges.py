@@ -76,3 +76,27 @@ def test_wide_pixels(i, dtype):
     shape, groups = WIDE[i]
     both_ways(shape, groups, TYPES[dtype], ["silu", "identity", "gelu"][(i + len(dtype)) % 3], [0.0, 0.3][i % 2],
               seed=2000 + 10 * i, affine=i % 4 != 3)
+
+
+@pytest.mark.parametrize("dtype,shape,groups", [
+    ("fp32", [2, 3000, 2116], 23), ("fp32", [1, 5000, 2068], 47), ("fp16", [2, 4000, 4416], 23),
+    ("bf16", [3, 2500, 4098], 6), ("fp32", [2, 2001, 2565], 27)])
+def test_tiles_that_share_a_group_agree(dtype, shape, groups):
+    """A group whose channels lie in two column tiles is joined by the blocks
+    of both. Where all of its channels are alike, so are the outputs, to the
+    bit: the tiles' statistics and means may differ in no bit, or what mean
+    and rstd hold depends on which block is last."""
+    n, s, c = shape
+    g = torch.Generator(device="cuda").manual_seed(c)
+    for _ in range(4):
+        x, dy = (torch.randn(n, s, groups, 1, generator=g, device="cuda").expand(n, s, groups, c // groups)
+                 .reshape(shape).to(TYPES[dtype]) for _ in range(2))
+        x = x * 3 + 1
+        y, mean, rstd = ct.group_norm_nhwc(x, groups, activation="silu", return_stats=True)
+        dx, _, _ = ct.group_norm_nhwc_backward(dy, x, mean, rstd, groups, activation="silu")
+        for t in (y, dx):
+            t = t.view(n, s, groups, -1)
+            assert torch.equal(t, t[..., :1].expand(t.shape))
+        for _ in range(3):
+            again = ct.group_norm_nhwc(x, groups, activation="silu", return_stats=True)
+            assert all(torch.equal(a, b) for a, b in zip(again, (y, mean, rstd)))

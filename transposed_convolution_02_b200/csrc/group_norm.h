@@ -53,6 +53,7 @@ struct GnGeom {
     // channels lie in there. The workspace holds a slot per group and tile of
     // it, and per channel and copy.
     int32_t copies, slots;
+    int32_t tile_groups;   // groups that a tile meets at most; all with one tile
     DivMagic by_bx, by_by, by_cg, by_tile;   // divisors bx, by, Cg, bx * V
 };
 

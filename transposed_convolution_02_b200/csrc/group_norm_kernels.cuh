@@ -778,13 +778,15 @@ __device__ __forceinline__ int parts_of(const GnGeom &g, const Share &t, int gi)
 }
 
 // f(group of the tile, triple) with an image's parts joined: a thread takes
-// every `slices`-th part of a group, neighbours neighbouring groups.
+// every `slices`-th part of a group, neighbours neighbouring groups. The slices
+// are as many in every tile, so that the tiles which share a group add its
+// parts in the same order and find the same bits.
 template <bool PLAIN, typename F>
 __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, const FwdShared &sh, const float4 *part,
                                            F f) {
     const float4 *in = part + slots_of<PLAIN>(g, t) * g.G;
     float *acc = sh.sums;   // three arrays of kThreads
-    const int log = log_lanes_for(t.groups);   // at most 32 slices
+    const int log = log_lanes_for(g.tile_groups);   // at most 32 slices
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
         const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;   // groups of this step
         const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;
@@ -1085,7 +1087,7 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
                                            F f) {
     const float2 *in = sums + slots_of<PLAIN>(g, t) * g.G;
     float2 *acc = (float2 *)sh.sums;
-    const int log = log_lanes_for(t.groups);
+    const int log = log_lanes_for(g.tile_groups);
     for (int gb = 0; gb < t.groups; gb += kThreads >> log) {
         const int here = t.groups - gb < kThreads >> log ? t.groups - gb : kThreads >> log;
         const int slices = 1 << log, slice = threadIdx.x / here, lg = gb + threadIdx.x - slice * here;

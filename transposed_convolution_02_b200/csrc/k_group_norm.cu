@@ -47,7 +47,11 @@ GnGeom gn_geom(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int tensor
     const int64_t width = (int64_t)g.bx * g.V;   // positions of a tile
     g.by_tile = make_magic((uint32_t)width);
     g.copies = g.slots = 1;
+    g.tile_groups = g.G;
     if (g.ctiles > 1) {
+        // as many as `width` neighbours meet, the first and the last cut
+        const int64_t met = (width + 2 * (int64_t)g.Cg - 2) / g.Cg;
+        if (met < g.G) g.tile_groups = (int32_t)met;
         // an image's head moves its channels along the row by less than C, so S
         // pixels take S + 1 copies there; a group that the row's ends cut has a
         // run more than copies, and a run of Cg positions lies in at most
