@@ -257,9 +257,10 @@ CT_API void ct_plan_destroy(ct_plan_t *plan);
  * an offset of its own, for each tensor. */
 
 /* y = drop(x) + residual, computed in fp32 and rounded once.  n elements;
- * residual may be NULL.  y may be x or residual; other overlap is not
- * allowed.  The gradient in x is this call on dy with the same p, seed and
- * offset and no residual; the gradient in the residual is dy itself. */
+ * residual may be NULL.  y may be x or residual; other overlap, with the words
+ * at rng too, is not allowed.  The gradient in x is this call on dy with the
+ * same p, seed and offset and no residual; the gradient in the residual is dy
+ * itself. */
 CT_API ct_status ct_dropout(int32_t dtype, int64_t n, const void *x, const void *residual, double p,
                             uint64_t seed, uint64_t offset, const void *rng, void *y, void *stream);
 
@@ -293,7 +294,8 @@ CT_API ct_status ct_group_norm_workspace_bytes(const ct_group_norm_desc *desc, s
 /* Forward.  weight and bias may be NULL (1 and 0).  mean and rstd, each
  * [N, groups] fp32, may be NULL; the backward call needs them.  p = 0: no
  * dropout, seed, offset and rng are then not read.  Asynchronous on `stream`.
- * y may not overlap x. */
+ * y, mean and rstd may overlap neither each other nor anything that the call
+ * reads: x, weight, bias and the words at rng. */
 CT_API ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, const void *weight,
                                const void *bias, double p, uint64_t seed, uint64_t offset, const void *rng,
                                void *y, float *mean, float *rstd, void *workspace, void *stream);
@@ -302,8 +304,9 @@ CT_API ct_status ct_group_norm(const ct_group_norm_desc *desc, const void *x, co
  * images and pixels), each NULL when it is not wanted.  x, weight, bias,
  * mean, rstd, p, seed, offset and rng as the forward call had and gave them;
  * a is computed again from x.  With S or N of 0 the parameters' gradients
- * are 0, and the other tensors are not read and may be NULL.  The same call gives the same bits: no sum's order depends on
- * timing. */
+ * are 0, and the other tensors are not read and may be NULL.  dx, dweight and
+ * dbias may overlap neither each other nor anything that the call reads.  The
+ * same call gives the same bits: no sum's order depends on timing. */
 CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const void *dy, const void *x,
                                         const float *mean, const float *rstd, const void *weight,
                                         const void *bias, double p, uint64_t seed, uint64_t offset,

@@ -51,3 +51,27 @@ def test_workspace_of_wide_pixels(dtype, n, s, c, groups):
     x = n * s * c * (4 if dtype == ct.CT_F32 else 2)
     f, b = workspace(dtype, n, s, c, groups)
     assert f <= 16 * x + (1 << 20) and b <= 16 * x + (1 << 20)
+
+
+FLAT = torch.zeros(400)
+PIXELS, OUT = FLAT[:72].view(2, 3, 12), FLAT[100:172].view(2, 3, 12)
+WORDS = FLAT[168:176].view(torch.int64)       # the first two lie in OUT, the last two behind it
+
+
+@pytest.mark.parametrize("call,refusal", [
+    (lambda: ct.group_norm_nhwc(PIXELS, 4, FLAT[100:112], out=OUT), "overlaps"),
+    (lambda: ct.group_norm_nhwc(PIXELS, 4, FLAT[89:101], out=OUT), "overlaps"),
+    (lambda: ct.group_norm_nhwc(PIXELS, 4, FLAT[200:212], FLAT[171:183], out=OUT), "overlaps"),
+    (lambda: ct.group_norm_nhwc(PIXELS, 4, p=0.5, rng=WORDS[:2], out=OUT), "overlaps"),
+    (lambda: ct.dropout(PIXELS, 0.5, rng=WORDS[:2], out=OUT), "overlaps"),
+    (lambda: ct.dropout(PIXELS, 0.5, rng=FLAT[100:104].view(torch.int64), out=OUT), "overlaps"),
+    (lambda: ct.dropout_backward(PIXELS, 0.5, rng=WORDS[1:3], out=OUT), "overlaps"),
+    # beside it: refused for the device alone
+    (lambda: ct.group_norm_nhwc(PIXELS, 4, FLAT[88:100], FLAT[172:184], p=0.5, rng=WORDS[2:], out=OUT), "CUDA"),
+    (lambda: ct.dropout(PIXELS, 0.5, rng=WORDS[2:], out=OUT), "CUDA"),
+    (lambda: ct.dropout(OUT, 0.5, rng=WORDS[2:], residual=PIXELS, out=OUT), "CUDA")])
+def test_output_over_parameters(call, refusal):
+    """Blocks still read the parameters and the random words while others
+    write the output: it may not lie over them."""
+    with pytest.raises(ValueError, match=refusal):
+        call()

@@ -556,7 +556,7 @@ def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="
     if p:
         check_random(p, seed, offset, rng, x.device)
     if out is not None:
-        check_out(out, x, (x,))
+        check_out(out, x, (x, weight, bias, rng if p else None))
     _check_cuda(x, weight, bias)
 
     def call(raw):
@@ -632,6 +632,7 @@ def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream
         check_like(residual, "residual", x)
     if out is not None:
         check_out(out, x, (x, residual), in_place=True)
+        check_out(out, x, (rng,))
     _check_cuda(x, residual)
 
     def call(raw):
