@@ -100,3 +100,28 @@ def test_tiles_that_share_a_group_agree(dtype, shape, groups):
         for _ in range(3):
             again = ct.group_norm_nhwc(x, groups, activation="silu", return_stats=True)
             assert all(torch.equal(a, b) for a, b in zip(again, (y, mean, rstd)))
+
+
+def test_inputs_whose_derivatives_would_be_lost():
+    """No call records a derivative: inputs that carry one are refused, the
+    statistics of the backward call as well."""
+    x, w, b = torch.randn(2, 9, 8, device="cuda"), torch.ones(8, device="cuda"), torch.zeros(8, device="cuda")
+    _, mean, rstd = ct.group_norm_nhwc(x, 2, w, b, return_stats=True)
+    with torch.autograd.forward_ad.dual_level(), torch.no_grad():
+        def dual(t):
+            return torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))
+        for call in (lambda: ct.group_norm_nhwc(dual(x), 2, w, b), lambda: ct.group_norm_nhwc(x, 2, dual(w), b),
+                     lambda: ct.group_norm_nhwc(x, 2, w, dual(b)), lambda: ct.dropout(dual(x), 0.5),
+                     lambda: ct.dropout(x, 0.5, residual=dual(x)), lambda: ct.dropout_backward(dual(x), 0.5),
+                     lambda: ct.group_norm_nhwc_backward(dual(x), x, mean, rstd, 2, w, b),
+                     lambda: ct.group_norm_nhwc_backward(x, x, dual(mean), rstd, 2, w, b),
+                     lambda: ct.group_norm_nhwc_backward(x, x, mean, dual(rstd), 2, w, b)):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+    for call in (lambda m: ct.group_norm_nhwc_backward(x, x, m, rstd, 2, w, b),
+                 lambda m: ct.group_norm_nhwc_backward(x, x, mean, m, 2, w, b)):
+        leaf = rstd.clone().requires_grad_()
+        with pytest.raises(ValueError, match="gradient"):
+            call(leaf)
+        with torch.no_grad():
+            call(leaf)

@@ -75,3 +75,21 @@ def test_output_over_parameters(call, refusal):
     write the output: it may not lie over them."""
     with pytest.raises(ValueError, match=refusal):
         call()
+
+
+def test_tangents_are_refused():
+    """Forward-mode tangents would be dropped silently, under no_grad too."""
+    class OnCuda(torch.Tensor):
+        is_cuda = True
+
+    x, w = torch.zeros(3).as_subclass(OnCuda), torch.zeros(3)
+    with torch.autograd.forward_ad.dual_level():
+        ct._check_cuda(x, w, None)
+        dual = torch.autograd.forward_ad.make_dual(w, torch.ones(3))
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                with pytest.raises(ValueError, match="tangent"):
+                    ct._check_cuda(x, None, dual)
+                with pytest.raises(ValueError, match="tangent"):
+                    ct._check_cuda(dual.as_subclass(OnCuda), w)
+    ct._check_cuda(x, w)

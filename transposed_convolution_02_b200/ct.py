@@ -17,6 +17,7 @@ import functools
 import os
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libct.so")
@@ -460,10 +461,14 @@ def check_norm(x, groups, weight, bias, activation):
 
 
 def _check_cuda(x, *leaves):
-    """The operators run on CUDA tensors only and record no autograd graph: a
-    call that would drop a gradient silently is refused."""
+    """The operators run on CUDA tensors only and record no derivatives: a call
+    that would drop a gradient or a forward-mode tangent silently is refused."""
     if not x.is_cuda:
         raise ValueError("X must be a CUDA tensor")
+    if forward_ad._current_level >= 0:      # within a dual_level, whatever the grad mode
+        for t in (x,) + leaves:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("an input carries a forward-mode tangent, and this call computes none")
     if not torch.is_grad_enabled():
         return
     for t in (x,) + leaves:
@@ -595,7 +600,7 @@ def group_norm_nhwc_backward(dy, x, mean, rstd, groups, weight=None, bias=None, 
                              % (name, list(norm.stats), x.device))
     if p:
         check_random(p, seed, offset, rng, x.device)
-    _check_cuda(x, dy, weight, bias)
+    _check_cuda(x, dy, mean, rstd, weight, bias)
 
     def call(raw):
         xc, dyc, m, r = x.contiguous(), dy.contiguous(), mean.contiguous(), rstd.contiguous()
