@@ -4,6 +4,7 @@ arguments."""
 import ctypes
 import os
 
+import numpy
 import pytest
 import torch
 
@@ -93,3 +94,13 @@ def test_tangents_are_refused():
                 with pytest.raises(ValueError, match="tangent"):
                     ct._check_cuda(dual.as_subclass(OnCuda), w)
     ct._check_cuda(x, w)
+
+
+@pytest.mark.parametrize("groups", [2.5, 1.25, numpy.float64(2.5)])
+def test_group_counts_are_whole_numbers(groups):
+    """A fraction that divides the channels (20 by 2.5) is no number of groups."""
+    x = torch.zeros(2, 3, 20)
+    with pytest.raises(ValueError, match="groups"):
+        ct._norm_of(x, groups, None, None, "silu", 1e-5)
+    for whole in (4, 4.0, numpy.int64(4)):
+        assert ct._norm_of(x, whole, None, None, "silu", 1e-5).stats == (2, 4)

@@ -445,8 +445,8 @@ def check_norm(x, groups, weight, bias, activation):
     if x.dim() < 2:
         raise ValueError("X must be [N, D.., C], it has shape %s" % list(x.shape))
     c = x.shape[-1]
-    if groups < 1 or c < 1 or c % groups != 0:
-        raise ValueError("%d channels cannot be split into %d groups" % (c, groups))
+    if groups < 1 or groups % 1 != 0 or c < 1 or c % groups != 0:
+        raise ValueError("%d channels cannot be split into %s groups" % (c, groups))
     if activation not in NORM_ACTIVATION:
         raise ValueError("activation must be one of %s, not %r" % (sorted(NORM_ACTIVATION), activation))
     for t, name in ((weight, "weight"), (bias, "bias")):
