@@ -4,6 +4,7 @@ arguments, against fp64."""
 import pytest
 import torch
 
+import layers_ref as ref
 from test_gpu_layers import EPS, TYPES, both_ways
 from transposed_convolution_02_b200 import ct
 
@@ -125,3 +126,42 @@ def test_inputs_whose_derivatives_would_be_lost():
             call(leaf)
         with torch.no_grad():
             call(leaf)
+
+
+# pixels of an image of s that lie far from the others: the first one, a column
+# at the image's border, a band at its top
+FAR_PIXELS = {"first": lambda s: slice(0, 1), "column": lambda s: slice(0, s, 256), "band": lambda s: slice(0, s // 290)}
+
+
+@pytest.mark.parametrize("far", [0.0, 20.0, 100.0, 1e4])
+@pytest.mark.parametrize("where", sorted(FAR_PIXELS))
+@pytest.mark.parametrize("dtype,shape,groups", [
+    ("fp16", [300, 60000, 8], 4), ("bf16", [160, 60000, 8], 2), ("fp32", [300, 30000, 8], 4),
+    ("fp32", [1, 2000000, 8], 4), ("fp32", [300, 30000, 7], 1), ("fp16", [2, 300001, 24], 3),
+    ("fp32", [8, 16384, 128], 32)])
+def test_far_pixels_in_long_images(dtype, shape, groups, where, far):
+    """Pixels far from all others, those among them that sums and joins are
+    shifted by: the statistics keep the bound that they have without them,
+    however many pixels follow."""
+    n, s, c = shape
+    x = torch.randn(shape, generator=torch.Generator(device="cuda").manual_seed(s), device="cuda")
+    if far:
+        at = FAR_PIXELS[where](s)
+        x[:, at] = far
+        x[::3, at, c // 2:] = -far
+    x = x.to(TYPES[dtype])
+    y, mean, rstd = ct.group_norm_nhwc(x, groups, eps=EPS, return_stats=True)
+    g = x.view(n, s, groups, -1).double()
+    m = g.mean(dim=(1, 3))
+    d = g - m[:, None, :, None]
+    r = 1 / torch.sqrt((d * d).mean(dim=(1, 3)) + EPS)
+    spread = d.abs().mean(dim=(1, 3))
+    assert bool(((mean - m).abs() <= ref.U * (ref.CHAIN * 2 * spread + 4 * m.abs())).all())
+    assert float((rstd / r - 1).abs().max()) <= ref.U * (ref.CHAIN + 8)
+    del d, g
+    # y from the fp64 statistics, pixels of the image's start, middle and end
+    for at in (0, s // 2, s - 100):
+        h = (x[:, at: at + 100].double().view(n, 100, groups, -1) - m[:, None, :, None]) * r[:, None, :, None]
+        e = (6 + ref.CHAIN / 2) * h.abs() + ref.CHAIN * 2 + 4 * (m.abs() * r)[:, None, :, None]
+        off = (y[:, at: at + 100].double().view(h.shape) - h).abs()
+        assert bool((off <= 1.01 * (ref.HALF[TYPES[dtype]] * h.abs() + ref.U * e) + ref.TINY[TYPES[dtype]]).all())

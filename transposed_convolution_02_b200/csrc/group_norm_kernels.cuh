@@ -39,12 +39,18 @@
 // arithmetic; SiLU's exponential and reciprocal take the special-function pipe
 // to half of its rate.
 //
-// Statistics: every thread of a column sums x - k and (x - k)^2 with one k, the
-// mean of up to four rows of the chunk, so a block's sums are plain sums; they
-// are then joined as (count, mean, M2) with M2 the sum of squared distances
-// from the mean.  As k is the mean of m of the n values summed, m (k - mean)^2
-// <= M2, so sum (x - k)^2 <= (1 + n/m) M2, and the subtraction that gives M2
-// loses at most that factor however far the mean is from 0.
+// Statistics: a thread sums x - k and (x - k)^2 with k one of its own values and
+// makes its mean and M2 of them, M2 being the sum of squared distances from the
+// mean; the threads of a column are joined about one of their means, the columns
+// of a group about the group's, blocks about the mean of one.  What an M2 is the
+// difference of is never much larger than it, however far the mean is from 0: k is
+// the middle() one of four values, so at least two of the thread's n <= 1024 lie
+// as far from their mean as k, the sum of (x - k)^2 is at most 1 + n/2 times M2,
+// and about 1.5 times where no two of the four are far; likewise for threads and
+// blocks.  (With one k for a whole column, the mean of four of its n <= 2^18
+// values, rstd of [300, 60000] values was off by up to 40000 steps of 2^-24 where
+// the first pixel was a thousand deviations off; it is now by 8, for 0.4 us more
+// at decoder size.)
 #pragma once
 
 #include <string.h>
@@ -286,10 +292,17 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+struct Nothing {
+    template <typename Get>
+    __device__ __forceinline__ void operator()(int, Get) const {}
+};
+
 // f(element, pairs of each of N tensors, bits) for a thread's vectors: the
 // whole ones with U in flight, then those that an end of the image cuts (the
 // elements outside `bits` read as 0); on unaligned tensors all one by one.
-// pre() runs before the first of them, while the first loads are in flight.
+// pre(n, get) runs before the first of them, while the first loads are in
+// flight: n whole vectors follow, get(i) is number i < min(n, U) of the first
+// tensor's.
 template <typename T, bool PLAIN, int N, int U, typename Pre, typename F>
 __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T *const (&src)[N], bool vec, Pre pre,
                                        F f) {
@@ -312,7 +325,7 @@ __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T 
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (u < left) load(u);
-        pre();
+        pre(left, [&](int i) { return w[i][0]; });
         while (left > 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -325,7 +338,7 @@ __device__ __forceinline__ void stream(const GnGeom &g, const Share &t, const T 
         }
         if (PLAIN || (t.cut_head < 0 && t.cut_tail < 0)) return;
     } else {
-        pre();
+        pre(t.last - t.first, [&](int i) { return gather(src[0] + t.e + (t.first + i) * step); });
     }
 #pragma unroll 1
     for (int i = vec ? t.last : t.first; i < t.last + 2; ++i) {
@@ -489,46 +502,80 @@ size_t forward_smem(const GnGeom &g) {
            (size_t)groups_max(g) * (32 * g.cluster + 8);
 }
 
-// The shift k of a thread's channels, the same in every thread of a column: the
-// mean of up to four rows of the chunk, or where no row of it is whole the
-// image's first pixel.
-template <typename T, bool PLAIN>
+// The larger of the smaller ones of two pairs: at least two of the four lie on
+// either side of it (itself among them), so that it is as far from their mean as
+// two of them, and no single far one is taken.
+__device__ __forceinline__ float middle(float a, float b, float c, float d) { return fmaxf(fminf(a, b), fminf(c, d)); }
+
+// Per position, runs of thread rows apart: the sums of n (m - r) and of
+// M2 + n (m - r)^2 about r = sh.nmean, and of n where rows are not whole.
+struct ColumnStats {
+    const float *s, *q, *n;
+    int width, segs;
+    __device__ __forceinline__ float sum(const float *at) const {
+        float v = at[0];
+        for (int i = 1; i < segs; ++i) v += at[i * width];
+        return v;
+    }
+};
+
+// The thread rows of sh.sums (m, M2 and n of each) joined, about the middle one
+// of four rows' means. Row y of an array is read by one thread only but for the
+// means', so the sums go to the first rows of M2.
+__device__ __forceinline__ ColumnStats column_stats(const GnGeom &g, const Share &t, const FwdShared &sh, bool counted) {
+    const int width = g.bx * g.V, apart = kThreads * g.V;
+    float *means = sh.sums, *m2 = means + apart, *counts = m2 + apart;
+    int segs = 1;
+    while (segs * 2 * width <= kThreads && segs * 4 <= g.by) segs *= 2;
+    __syncthreads();
+    if (g.by == 1) return {means, m2, counts, width, 1};   // the row's own, with s = 0
+    const int runs = segs * width, all = g.by * width, rounds = divq(t.rows, g.by_by);
+    const int more = (t.rows - rounds * g.by) * width;   // rows below have a value more
+    const float least = (float)rounds, most = (float)(rounds + 1);
+    const int last = max(min(g.by, t.rows) - 1, 0);   // the last row that has values
+    for (int i = threadIdx.x; i < runs; i += kThreads) {
+        int pos = i;
+        while (pos >= width) pos -= width;
+        const float r = middle(means[pos], means[pos + min(1, last) * width], means[pos + min(2, last) * width],
+                               means[pos + min(3, last) * width]);
+        float n = 0.f, s = 0.f, q = 0.f;
+#pragma unroll 8
+        for (int y = i; y < all; y += runs) {
+            const float ny = counted ? counts[y] : y - pos < more ? most : least;
+            const float d = means[y] - r, w = ny * d;
+            n += ny;
+            s += w;
+            q += m2[y] + w * d;
+        }
+        if (i == pos) sh.nmean[pos] = r;
+        m2[i] = s;
+        m2[runs + i] = q;
+        if (counted) counts[i] = n;
+    }
+    __syncthreads();
+    return {m2, m2 + runs, counts, width, segs};
+}
+
+// The shift k of a thread's channels, of its n whole vectors get(i): the middle()
+// of the first four's values, or where there is no whole vector the image's first
+// pixel. One of the values, so that x - k has x's low bits, which vary: with bits
+// of k below x's steps, the same in every term, each addition rounds the same way
+// once a sum has grown past them (rstd of 60000 fp16 values was off by 50 steps
+// of 2^-24).
+template <typename T, bool PLAIN, typename Get>
 __device__ __forceinline__ void shift(const GnGeom &g, const Params &p, const Shares<PLAIN> &shares, const Share &t,
-                                      float2 (&k)[kVec<T> / 2]) {
+                                      int n, Get get, float2 (&k)[kVec<T> / 2]) {
     constexpr int V = kVec<T>, P = V / 2;
-    const T *x = (const T *)p.x;
 #pragma unroll
     for (int j = 0; j < P; ++j) k[j] = both(0.f);
-    const int64_t step = (int64_t)V * g.LV * g.by, top = t.e - (int64_t)V * g.LV * t.ty;   // the column's first row
-    const int64_t whole = t.whole_rows + (t.col < t.rest ? 1 : 0) - t.r0;
-    const int rows = whole < t.rows ? (int)whole : t.rows;
-    const int skip = t.head != 0 && t.r0 == 0 && t.col == 0 ? 1 : 0;
-    int n = 0;
-    uint4 w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i >= skip && i * g.by < rows) {
-            const T *q = x + top + i * step;
-            w[i] = PLAIN || p.vec ? *reinterpret_cast<const uint4 *>(q) : gather(q);
-            ++n;
-        }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i >= skip && i * g.by < rows) {
-            float2 v[P];
-            unpack(w[i], v, T());
-#pragma unroll
-            for (int j = 0; j < P; ++j) k[j] = add2(k[j], v[j]);
-        }
     if (n > 0) {
-        const float inv = n == 1 ? 1.f : n == 2 ? 0.5f : n == 3 ? 1.f / 3.f : 0.25f;
-#pragma unroll
-        for (int j = 0; j < P; ++j) k[j] = mul2(k[j], both(inv));
+        const uint4 a = get(0), b = n > 1 ? get(1) : a, c = n > 2 ? get(2) : b, d = n > 3 ? get(3) : c;
+        unpack(larger(smaller(a, b, T()), smaller(c, d, T()), T()), k, T());
     } else if (!PLAIN) {
         int c = shares.channel(t, V * t.col);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (g.E > 0) lane_of(k[i / 2], i) = to_f<T>(x[t.e0 + c]);
+            lane_of(k[i / 2], i) = to_f<T>(((const T *)p.x)[t.e0 + c]);
             if (++c == g.C) c = 0;
         }
     }
@@ -537,7 +584,7 @@ __device__ __forceinline__ void shift(const GnGeom &g, const Params &p, const Sh
 // The running join of (count, mean, M2) triples about a reference r, the mean
 // of one of them: sum n (m - r) and sum M2 + n (m - r)^2.  As r is the mean of
 // part of the values, the distance that the second carries is at most their M2
-// times the number of parts of that size.
+// times the number of parts of that size (of half of it where r is a middle()).
 struct Joined {
     float n, s, q, r;
     __device__ __forceinline__ void add(float4 v) {
@@ -569,9 +616,8 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
 #pragma unroll
         for (int k = 0; k < V; ++k) n[k] = whole;
         const T *const x[1] = {(const T *)p.x};
-        auto pre = [&] {
-            shift<T, PLAIN>(g, p, shares, t, nk);
-            if (threadIdx.x < g.bx) put_own<V>(sh.nmean, nk);   // the block's shifts, for the merge
+        auto pre = [&](int whole_ones, auto get) {
+            shift<T, PLAIN>(g, p, shares, t, whole_ones, get, nk);
 #pragma unroll
             for (int j = 0; j < P; ++j) nk[j] = neg2(nk[j]);
         };
@@ -595,7 +641,21 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
                     }
             }
         });
-        if (t.ty >= 0) {
+        if (t.ty >= 0) {   // to mean and M2
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const float2 inv = make_float2(n[2 * j] > 0.f ? __fdividef(1.f, n[2 * j]) : 0.f,
+                                               n[2 * j + 1] > 0.f ? __fdividef(1.f, n[2 * j + 1]) : 0.f);
+                const float2 d = mul2(s[j], inv);
+                q[j] = fma2(neg2(s[j]), d, q[j]);
+                q[j] = make_float2(at_least_0(q[j].x), at_least_0(q[j].y));
+                s[j] = add2(d, neg2(nk[j]));
+            }
+            if (g.by == 1) {   // nothing to join: about its own mean
+                put_own<V>(sh.nmean, s);
+#pragma unroll
+                for (int j = 0; j < P; ++j) s[j] = both(0.f);
+            }
             put_own<V>(sh.sums, s);
             put_own<V>(sh.sums + kThreads * V, q);
             if (!PLAIN && g.wraps > 1) {
@@ -607,9 +667,7 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
         }
     }
     const bool counted = !PLAIN && g.wraps > 1;   // counts differ by position
-    Columns cols;
-    if (counted) cols = column_sums<3>(g, sh.sums);
-    else cols = column_sums<2>(g, sh.sums);
+    const ColumnStats cols = column_stats(g, t, sh, counted);
     // per group: its positions' means, then the distances from their mean
     const int log = log_lanes_for(t.groups), lanes = 1 << log, lane = threadIdx.x & (lanes - 1);
     const int logw = PLAIN ? 0 : log_warps_for(t.groups), warps = 1 << logw;
@@ -621,18 +679,18 @@ __device__ __forceinline__ void block_stats(const GnGeom &g, const Params &p, co
         const int c = wrap_group(g, t.first_group + lg) * g.Cg, many = lg < t.groups ? g.Cg : 0;
         float sn = 0.f, sm = 0.f, sq = 0.f;
         group_positions<PLAIN>(g, t, c, many, at, lanes << logw, [&](int pos) {
-            const float n = counted ? cols.at(2, pos) : rows;
+            const float n = counted ? cols.sum(cols.n + pos) : rows;
             sn += n;
-            sm += n * sh.nmean[pos] + cols.at(0, pos);
+            sm += n * sh.nmean[pos] + cols.sum(cols.s + pos);
         });
         sn = group_sum(sn, lanes);
         sm = group_sum(sm, lanes);
         const float m = sn > 0.f ? __fdividef(sm, sn) : 0.f;
         group_positions<PLAIN>(g, t, c, many, at, lanes << logw, [&](int pos) {
-            const float n = counted ? cols.at(2, pos) : rows;
+            const float n = counted ? cols.sum(cols.n + pos) : rows;
             const float inv = counted ? (n > 0.f ? __fdividef(1.f, n) : 0.f) : by_rows;
-            const float s = cols.at(0, pos), d = sh.nmean[pos] + s * inv - m;
-            sq += at_least_0(cols.at(1, pos) - s * s * inv) + n * d * d;
+            const float s = cols.sum(cols.s + pos), d = sh.nmean[pos] + s * inv - m;
+            sq += at_least_0(cols.sum(cols.q + pos) - s * s * inv) + n * d * d;
         });
         sq = group_sum(sq, lanes);
         float4 v = make_float4(sn, m, sq, 0.f);
@@ -706,7 +764,7 @@ __device__ __forceinline__ void apply_rows(const GnGeom &g, const Params &p, con
     const uint32_t limit = drop_limit(p.rng.threshold);
     constexpr bool on = DROP != 0;
     if (t.ty >= 0)
-        stream<T, PLAIN, 1, kForwardUnroll>(g, t, x, p.vec, [] {}, [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
+        stream<T, PLAIN, 1, kForwardUnroll>(g, t, x, p.vec, Nothing(), [&](int64_t e, float2 (&v)[1][P], uint32_t bits) {
         uint32_t w[P];
         if (on) draw(philox, (uint64_t)e, w);
 #pragma unroll
@@ -795,11 +853,18 @@ __device__ __forceinline__ void join_parts(const GnGeom &g, const Share &t, cons
             const int gi = wrap_group(g, t.first_group + lg);
             const float4 *q = in + gi;
             const int parts = parts_of<PLAIN>(g, t, gi);
-            // a part that surely has values: the first of the tile that the group's first channel is in
+            // about the middle() of four parts of the tile that the group's first channel is in, of which
+            // the first surely has values
             const int first = PLAIN || g.ctiles == 1
                                   ? 0
                                   : tiles_of(g, t.head, gi, divq(gi * g.Cg + t.head, g.by_tile)) * g.chunks;
-            j.r = q[(int64_t)first * g.G].y;
+            float4 some[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) some[k] = q[(int64_t)(first + (int)((int64_t)g.chunks * k / 4)) * g.G];
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                if (some[k].x == 0.f) some[k].y = some[0].y;
+            j.r = middle(some[0].y, some[1].y, some[2].y, some[3].y);
 #pragma unroll 8
             for (int i = slice; i < parts; i += slices) j.add(q[(int64_t)i * g.G]);
             acc[threadIdx.x] = j.n;
@@ -915,7 +980,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
         for (int j = 0; j < P; ++j) u[j] = w[j] = both(0.f);
         const T *const src[2] = {(const T *)p.x, (const T *)p.dy};
         if (t.ty >= 0)
-            stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+            stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, Nothing(), [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
             uint32_t r[P];
             if (on) draw(philox, (uint64_t)e, r);
             if (bits != ~0u) {   // outside the image x is the mean and dy is 0: nothing is added
@@ -1009,7 +1074,7 @@ __device__ __forceinline__ void grad_rows(const GnGeom &g, const Params &p, cons
     const uint32_t limit = drop_limit(p.rng.threshold);
     constexpr bool on = DROP != 0;
     if (t.ty >= 0)
-        stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, [] {}, [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
+        stream<T, PLAIN, 2, DROP || !PLAIN ? kFewerUnroll : kBackwardUnroll>(g, t, src, p.vec, Nothing(), [&](int64_t e, float2 (&v)[2][P], uint32_t bits) {
         uint32_t r[P];
         if (on) draw(philox, (uint64_t)e, r);
 #pragma unroll

@@ -66,6 +66,40 @@ __device__ __forceinline__ uint4 pack(const float2 (&v)[4], T) {
     return make_uint4(pack1(v[0], T()), pack1(v[1], T()), pack1(v[2], T()), pack1(v[3], T()));
 }
 
+// Element by element the smaller and the larger of two vectors.
+__device__ __forceinline__ uint32_t smaller1(uint32_t a, uint32_t b, float) {
+    return __float_as_uint(fminf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t larger1(uint32_t a, uint32_t b, float) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+}
+__device__ __forceinline__ uint32_t smaller1(uint32_t a, uint32_t b, __half) {
+    const __half2 m = __hmin2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+__device__ __forceinline__ uint32_t larger1(uint32_t a, uint32_t b, __half) {
+    const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+__device__ __forceinline__ uint32_t smaller1(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 m =
+        __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+__device__ __forceinline__ uint32_t larger1(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 m =
+        __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+template <typename T>
+__device__ __forceinline__ uint4 smaller(uint4 a, uint4 b, T t) {
+    return make_uint4(smaller1(a.x, b.x, t), smaller1(a.y, b.y, t), smaller1(a.z, b.z, t), smaller1(a.w, b.w, t));
+}
+template <typename T>
+__device__ __forceinline__ uint4 larger(uint4 a, uint4 b, T t) {
+    return make_uint4(larger1(a.x, b.x, t), larger1(a.y, b.y, t), larger1(a.z, b.z, t), larger1(a.w, b.w, t));
+}
+
 // A vector from any element's address.
 __device__ __forceinline__ uint4 gather(const float *p) {
     const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
