@@ -165,3 +165,39 @@ def test_far_pixels_in_long_images(dtype, shape, groups, where, far):
         e = (6 + ref.CHAIN / 2) * h.abs() + ref.CHAIN * 2 + 4 * (m.abs() * r)[:, None, :, None]
         off = (y[:, at: at + 100].double().view(h.shape) - h).abs()
         assert bool((off <= 1.01 * (ref.HALF[TYPES[dtype]] * h.abs() + ref.U * e) + ref.TINY[TYPES[dtype]]).all())
+
+
+@pytest.mark.parametrize("c,rows,groups", [(8, 128, 4), (7, 36 * 4, 1), (64, 16, 8)])
+def test_threads_that_sum_a_thousand_vectors(c, rows, groups, monkeypatch):
+    """As many images as fill the GPU, each the work of one block, so long that
+    a thread adds 1000 vectors (`rows` pixels of a block at a time): forward and
+    backward against fp64. The longest chain of additions is a thread's 1024, a
+    column's 256 and 64 for lanes, parts and images."""
+    monkeypatch.setattr(ref, "CHAIN", 1024 + 256 + 64)
+    n, s = 300, 1000 * rows - 3
+    gen = torch.Generator(device="cuda").manual_seed(c)
+    x, dy = (torch.randn(n, s, c, generator=gen, device="cuda") for _ in range(2))
+    w, b = (torch.randn(c, generator=gen, device="cuda") for _ in range(2))
+    y, mean, rstd = ct.group_norm_nhwc(x, groups, w, b, eps=EPS, activation="silu", return_stats=True)
+    dx, dw, db = ct.group_norm_nhwc_backward(dy, x, mean, rstd, groups, w, b, activation="silu")
+    w64, b64, one = w.double(), b.double(), torch.ones(1, dtype=torch.float64, device="cuda")
+    sums = [torch.zeros(c, dtype=torch.float64, device="cuda") for _ in range(4)]
+    part = 30                                   # images at a time
+    for i in range(0, n, part):
+        v, g = x[i: i + part].double(), dy[i: i + part].double()
+        want, m, r, a = ref.forward(v, groups, w64, b64, EPS, "silu")
+        spread = (v - ref._spread(m, v, groups)).abs().view(part, s, groups, -1).mean(dim=(1, 3))
+        assert bool(((mean[i: i + part] - m).abs() <= ref.U * (ref.CHAIN * 2 * spread + 4 * m.abs())).all())
+        assert bool(((rstd[i: i + part] / r - 1).abs() <= ref.U * (ref.CHAIN + 8)).all())
+        bound = ref.forward_bound(v, m, r, groups, w64, b64, a, want, torch.float32, 1.0)
+        assert bool(((y[i: i + part] - want).abs() <= bound).all())
+        del want, a, bound
+        # the gradients with the statistics as they are
+        m, r = mean[i: i + part].double(), rstd[i: i + part].double()
+        want = ref.backward(g, v, m, r, groups, w64, b64, "silu")
+        bounds = ref.backward_bounds(g, v, m, r, groups, w64, b64, "silu", one, torch.float32, torch.float32, *want)
+        assert bool(((dx[i: i + part] - want[0]).abs() <= bounds[0]).all())
+        for j in (1, 2):
+            sums[j - 1] += want[j]
+            sums[j + 1] += bounds[j]            # the roundings of the parts bound that of their sum
+    assert bool(((dw - sums[0]).abs() <= sums[2]).all()) and bool(((db - sums[1]).abs() <= sums[3]).all())
