@@ -8,9 +8,9 @@
 //   dw = sum da h,  db = sum da  (over images and pixels),
 //   dx = rstd (dh - mean(dh) - h mean(dh h))  (means over the group).
 //
-// Bound: HBM.  Forward must read x and write y, backward read x and dy and
-// write dx; both need a whole group's sums before the first output, so there
-// are two passes over the inputs.
+// Bound: HBM, at x and y once forward, x, dy and dx once backward.  All of a
+// group's values are needed before its first output, so there are two passes over
+// the inputs, of which the second finds them in L2 or reads HBM again.
 //   One launch: a cluster of blocks works on an image (a strip), joins its
 // blocks' sums through distributed shared memory and goes on to the second
 // pass.  For small tensors, where a launch counts, and where such clusters fill
@@ -19,11 +19,10 @@
 // workspace, and apply, each block joining the parts of its groups.  The
 // second starts while the first one ends (programmatic dependent launch).
 // Inputs of up to about 90 MB are then found in L2.
-// Measured, [8, 128x128, 128] fp16 with SiLU, 33.5 MB in and out: 25.6 us,
-// where reading x alone takes 6.9 and copying it 12.3; of it 8.4 reading, 3.5
-// sums and joining them, 2 between the launches and the parts, 7.2 on average
-// and 10.3 at most writing.  [16, 16384, 256] fp32, 268 MB: 151 us, a read (41)
-// and a copy (87) being the least for tensors that L2 does not hold.
+// Measured, [8, 128x128, 128] fp16 with SiLU, 33.5 MB in and out: 25.4 us,
+// where reading x alone takes 6.9 and copying it 12.3.  [16, 16384, 256] fp32,
+// 268 MB in and out: 148 us, where x is read twice from HBM; one read and one
+// write of it would take 82 at the measured copy rate (a copy takes 87).
 // Tried and slower: images taken in waves that fit L2 (every wave paid the 10
 // us that do not stream; vocoder size 176 to 230 us), a ring of bulk copies
 // with a copying warp (its hand-overs cost more than the registers it saved),
@@ -37,7 +36,7 @@
 // and joins: as many instructions as about 25 vectors) then weighs more (decoder
 // size 27.3 us).  Packed fp32 instructions (two lanes an issue slot) carry the
 // arithmetic; SiLU's exponential and reciprocal take the special-function pipe
-// to half of its rate.
+// to 0.49 of its rate at that size and 0.65 at [16, 112x112, 512] fp16.
 //
 // Statistics: a thread sums x - k and (x - k)^2 with k one of its own values and
 // makes its mean and M2 of them, M2 being the sum of squared distances from the
@@ -47,10 +46,11 @@
 // the middle() one of four values, so at least two of the thread's n <= 1024 lie
 // as far from their mean as k, the sum of (x - k)^2 is at most 1 + n/2 times M2,
 // and about 1.5 times where no two of the four are far; likewise for threads and
-// blocks.  (With one k for a whole column, the mean of four of its n <= 2^18
-// values, rstd of [300, 60000] values was off by up to 40000 steps of 2^-24 where
-// the first pixel was a thousand deviations off; it is now by 8, for 0.4 us more
-// at decoder size.)
+// blocks.  Measured on [300, 60000, 8] fp16: rstd is off by 5 steps of 2^-24, by
+// 8 with a first pixel a thousand deviations off, by 830 where three of the first
+// four values of one thread are 10^4 off and no others.  (With one k for a whole
+// column, the mean of four of its n <= 2^18 values, it was off by 40000 with the
+// first pixel a thousand deviations off.)
 #pragma once
 
 #include <string.h>
@@ -375,10 +375,10 @@ __device__ __forceinline__ int log_lanes_for(int n) {
 
 // log2 of the warps that share one of `n` groups: a block's eight among fewer
 // than eight groups.  The general kernels only ([8, 16383, 127] fp16 in one
-// group 32.4 us in place of 36.5): the plain ones have short sums, and sharing
-// costs them 2% at every size (backward [16, 112x112, 512] fp16 190 us in place
-// of 186, decoder size 26.1 in place of 25.5), more than their one kind of
-// shape that gains is worth ([8, 256, 2048] bf16 in one group 18.5 in place of 24).
+// group 29.7 us in place of 31.9): the plain ones have short sums, and sharing
+// costs them about 1% at most sizes (decoder size 25.6 us in place of 25.3,
+// backward [16, 112x112, 512] fp16 187.5 in place of 187.0) where shapes of one
+// group and few pixels would gain ([8, 256, 2048] bf16 18.8 in place of 24.5).
 __device__ __forceinline__ int log_warps_for(int n) { return n == 1 ? 3 : n == 2 ? 2 : n <= 4 ? 1 : 0; }
 
 __device__ __forceinline__ int wrap_group(const GnGeom &g, int gi) { return gi >= g.G ? gi - g.G : gi; }

@@ -553,7 +553,9 @@ def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="
     """Group norm of channels-last X[N, D.., C] (what conv_transpose_nhwc
     returns), then the activation (identity, relu, silu or gelu), then dropout
     with probability p (see dropout for seed, offset and rng): float32,
-    float16 or bfloat16, weight and bias [C] in X's dtype or float32.
+    float16 or bfloat16, weight and bias [C] in X's dtype or float32.  Inputs
+    that are not contiguous (a permuted channels-first X) are copied first.
+    ``out`` may not overlap an input.
 
     Returns Y, or (Y, mean, rstd) with ``return_stats``: mean and rstd are
     float32 [N, groups], what group_norm_nhwc_backward takes."""
