@@ -444,51 +444,13 @@ __device__ __forceinline__ void group_positions(const GnGeom &g, const Share &t,
     }
 }
 
-// Sums over the thread rows: ARRAYS arrays [by][bx * V], kThreads * V apart.
-// Every array's rows are cut into a few runs; run s is summed into row s, and
-// at(k, pos) adds the runs of array k.
-struct Columns {
-    const float *sums;
-    int width, apart, segs;
-    __device__ __forceinline__ float at(int k, int pos) const {
-        const float *a = sums + k * apart + pos;
-        float v = a[0];
-        for (int s = 1; s < segs; ++s) v += a[s * width];
-        return v;
-    }
-};
-template <int ARRAYS>
-__device__ __forceinline__ Columns column_sums(const GnGeom &g, float *sums) {
-    Columns c = {sums, g.bx * g.V, kThreads * g.V, 1};
-    while (c.segs * 2 * ARRAYS * c.width <= kThreads && c.segs * 4 <= g.by) c.segs *= 2;
-    __syncthreads();
-    const int runs = c.segs * c.width;   // of an array; consecutive threads take consecutive positions
-    if (g.by > 1)
-        for (int i = threadIdx.x; i < ARRAYS * runs; i += kThreads) {
-            int k = 0, j = i;
-#pragma unroll
-            for (int m = 1; m < ARRAYS; ++m)
-                if (j >= runs) {
-                    j -= runs;
-                    ++k;
-                }
-            float *a = sums + k * c.apart + j;   // row s, position pos of run s: this thread's own
-            const int stride = runs, rows = g.by * c.width - j;
-            float v = 0.f;
-#pragma unroll 8
-            for (int y = 0; y < rows; y += stride) v += a[y];
-            a[0] = v;
-        }
-    __syncthreads();
-    return c;
-}
-
 // ---- forward ----------------------------------------------------------------
 
 // Dynamic shared memory of the forward kernels.
 struct FwdShared {
-    float *nmean, *mul, *add;   // per position of the tile: a = (x + nmean) mul + add
-    float *sums;                // the threads' sums of x - k, of its square, and counts
+    float *nmean, *mul, *add;   // per position of the tile: a = (x + nmean) mul + add; nmean before that
+                                // what the columns' sums are about
+    float *sums;                // the threads' means, M2 and counts, then their columns' sums
     float4 *pushed;             // [2][cluster][groups]: the cluster's (count, mean, M2), taking turns by strip
     float2 *stat;               // (mean, rstd) of the groups
     int groups;
@@ -940,6 +902,38 @@ size_t backward_smem(const GnGeom &g) {
     return (size_t)g.bx * g.V * 20 + (size_t)kThreads * g.V * 8 + (size_t)groups_max(g) * (32 * g.cluster + 8);
 }
 
+// Sums over the thread rows of the two arrays [by][bx * V], kThreads * V apart,
+// of sh.sums: an array's rows are cut into a few runs, run s is summed into row
+// s, and at(k, pos) adds the runs of array k.
+struct Columns {
+    const float *sums;
+    int width, apart, segs;
+    __device__ __forceinline__ float at(int k, int pos) const {
+        const float *a = sums + k * apart + pos;
+        float v = a[0];
+        for (int s = 1; s < segs; ++s) v += a[s * width];
+        return v;
+    }
+};
+__device__ __forceinline__ Columns column_sums(const GnGeom &g, float *sums) {
+    Columns c = {sums, g.bx * g.V, kThreads * g.V, 1};
+    while (c.segs * 4 * c.width <= kThreads && c.segs * 4 <= g.by) c.segs *= 2;
+    __syncthreads();
+    const int runs = c.segs * c.width;   // of an array; consecutive threads take consecutive positions
+    if (g.by > 1)
+        for (int i = threadIdx.x; i < 2 * runs; i += kThreads) {
+            const int k = i >= runs ? 1 : 0, j = i - k * runs;
+            float *a = sums + k * c.apart + j;   // row s, position pos of run s: this thread's own
+            const int rows = g.by * c.width - j;
+            float v = 0.f;
+#pragma unroll 8
+            for (int y = 0; y < rows; y += runs) v += a[y];
+            a[0] = v;
+        }
+    __syncthreads();
+    return c;
+}
+
 // The coefficients of the tile's positions, and this thread's.
 template <int V>
 struct Coef {
@@ -1010,7 +1004,7 @@ __device__ __forceinline__ void block_sums(const GnGeom &g, const Params &p, con
             put_own<V>(sh.sums + kThreads * V, w);
         }
     }
-    const Columns cols = column_sums<2>(g, sh.sums);
+    const Columns cols = column_sums(g, sh.sums);
     if (p.chan) {
         float2 *out = p.chan + (t.n * g.chunks + blockIdx.x) * g.copies * g.C;
         if (!PLAIN && g.ctiles > 1) {   // the tile's own, copies apart
