@@ -410,7 +410,8 @@ def work(case):
         if case["way"] == "e4m3":
             forward += e * (1 - size) + 4 * rows * (-(-c // case["block"]) if case["block"] else 1)
         moved = {"backward": backward, "train": forward + backward}.get(case["way"], forward)
-        return {"bytes": moved + 8 * c, "flops": e * {"forward": 5, "e4m3": 8, "backward": 12, "train": 17}[case["way"]]}
+        ops = {"forward": 5, "e4m3": 8, "backward": 12, "train": 17}[case["way"]]
+        return {"bytes": moved + 8 * c, "flops": ops * e}
     if case["op"] == "rotary":
         pixels = case["n"] * math.prod(_dims(case["dims"]))
         e = pixels * case["heads"] * case["dim"]
@@ -419,7 +420,8 @@ def work(case):
     e = sum(_sizes(case))
     state = 16 if case["bits"] == 32 else 4 + 16 / BLOCK           # both states, read and written
     weight = 8 if case["dtype"] == "fp32" else 8 + size            # read and written; masters, and the 16-bit copy
-    return {"bytes": e * (state + weight + size * (2 if case["clip"] else 1)), "flops": e * (18 if case["bits"] == 32 else 45)}
+    return {"bytes": e * (state + weight + size * (2 if case["clip"] else 1)),
+            "flops": e * (18 if case["bits"] == 32 else 45)}
 
 
 # ---- the definition in 64 bits --------------------------------------------------------------------------------------
