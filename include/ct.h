@@ -313,6 +313,63 @@ CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const vo
                                         const void *rng, void *dx, void *dweight, void *dbias,
                                         void *workspace, void *stream);
 
+/* Root-mean-square norm of `rows` rows of C channels (pixels, tokens or heads,
+ * dense), of x or of x plus a residual:
+ *
+ *     h = x + residual,   rstd = (sum_c h^2 / C + eps)^-1/2,   y[c] = h[c] * rstd * weight[c].
+ *
+ * h is formed in fp32; `sum` gets it rounded to dtype (what the residual
+ * stream carries on), y and rstd come from the unrounded values.  Everything
+ * is computed in fp32 (the squares too: a row whose root mean square passes
+ * 1e19 has an rstd of 0) and rounded once.  dtype is x's, residual's, y's and
+ * sum's; param_dtype weight's and its gradient's, CT_F32 or dtype.
+ *
+ * e4m3 output: y is not rounded to dtype but held as codes and fp32 scales,
+ *     scale = max(max |y| / 448, 2^-126) of a block,   q = e4m3(y * (1 / scale)), to nearest even;
+ * a block is `block` neighbouring channels of a row (32, 64 or 128; the last
+ * one of a row may be shorter), or all C of them for 0.  q * scale is the
+ * value.  A block with a NaN or an infinity in it has a scale of NaN.
+ *
+ * Limits: 1 <= C <= 2^24 (CT_ERR_CHANNELS), rows * C <= 2^60. */
+typedef struct ct_rms_norm_desc {
+    int32_t dtype;         /* ct_dtype */
+    int32_t param_dtype;   /* CT_F32, or dtype */
+    int32_t block;         /* channels under one scale, 0: all of a row.  ct_rms_norm_e4m3 alone reads it */
+    int32_t reserved;      /* not read */
+    int64_t rows, C;
+    double eps;            /* >= 0 */
+} ct_rms_norm_desc;
+
+/* Bytes of device workspace (256-byte aligned) of a backward call that wants
+ * dweight; the forward calls need none.  Its contents need not be set before
+ * a call and mean nothing after it; calls that may run at the same time need
+ * one each. */
+CT_API ct_status ct_rms_norm_workspace_bytes(const ct_rms_norm_desc *desc, size_t *backward_bytes);
+
+/* Forward.  residual, weight (1), sum and rstd ([rows] fp32) may be NULL; sum
+ * needs a residual.  y may be x or residual, and sum too, each exactly; else
+ * no output may overlap another one or anything that the call reads.
+ * Asynchronous on `stream`. */
+CT_API ct_status ct_rms_norm(const ct_rms_norm_desc *desc, const void *x, const void *residual, const void *weight,
+                             void *y, void *sum, float *rstd, void *stream);
+
+/* Forward with e4m3 output: q [rows, C] (one byte each), scale [rows] or, with
+ * a block, [rows, ceil(C / block)].  The rest as ct_rms_norm; q and scale may
+ * overlap nothing that the call reads. */
+CT_API ct_status ct_rms_norm_e4m3(const ct_rms_norm_desc *desc, const void *x, const void *residual,
+                                  const void *weight, void *q, float *scale, void *sum, float *rstd, void *stream);
+
+/* Backward: dx, the gradient in x and in the residual alike, and dweight,
+ * summed over the rows; each NULL when it is not wanted.  x is what was normed
+ * (sum where there was a residual), rstd as the forward call gave it; dsum,
+ * the gradient that reaches `sum` on its own way, is added to dx and may be
+ * NULL.  With rows of 0 dweight is 0 and the other tensors are not read.
+ * Outputs may overlap neither each other nor anything that the call reads.
+ * The same call gives the same bits. */
+CT_API ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *dy, const void *x, const float *rstd,
+                                      const void *weight, const void *dsum, void *dx, void *dweight,
+                                      void *workspace, void *stream);
+
 /* Static, human-readable text for a status code. */
 CT_API const char *ct_status_string(ct_status status);
 

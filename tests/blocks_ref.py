@@ -1,0 +1,84 @@
+"""Plain fp64 forms of the root-mean-square norm, of rotary positions and of
+AdamW, for the tests: written from the definitions, sharing nothing with the
+library.  They run wherever their inputs lie.
+
+Rounding bounds: u = 2^-24 is half a step of fp32.  The library computes in
+fp32 and rounds once; CHAIN bounds the relative error of a sum against the sum
+of its terms' magnitudes in units of u (a thread's own terms, lanes, warps,
+rows of a block, parts, one after the other).
+"""
+
+import torch
+
+U = 2.0 ** -24
+CHAIN = 256
+HALF = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -126}
+LEAST_SCALE = 2.0 ** -126
+
+
+def check(got, want, bound, where):
+    """Elementwise |got - want| <= bound; NaN and infinities have to agree."""
+    got, want = got.double(), want.double()
+    assert got.shape == want.shape, "%s: shape %s, not %s" % (where, list(got.shape), list(want.shape))
+    err = (got - want).abs()
+    bad = ~(err <= bound) & ~((got == want) | (got.isnan() & want.isnan()))
+    assert not bad.any(), "%s: %d of %d outside, worst %.3g of its bound" % (
+        where, int(bad.sum()), bad.numel(), float((err / bound)[bad].nan_to_num(float("inf")).max()))
+
+
+# ---- root-mean-square norm ----------------------------------------------------
+
+def rms_forward(x, residual, weight, eps):
+    """fp64 -> y, h, rstd."""
+    h = x if residual is None else x + residual
+    rstd = 1 / torch.sqrt((h * h).mean(dim=-1) + eps)
+    return h * rstd[..., None] * weight, h, rstd
+
+
+def rms_bounds(y, h, rstd, dtype):
+    """(y, sum, rstd): the squares' sum is good to CHAIN u of itself, and half
+    of that enters rstd; a square root, a quotient, h, and two products lose
+    half a step each."""
+    return (1.01 * (HALF[dtype] + (CHAIN / 2 + 8) * U) * y.abs() + TINY[dtype],
+            1.01 * (HALF[dtype] + U) * h.abs() + TINY[dtype], (CHAIN / 2 + 6) * U * rstd)
+
+
+def rms_backward(dy, h, rstd, weight, dsum):
+    """fp64 -> dx, dweight."""
+    hat = h * rstd[..., None]
+    t = dy * weight
+    dx = rstd[..., None] * (t - hat * (t * hat).mean(dim=-1, keepdim=True))
+    if dsum is not None:
+        dx = dx + dsum
+    return dx, (dy * hat).sum(dim=tuple(range(dy.dim() - 1)))
+
+
+def rms_backward_bounds(dy, h, rstd, weight, dsum, dx, dw, dtype, pdtype):
+    hat = (h * rstd[..., None]).abs()
+    t = (dy * weight).abs()
+    e = rstd[..., None] * (6 * t + (CHAIN + 8) * hat * (t * hat).mean(dim=-1, keepdim=True))
+    if dsum is not None:
+        e = e + 2 * dsum.abs()
+    terms = (dy.abs() * hat).sum(dim=tuple(range(dy.dim() - 1)))
+    return (1.01 * (HALF[dtype] * dx.abs() + U * e) + TINY[dtype],
+            1.01 * (HALF[pdtype] * dw.abs() + (CHAIN + 4) * U * terms) + TINY[pdtype])
+
+
+def block_scales(y, block):
+    """The scales of y's blocks (0: whole rows), without their last axis then."""
+    c = y.shape[-1]
+    width = block or c
+    scale = torch.stack([y[..., k:k + width].abs().amax(dim=-1) for k in range(0, c, width)], dim=-1) / 448
+    return scale.clamp(min=LEAST_SCALE) if block else scale[..., 0].clamp(min=LEAST_SCALE)
+
+
+def spread_scales(scale, block, c):
+    """One scale for each of c channels."""
+    return scale.repeat_interleave(block, dim=-1)[..., :c] if block else scale[..., None].expand(*scale.shape, c)
+
+
+def e4m3_bound(v, steps=0.5):
+    """How far a code may lie from v: `steps` of the grid there, 2^-3 of the
+    power of two below v, 2^-9 at the least; and v's own error."""
+    return steps * torch.maximum(v.abs() * 2.0 ** -3, torch.full_like(v, 2.0 ** -9)) + (CHAIN + 16) * U * v.abs()

@@ -1,0 +1,130 @@
+"""Root-mean-square norm without a GPU: the plain forms against differences, and
+the refusals of the C entries and the binding."""
+
+import ctypes
+
+import pytest
+import torch
+
+import blocks_ref as ref
+from transposed_convolution_02_b200 import ct
+
+
+def differences(loss, leaves, grads, step=1e-6, tol=1e-6):
+    """Central differences of loss(*leaves) against grads, at some elements of each."""
+    for which, (t, gr) in enumerate(zip(leaves, grads)):
+        for i in range(0, t.numel(), max(1, t.numel() // 12)):
+            args = [v.clone() for v in leaves]
+            args[which].view(-1)[i] += step
+            hi = loss(*args)
+            args[which].view(-1)[i] -= 2 * step
+            # rounding of the difference: 1e-16 * |loss| / step
+            assert abs((hi - loss(*args)) / (2 * step) - float(gr.reshape(-1)[i])) < tol
+
+
+def test_rms_formulas_against_differences():
+    g = torch.Generator().manual_seed(5)
+    x, r, dy, dsum = (torch.randn(3, 4, 7, generator=g, dtype=torch.float64) for _ in range(4))
+    w = torch.randn(7, generator=g, dtype=torch.float64)
+
+    def loss(x, r, w):
+        y, h, _ = ref.rms_forward(x, r, w, 1e-3)
+        return float((y * dy).sum() + (h * dsum).sum())
+
+    _, h, rstd = ref.rms_forward(x, r, w, 1e-3)
+    dx, dw = ref.rms_backward(dy, h, rstd, w, dsum)
+    differences(loss, (x, r, w), (dx, dx, dw))
+
+
+def rms_desc(**over):
+    d = ct.ct_rms_norm_desc(1, 0, 0, 0, 6, 12, 1e-6)
+    for k, v in over.items():
+        setattr(d, k, v)
+    return d
+
+
+@pytest.mark.parametrize("over, status", [
+    ({}, 0), (dict(dtype=2), 0), (dict(param_dtype=1), 0), (dict(rows=0), 0), (dict(eps=0.0), 0),
+    (dict(block=5), 0), (dict(dtype=3), 3), (dict(dtype=-1), 3), (dict(param_dtype=2), 3),
+    (dict(dtype=0, param_dtype=1), 3), (dict(C=0), 1), (dict(C=-4), 1), (dict(C=(1 << 24) + 1), 1),
+    (dict(rows=-1), 4), (dict(rows=1 << 60), 4), (dict(rows=1 << 62), 4),
+    (dict(eps=-1e-6), 4), (dict(eps=float("nan")), 4), (dict(eps=float("inf")), 4)])
+def test_rms_desc_refusals(over, status):
+    b = ctypes.c_size_t()
+    assert ct.lib().ct_rms_norm_workspace_bytes(ctypes.byref(rms_desc(**over)), ctypes.byref(b)) == status
+    assert ct.lib().ct_rms_norm_workspace_bytes(None, ctypes.byref(b)) == 6
+    assert ct.lib().ct_rms_norm_workspace_bytes(ctypes.byref(rms_desc()), None) == 6
+
+
+def refused(fn, args, over, status):
+    v = list(args)
+    for k, x in over.items():
+        v[k] = x
+    return fn(*v) == status
+
+
+# an aligned address that is never followed: every call is refused before a launch
+A = 1 << 20
+
+
+def test_rms_call_refusals():
+    L = ct.lib()
+    d = ctypes.byref(rms_desc())
+    fwd = [d, A, A, A, A, A, A, None]
+    for over, status in [({0: None}, 6), ({1: None}, 6), ({4: None}, 6), ({2: None}, 6), ({1: A + 1}, 5),
+                         ({2: A + 1}, 5), ({3: A + 2}, 5), ({4: A + 1}, 5), ({5: A + 1}, 5), ({6: A + 2}, 5),
+                         ({0: ctypes.byref(rms_desc(dtype=7))}, 3), ({0: ctypes.byref(rms_desc(rows=0)), 1: None}, 0)]:
+        assert refused(L.ct_rms_norm, fwd, over, status), (over, status)
+    quant = [d, A, A, A, A + 1, A, A, A, None]      # codes are bytes: any address
+    for over, status in [({0: None}, 6), ({1: None}, 6), ({4: None}, 6), ({5: None}, 6), ({2: None}, 6),
+                         ({5: A + 2}, 5), ({6: A + 1}, 5), ({7: A + 1}, 5)] + \
+            [({0: ctypes.byref(rms_desc(block=b))}, 4) for b in (-32, 1, 16, 31, 33, 96, 256)]:
+        assert refused(L.ct_rms_norm_e4m3, quant, over, status), (over, status)
+    back = [d, A, A, A, A, A, A, A, A, None]
+    for over, status in [({0: None}, 6), ({1: None}, 6), ({2: None}, 6), ({3: None}, 6), ({8: None}, 8),
+                         ({8: A + 16}, 5), ({1: A + 1}, 5), ({2: A + 1}, 5), ({3: A + 2}, 5), ({4: A + 2}, 5),
+                         ({5: A + 1}, 5), ({6: A + 1}, 5), ({7: A + 2}, 5), ({6: None, 7: None}, 0)]:
+        assert refused(L.ct_rms_norm_backward, back, over, status), (over, status)
+    if not torch.cuda.is_available():
+        for fn, args in ((L.ct_rms_norm, fwd), (L.ct_rms_norm_e4m3, quant), (L.ct_rms_norm_backward, back)):
+            assert refused(fn, args, {}, 7)
+
+
+FLAT = torch.zeros(400)
+X, R, OUT = FLAT[:72].view(2, 3, 12), FLAT[80:152].view(2, 3, 12), FLAT[160:232].view(2, 3, 12)
+RSTD = FLAT[300:306].view(2, 3)
+
+
+@pytest.mark.parametrize("call, refusal", [
+    (lambda: ct.rms_norm_nhwc(X.double()), "float32"),
+    (lambda: ct.rms_norm_nhwc(X.int()), "float32"),
+    (lambda: ct.rms_norm_nhwc(torch.zeros(())), "shape"),
+    (lambda: ct.rms_norm_nhwc(torch.zeros(4, 0)), "shape"),
+    (lambda: ct.rms_norm_nhwc(X, FLAT[:11]), "weight"),
+    (lambda: ct.rms_norm_nhwc(X, FLAT[:12].half()), "weight"),
+    (lambda: ct.rms_norm_nhwc(X, FLAT[:12].view(1, 12)), "weight"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R[:1]), "residual"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R.half()), "residual"),
+    (lambda: ct.rms_norm_nhwc(X, sum_out=OUT), "residual"),
+    (lambda: ct.rms_norm_nhwc(X, out=OUT.half()), "out"),
+    (lambda: ct.rms_norm_nhwc(X, out=OUT.transpose(0, 1)), "out"),
+    (lambda: ct.rms_norm_nhwc(X, out=FLAT[4:76].view(2, 3, 12)), "overlaps"),
+    (lambda: ct.rms_norm_nhwc(X, FLAT[165:177], out=OUT), "overlaps"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R, sum_out=FLAT[84:156].view(2, 3, 12)), "overlaps"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R, out=X, sum_out=X), "overlap"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R, out=OUT, sum_out=FLAT[231:303].view(2, 3, 12)), "overlap"),
+    (lambda: ct.rms_norm_nhwc(X, residual=R, out=X, sum_out=R), "CUDA"),
+    (lambda: ct.rms_norm_nhwc(X, eps=-1.0), "CT_ERR_ATTR"),
+    (lambda: ct.rms_norm_nhwc_e4m3(X, block=16), "block"),
+    (lambda: ct.rms_norm_nhwc_e4m3(X, block=48.0), "block"),
+    (lambda: ct.rms_norm_nhwc_e4m3(X, sum_out=OUT), "residual"),
+    (lambda: ct.rms_norm_nhwc_e4m3(X, block=64), "CUDA"),
+    (lambda: ct.rms_norm_nhwc_backward(R[:1], X, RSTD), "dy"),
+    (lambda: ct.rms_norm_nhwc_backward(R, X, RSTD, dsum=R.half()), "dsum"),
+    (lambda: ct.rms_norm_nhwc_backward(R, X, RSTD.double()), "rstd"),
+    (lambda: ct.rms_norm_nhwc_backward(R, X, RSTD.view(6)), "rstd"),
+    (lambda: ct.rms_norm_nhwc_backward(R, X, RSTD, FLAT[:13]), "weight"),
+    (lambda: ct.rms_norm_nhwc_backward(R, X, RSTD, FLAT[:12]), "CUDA")])
+def test_rms_binding_refusals(call, refusal):
+    with pytest.raises((ValueError, ct.CtError), match=refusal):
+        call()

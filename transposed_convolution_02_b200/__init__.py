@@ -24,4 +24,7 @@ from .ct import (  # noqa: F401
     group_norm_nhwc,
     group_norm_nhwc_backward,
     make_desc,
+    rms_norm_nhwc,
+    rms_norm_nhwc_backward,
+    rms_norm_nhwc_e4m3,
 )

@@ -14,6 +14,7 @@
 
 #include "ct_internal.h"
 #include "group_norm.h"
+#include "rms_norm.h"
 
 using namespace ct;
 
@@ -280,6 +281,50 @@ ct_status norm_args(const ct_group_norm_desc *d, const GnGeom &g, const void *we
     return CT_OK;
 }
 
+// A root-mean-square norm's descriptor -> the sizes and types of its arguments.
+ct_status resolve_rms(const ct_rms_norm_desc *d, bool blocks, RmsArgs *a) {
+    if (!d) return CT_ERR_NULL;
+    if (!known_dtype(d->dtype)) return CT_ERR_DTYPE;
+    if (d->param_dtype != CT_F32 && d->param_dtype != d->dtype) return CT_ERR_DTYPE;
+    if (!(d->eps >= 0.0) || !isfinite(d->eps)) return CT_ERR_ATTR;
+    if (d->C < 1 || d->C > kRmsMaxC) return CT_ERR_CHANNELS;
+    if (d->rows < 0 || mul_capped(d->rows, d->C) < 0) return CT_ERR_ATTR;
+    if (blocks && d->block != 0 && d->block != 32 && d->block != 64 && d->block != 128) return CT_ERR_ATTR;
+    memset(a, 0, sizeof(*a));
+    a->dtype = d->dtype;
+    a->param_dtype = d->param_dtype;
+    a->rows = d->rows;
+    a->C = d->C;
+    a->eps = (float)d->eps;
+    a->block = blocks ? d->block : 0;
+    return CT_OK;
+}
+
+// Both forward calls: `scale` is set where y takes e4m3 codes.
+ct_status rms_call(const ct_rms_norm_desc *desc, bool codes, const void *x, const void *residual, const void *weight,
+                   void *y, float *scale, void *sum, float *rstd, void *stream) {
+    RmsArgs a;
+    ct_status st = resolve_rms(desc, codes, &a);
+    if (st != CT_OK) return st;
+    if (sum && !residual) return CT_ERR_NULL;
+    if (a.rows == 0) return CT_OK;
+    if (!x || !y || (codes && !scale)) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(a.dtype);
+    if (!aligned(x, eb) || !aligned(residual, eb) || !aligned(sum, eb) || (!codes && !aligned(y, eb)) ||
+        !aligned(weight, dtype_bytes(a.param_dtype)) || !aligned(rstd, 4) || !aligned(scale, 4))
+        return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.y = y;
+    a.sum = sum;
+    a.rstd = rstd;
+    a.scale = codes ? scale : nullptr;
+    return rms_forward(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -523,6 +568,53 @@ ct_status ct_dropout(int32_t dtype, int64_t n, const void *x, const void *residu
     st = check_device();
     if (st != CT_OK) return st;
     return dropout_run(dtype, x, residual, y, n, r, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_rms_norm_workspace_bytes(const ct_rms_norm_desc *desc, size_t *backward_bytes) {
+    if (!backward_bytes) return CT_ERR_NULL;
+    RmsArgs a;
+    ct_status st = resolve_rms(desc, false, &a);
+    if (st != CT_OK) return st;
+    *backward_bytes = (size_t)rms_parts(a.rows, a.C) * a.C * 4;
+    return CT_OK;
+}
+
+ct_status ct_rms_norm(const ct_rms_norm_desc *desc, const void *x, const void *residual, const void *weight, void *y,
+                      void *sum, float *rstd, void *stream) {
+    return rms_call(desc, false, x, residual, weight, y, nullptr, sum, rstd, stream);
+}
+
+ct_status ct_rms_norm_e4m3(const ct_rms_norm_desc *desc, const void *x, const void *residual, const void *weight,
+                           void *q, float *scale, void *sum, float *rstd, void *stream) {
+    return rms_call(desc, true, x, residual, weight, q, scale, sum, rstd, stream);
+}
+
+ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *dy, const void *x, const float *rstd,
+                               const void *weight, const void *dsum, void *dx, void *dweight, void *workspace,
+                               void *stream) {
+    RmsArgs a;
+    ct_status st = resolve_rms(desc, false, &a);
+    if (st != CT_OK) return st;
+    if (!dx && !dweight) return CT_OK;
+    if (a.rows == 0 && !dweight) return CT_OK;
+    if (a.rows > 0 && (!dy || !x || !rstd)) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(a.dtype), pb = dtype_bytes(a.param_dtype);
+    if (!aligned(dy, eb) || !aligned(x, eb) || !aligned(dsum, eb) || !aligned(dx, eb) || !aligned(rstd, 4) ||
+        !aligned(weight, pb) || !aligned(dweight, pb))
+        return CT_ERR_ALIGN;
+    if (dweight && !workspace) return CT_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    a.dy = dy;
+    a.x = x;
+    a.rstd_in = rstd;
+    a.weight = weight;
+    a.dsum = dsum;
+    a.dx = dx;
+    a.dweight = dweight;
+    a.ws = (float *)workspace;
+    return rms_backward(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ct_status ct_take_device_error(void *stream, int32_t *code) {

@@ -1,0 +1,8 @@
+#include "rms_norm_kernels.cuh"
+
+namespace ct {
+
+ct_status rms_forward_f16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st) { return forward_t<__half>(a, g, st); }
+ct_status rms_backward_f16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st) { return backward_t<__half>(a, g, st); }
+
+}  // namespace ct

@@ -1,0 +1,57 @@
+// Root-mean-square norm: arguments and geometry, shared by the C entry points
+// and the kernels.
+//
+// A row (a pixel, a token, a head) of C channels belongs to `tpr` threads, a
+// power of two from 1 to 512; a thread holds K vectors of E elements of it in
+// registers, so that every tensor is read once.  E is a vector of 16 bytes
+// where all rows start on one, else a single element.  Rows longer than 512
+// threads hold are walked twice by kernels of their own.
+#pragma once
+
+#include <stdint.h>
+
+#include "ct_internal.h"
+
+namespace ct {
+
+struct RmsArgs {
+    int dtype, param_dtype;      // ct_dtype
+    int64_t rows;
+    int64_t C;
+    float eps;
+    int block;                   // channels under one scale; 0: all of a row. (e4m3 only)
+    const void *x, *residual, *weight;
+    void *y, *sum;               // y: of x's type, or e4m3 codes where `scale` is set
+    float *rstd, *scale;
+    const void *dy, *dsum;       // backward; x is then what was normed
+    const float *rstd_in;
+    void *dx, *dweight;
+    float *ws;
+};
+
+struct RmsGeom {
+    int vec;        // 16-byte vectors, else single elements
+    int K;          // vectors of a row per thread; 0: the row is walked
+    int tpr;        // threads per row
+    int threads;    // per block
+    int64_t blocks;
+};
+
+constexpr int64_t kRmsMaxC = int64_t(1) << 24;
+
+// Where the pointers of a call allow vectors.  The workspace does not depend
+// on it: rms_parts is the same for both.
+RmsGeom rms_forward_geom(const RmsArgs &a, bool aligned);
+RmsGeom rms_backward_geom(const RmsArgs &a, bool aligned);
+int64_t rms_parts(int64_t rows, int64_t C);     // partial sums of dweight: rows of C floats in the workspace
+
+ct_status rms_forward(const RmsArgs &a, cudaStream_t st);
+ct_status rms_backward(const RmsArgs &a, cudaStream_t st);
+ct_status rms_forward_f32(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+ct_status rms_forward_f16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+ct_status rms_forward_bf16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+ct_status rms_backward_f32(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+ct_status rms_backward_f16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+ct_status rms_backward_bf16(const RmsArgs &a, const RmsGeom &g, cudaStream_t st);
+
+}  // namespace ct

@@ -14,6 +14,7 @@ weight [C_in, K.., O/groups], padding as (lo, hi) per spatial dim).
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -39,7 +40,8 @@ EXPORTED = ["ct_output_shape", "ct_plan", "ct_plan_kernel", "ct_plan_launches",
             "ct_workspace_bytes", "ct_prepack_weights", "ct_run", "ct_run_parts",
             "ct_run_noalloc", "ct_plan_destroy", "ct_status_string", "ct_take_device_error",
             "ct_selftest_wait_timeout", "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
-            "ct_group_norm_workspace_bytes"]
+            "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
+            "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes"]
 
 
 class CtError(RuntimeError):
@@ -67,6 +69,12 @@ class ct_group_norm_desc(ctypes.Structure):
                 ("activation", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("N", ctypes.c_int64), ("S", ctypes.c_int64), ("C", ctypes.c_int64),
                 ("groups", ctypes.c_int64), ("eps", ctypes.c_double)]
+
+
+class ct_rms_norm_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("C", ctypes.c_int64), ("eps", ctypes.c_double)]
 
 
 _lib = None
@@ -104,13 +112,19 @@ def lib():
         L.ct_group_norm_workspace_bytes.argtypes = [gp, szp, szp]
         L.ct_group_norm.argtypes = [gp, P, P, P, f64, u64, u64, P, P, P, P, P, P]
         L.ct_group_norm_backward.argtypes = [gp, P, P, P, P, P, P, f64, u64, u64, P, P, P, P, P, P]
+        rp = ctypes.POINTER(ct_rms_norm_desc)
+        L.ct_rms_norm_workspace_bytes.argtypes = [rp, szp]
+        L.ct_rms_norm.argtypes = [rp, P, P, P, P, P, P, P]
+        L.ct_rms_norm_e4m3.argtypes = [rp, P, P, P, P, P, P, P, P]
+        L.ct_rms_norm_backward.argtypes = [rp, P, P, P, P, P, P, P, P, P]
         L.ct_status_string.argtypes = [ctypes.c_int]
         L.ct_status_string.restype = ctypes.c_char_p
         for name in ("ct_output_shape", "ct_plan", "ct_plan_launches", "ct_prepacked_weight_bytes",
                      "ct_workspace_bytes", "ct_prepack_weights", "ct_run", "ct_run_parts",
                      "ct_run_noalloc", "ct_take_device_error", "ct_selftest_wait_timeout",
                      "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
-                     "ct_group_norm_workspace_bytes"):
+                     "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
+                     "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -659,3 +673,171 @@ def dropout_backward(dy, p, *, seed=0, offset=0, rng=None, out=None, stream=None
     """The gradient of dropout in X at dy, for the p, seed, offset and rng of
     the forward call (the residual's gradient is dy itself)."""
     return dropout(dy, p, seed=seed, offset=offset, rng=rng, out=out, stream=stream)
+
+
+# ---- root-mean-square norm ----------------------------------------------------
+
+class _Rms:
+    """A root-mean-square norm's descriptor and workspace size."""
+
+    def __init__(self, shape, dtype, param_dtype, block, eps):
+        block = int(block)
+        self.rows_shape, self.c = shape[:-1], shape[-1]
+        self.scale_shape = self.rows_shape + (-(-self.c // block),) if block else self.rows_shape
+        self.desc = ct_rms_norm_desc(NORM_DTYPE[dtype], NORM_DTYPE[param_dtype], block, 0,
+                                     math.prod(self.rows_shape), self.c, eps)
+        b = ctypes.c_size_t()
+        st = lib().ct_rms_norm_workspace_bytes(ctypes.byref(self.desc), ctypes.byref(b))
+        if st != CT_OK:
+            raise CtError(st, "ct_rms_norm_workspace_bytes")
+        self.backward_bytes = b.value
+
+
+_RMS = {}
+
+
+def check_rms(x, weight, block):
+    """Refuse arguments that the root-mean-square norm cannot take."""
+    if x.dtype not in NORM_DTYPE:
+        raise ValueError("X must be float32, float16 or bfloat16, not %s" % x.dtype)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("X must be [.., C] with C >= 1, it has shape %s" % list(x.shape))
+    if block not in (0, 32, 64, 128):
+        raise ValueError("block must be None, 32, 64 or 128, not %r" % (block,))
+    if weight is not None:
+        if weight.dtype != torch.float32 and weight.dtype != x.dtype:
+            raise ValueError("weight must be float32 or X's %s, not %s" % (x.dtype, weight.dtype))
+        if weight.dim() != 1 or weight.numel() != x.shape[-1] or weight.device != x.device:
+            raise ValueError("weight must have shape [%d] on %s" % (x.shape[-1], x.device))
+
+
+def _rms_of(x, weight, block, eps):
+    """The checked arguments' _Rms (made once per size and type)."""
+    pd = torch.float32 if weight is None else weight.dtype
+    key = (x.shape, x.dtype, pd, block, eps)
+    try:
+        r = _RMS[key]
+    except (KeyError, TypeError):
+        check_rms(x, weight, block)
+        r = _Rms(tuple(x.shape), x.dtype, pd, block, float(eps))
+        if len(_RMS) >= 1024:
+            _RMS.clear()
+        _RMS[key] = r
+        return r
+    if weight is not None and (weight.dim() != 1 or weight.numel() != r.c or weight.device != x.device):
+        check_rms(x, weight, block)
+    return r
+
+
+def _rms_inputs(x, weight, residual, outs):
+    """Checks of both forward calls; `outs` may be X or the residual."""
+    if residual is not None:
+        check_like(residual, "residual", x)
+    for t in outs:
+        if t is not None:
+            check_out(t, x, (x, residual), in_place=True)
+            check_out(t, x, (weight,))
+    if len(outs) == 2 and outs[0] is not None and outs[1] is not None and _overlap(*outs):
+        raise ValueError("out and sum_out overlap")
+    _check_cuda(x, weight, residual)
+
+
+def rms_norm_nhwc(x, weight=None, *, eps=1e-6, residual=None, out=None, sum_out=None, return_rstd=False, stream=None):
+    """Root-mean-square norm of the pixels (rows of C channels) of
+    channels-last X[.., C], of X + residual where a residual is given: float32,
+    float16 or bfloat16, weight [C] in X's dtype or float32.  Tensors that are
+    not contiguous are copied first.  ``out`` and ``sum_out`` may each be X or
+    the residual, but not overlap one another.
+
+    Returns Y; with a residual (Y, sum), sum being X + residual rounded (Y comes
+    from the unrounded sum); with ``return_rstd`` also rstd, float32 [..],
+    which rms_norm_nhwc_backward takes."""
+    r = _rms_of(x, weight, 0, eps)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out needs a residual")
+    _rms_inputs(x, weight, residual, (out, sum_out))
+
+    def call(raw):
+        xc = x.contiguous()
+        w = None if weight is None else weight.contiguous()
+        h = s = None
+        if residual is not None:
+            h = residual.contiguous()
+            s = torch.empty_like(xc) if sum_out is None else sum_out
+        y = torch.empty_like(xc) if out is None else out
+        rstd = xc.new_empty(r.rows_shape, dtype=torch.float32) if return_rstd else None
+        st = lib().ct_rms_norm(r.desc, xc.data_ptr(), _addr(h), _addr(w), y.data_ptr(), _addr(s), _addr(rstd), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_rms_norm")
+        if residual is None:
+            return (y, rstd) if return_rstd else y
+        return (y, s, rstd) if return_rstd else (y, s)
+
+    return _run_on(call, x, stream)
+
+
+def rms_norm_nhwc_e4m3(x, weight=None, *, block=None, eps=1e-6, residual=None, sum_out=None, return_rstd=False,
+                       stream=None):
+    """rms_norm_nhwc with its output in 8 bits for a matrix product that takes
+    them: q (float8_e4m3fn, X's shape) and scale (float32), q * scale being the
+    value.  A scale serves a pixel (scale [..]) or ``block`` of its channels,
+    32, 64 or 128 (scale [.., ceil(C / block)]), and is the largest magnitude
+    there / 448.  A block with a NaN or an infinity in it has a NaN scale.
+
+    Returns (q, scale), then sum where there is a residual and rstd with
+    ``return_rstd``, as rms_norm_nhwc does."""
+    r = _rms_of(x, weight, 0 if block is None else block, eps)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out needs a residual")
+    _rms_inputs(x, weight, residual, (sum_out,))
+
+    def call(raw):
+        xc = x.contiguous()
+        w = None if weight is None else weight.contiguous()
+        h = s = None
+        if residual is not None:
+            h = residual.contiguous()
+            s = torch.empty_like(xc) if sum_out is None else sum_out
+        q = xc.new_empty(xc.shape, dtype=torch.float8_e4m3fn)
+        scale = xc.new_empty(r.scale_shape, dtype=torch.float32)
+        rstd = xc.new_empty(r.rows_shape, dtype=torch.float32) if return_rstd else None
+        st = lib().ct_rms_norm_e4m3(r.desc, xc.data_ptr(), _addr(h), _addr(w), q.data_ptr(), scale.data_ptr(),
+                                    _addr(s), _addr(rstd), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_rms_norm_e4m3")
+        out = (q, scale) if residual is None else (q, scale, s)
+        return out + (rstd,) if return_rstd else out
+
+    return _run_on(call, x, stream)
+
+
+def rms_norm_nhwc_backward(dy, x, rstd, weight=None, *, dsum=None, need_x_grad=True, stream=None):
+    """Gradients (dx, dweight) of rms_norm_nhwc at dy.  X is what was normed
+    (the returned sum where there was a residual), rstd as the forward call
+    gave it.  dx is the gradient in X and in the residual alike; ``dsum``, the
+    gradient that reaches the sum on its own way, is added to it.  None for dx
+    without ``need_x_grad``, and for the gradient of a weight that is None."""
+    r = _rms_of(x, weight, 0, 0.0)
+    check_like(dy, "dy", x)
+    if dsum is not None:
+        check_like(dsum, "dsum", x)
+    if rstd.dtype != torch.float32 or rstd.shape != r.rows_shape or rstd.device != x.device:
+        raise ValueError("rstd must be a float32 tensor of shape %s on %s" % (list(r.rows_shape), x.device))
+    _check_cuda(x, dy, rstd, weight, dsum)
+
+    def call(raw):
+        xc, dyc, rs = x.contiguous(), dy.contiguous(), rstd.contiguous()
+        w = None if weight is None else weight.contiguous()
+        d = None if dsum is None else dsum.contiguous()
+        dx = torch.empty_like(xc) if need_x_grad else None
+        dweight = ws = None
+        if w is not None:
+            dweight = torch.empty_like(w)
+            ws = xc.new_empty((r.backward_bytes,), dtype=torch.uint8)
+        st = lib().ct_rms_norm_backward(r.desc, dyc.data_ptr(), xc.data_ptr(), rs.data_ptr(), _addr(w), _addr(d),
+                                        _addr(dx), _addr(dweight), _addr(ws), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_rms_norm_backward")
+        return dx, dweight
+
+    return _run_on(call, x, stream)
