@@ -370,6 +370,55 @@ CT_API ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *
                                       const void *weight, const void *dsum, void *dx, void *dweight,
                                       void *workspace, void *stream);
 
+/* Rotary positions of channels-last heads x[N, S, heads, dim], S pixels on 1
+ * to 3 axes.  Of each head the first sum(sections) elements are rotated in
+ * pairs, sections[a] of them (an even number) by the position on axis a; the
+ * rest stay as they are.  Pair i (of the first sum(sections) / 2, those of
+ * axis 0 first) is elements 2i and 2i + 1 (CT_PAIRS_ADJACENT) or i and
+ * i + sum(sections) / 2 (CT_PAIRS_HALVES); the j-th pair of axis a turns by
+ *
+ *     t = position * base^(-2 j / sections[a]),   (u, v) -> (u cos t - v sin t, u sin t + v cos t).
+ *
+ * Angles are formed in 64 bits, the rotation in fp32, rounded once.  The
+ * gradient in x is the inverse rotation of dy (`inverse`: by -t). */
+typedef enum ct_pairs { CT_PAIRS_ADJACENT = 0, CT_PAIRS_HALVES = 1 } ct_pairs;
+
+/* Positions: the pixels' indices on the grid, or numbers [S, axes] on the
+ * device, one such array for every image or one for all. */
+typedef enum ct_position_type {
+    CT_POSITION_GRID = 0,
+    CT_POSITION_I32 = 1,
+    CT_POSITION_I64 = 2,
+    CT_POSITION_F32 = 3
+} ct_position_type;
+
+/* Strides are in elements, a head's own elements are neighbours.  x may
+ * repeat (strides of 0); y's elements must be apart.  Limits: N, heads, dim
+ * and the grid's sizes in [0, 2^30], dim >= 1, sum(sections) <= dim and <=
+ * 512, each section >= 0 and even (CT_ERR_CHANNELS), 1 to 3 axes
+ * (CT_ERR_SPAN), base > 0 and finite, at most 2^60 elements, and no stride
+ * past 2^60 / 4 in magnitude; y's not negative (CT_ERR_ATTR). */
+typedef struct ct_rotary_desc {
+    int32_t dtype;          /* ct_dtype */
+    int32_t axes;           /* 1..3 */
+    int32_t pairs;          /* ct_pairs */
+    int32_t inverse;        /* 0, or 1: rotate by -t */
+    int32_t position_type;  /* ct_position_type */
+    int32_t position_images;/* 1: positions [N, S, axes]; 0: [S, axes] for every image */
+    int64_t N;
+    int64_t grid[3];        /* pixels along each axis, S their product (given positions too) */
+    int64_t heads, dim;
+    int64_t sections[3];
+    int64_t x_strides[3];   /* image, pixel, head */
+    int64_t y_strides[3];
+    double base;
+} ct_rotary_desc;
+
+/* y = rotated x.  y may be x with the same strides, else it may overlap
+ * nothing that the call reads.  positions is NULL for CT_POSITION_GRID.
+ * Asynchronous on `stream`. */
+CT_API ct_status ct_rotary(const ct_rotary_desc *desc, const void *x, const void *positions, void *y, void *stream);
+
 /* Static, human-readable text for a status code. */
 CT_API const char *ct_status_string(ct_status status);
 

@@ -82,3 +82,41 @@ def e4m3_bound(v, steps=0.5):
     """How far a code may lie from v: `steps` of the grid there, 2^-3 of the
     power of two below v, 2^-9 at the least; and v's own error."""
     return steps * torch.maximum(v.abs() * 2.0 ** -3, torch.full_like(v, 2.0 ** -9)) + (CHAIN + 16) * U * v.abs()
+
+
+# ---- rotary positions ---------------------------------------------------------
+
+def rotary_angles(at, sections, base):
+    """Positions [.., axes] in fp64 -> angles [.., pairs]."""
+    freq = [base ** (-torch.arange(0, d, 2, dtype=torch.float64, device=at.device) / d) for d in sections]
+    return torch.cat([at[..., a, None] * f for a, f in enumerate(freq)], dim=-1)
+
+
+def grid_positions(dims, device="cpu"):
+    return torch.stack(torch.meshgrid(*[torch.arange(d, device=device, dtype=torch.float64) for d in dims],
+                                      indexing="ij"), dim=-1)
+
+
+def rotary(x, angles, pairs):
+    """x [.., heads, dim] in fp64, angles [.., pairs]."""
+    half = angles.shape[-1]
+    c, s = torch.cos(angles)[..., None, :], torch.sin(angles)[..., None, :]
+    i = torch.arange(half, device=x.device)
+    i, k = (i, i + half) if pairs == "halves" else (2 * i, 2 * i + 1)
+    y = x.clone()
+    y[..., i], y[..., k] = x[..., i] * c - x[..., k] * s, x[..., i] * s + x[..., k] * c
+    return y
+
+
+def rotary_bound(x, y, angles, pairs, dtype):
+    """The angle is good to 2^-52 of itself (the frequency, the position's
+    product), and its fraction of half a turn to half a step of fp32; sincospi
+    to 4 steps; two products and a sum lose half a step of the terms each."""
+    half = angles.shape[-1]
+    off = (angles.abs() * 2.0 ** -51 + 12 * U)[..., None, :]
+    i = torch.arange(half, device=x.device)
+    i, k = (i, i + half) if pairs == "halves" else (2 * i, 2 * i + 1)
+    e = torch.zeros_like(x)
+    both = (x[..., i].abs() + x[..., k].abs()) * off
+    e[..., i], e[..., k] = both, both
+    return 1.01 * (HALF[dtype] * y.abs() + e) + torch.where(e > 0, TINY[dtype], 0.0)

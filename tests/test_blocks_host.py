@@ -128,3 +128,106 @@ RSTD = FLAT[300:306].view(2, 3)
 def test_rms_binding_refusals(call, refusal):
     with pytest.raises((ValueError, ct.CtError), match=refusal):
         call()
+
+
+# ---- rotary positions ---------------------------------------------------------
+
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+def test_rotary_formula(pairs):
+    """Turns keep lengths, add up, and the gradient is the turn back."""
+    g = torch.Generator().manual_seed(6)
+    x, dy = (torch.randn(2, 3, 4, 5, 9, generator=g, dtype=torch.float64) for _ in range(2))
+    angles = ref.rotary_angles(ref.grid_positions([3, 4]), [6, 2], 100.0)
+    y = ref.rotary(x, angles, pairs)
+    assert torch.allclose((y * y).sum(-1), (x * x).sum(-1)) and torch.equal(y[..., 8], x[..., 8])
+    assert torch.allclose(ref.rotary(y, angles, pairs), ref.rotary(x, 2 * angles, pairs))
+    differences(lambda v: float((ref.rotary(v, angles, pairs) * dy).sum()), (x,), (ref.rotary(dy, -angles, pairs),))
+    i, k = (0, 1) if pairs == "adjacent" else (0, 4)         # a turn by hand: pixel (2, 3), axis 0's first pair
+    assert abs(float(y[1, 2, 3, 4, i]) - float(x[1, 2, 3, 4, i] * torch.cos(torch.tensor(2.0, dtype=torch.float64))
+                                              - x[1, 2, 3, 4, k] * torch.sin(torch.tensor(2.0, dtype=torch.float64)))) < 1e-12
+
+
+def rotary_desc(**over):
+    d = ct.ct_rotary_desc(1, 2, 0, 0, 0, 0, 2)
+    d.grid[:] = [3, 4, 0]
+    d.heads, d.dim, d.base = 5, 16, 10000.0
+    d.sections[:] = [4, 8, 0]
+    d.x_strides[:] = d.y_strides[:] = [960, 80, 16]
+    for k, v in over.items():
+        if isinstance(v, list):
+            getattr(d, k)[:] = v
+        else:
+            setattr(d, k, v)
+    return d
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(N=0), 0), (dict(heads=0), 0), (dict(grid=[0, 4, 0]), 0), (dict(dtype=3), 3), (dict(axes=0), 2),
+    (dict(axes=4), 2), (dict(pairs=2), 4), (dict(inverse=2), 4), (dict(position_type=4), 4), (dict(position_images=2), 4),
+    (dict(base=0.0), 4), (dict(base=-1.0), 4), (dict(base=float("nan")), 4), (dict(base=float("inf")), 4),
+    (dict(N=-1), 4), (dict(heads=-1), 4), (dict(dim=0), 4), (dict(grid=[3, -1, 0]), 4), (dict(N=1 << 31), 4),
+    (dict(N=1 << 30, grid=[1 << 30, 1 << 30, 0]), 4), (dict(sections=[3, 4, 0]), 1), (dict(sections=[-2, 4, 0]), 1),
+    (dict(sections=[10, 8, 0]), 1), (dict(dim=600, sections=[500, 14, 0]), 1), (dict(sections=[1 << 40, 8, 0]), 1),
+    (dict(x_strides=[1 << 59, 80, 16]), 4), (dict(x_strides=[-(1 << 58), 80, 16]), 4), (dict(y_strides=[960, 80, -16]), 4),
+    (dict(y_strides=[960, 80, 15]), 4), (dict(y_strides=[960, 79, 16]), 4), (dict(y_strides=[959, 80, 16]), 4),
+    (dict(y_strides=[960, 0, 16]), 4), (dict(y_strides=[0, 80, 16]), 4)])
+def test_rotary_desc_refusals(over, status):
+    assert ct.lib().ct_rotary(ctypes.byref(rotary_desc(**over)), A, None, A, None) == status
+
+
+def test_rotary_call_refusals():
+    L = ct.lib()
+    d = ctypes.byref(rotary_desc())
+    given = ctypes.byref(rotary_desc(position_type=2))
+    for args, status in [((None, A, None, A), 6), ((d, None, None, A), 6), ((d, A, None, None), 6),
+                         ((given, A, None, A), 6), ((given, A, A + 4, A), 5), ((d, A + 1, None, A), 5),
+                         ((d, A, None, A + 1), 5)]:
+        assert L.ct_rotary(*args, None) == status
+    if not torch.cuda.is_available():
+        for over in ({}, dict(x_strides=[0, 0, 0]), dict(y_strides=[960, 16, 192]), dict(y_strides=[16, 32, 384]),
+                     dict(N=1, y_strides=[0, 80, 16]), dict(sections=[0, 0, 0])):
+            assert L.ct_rotary(ctypes.byref(rotary_desc(**over)), A, None, A, None) == 7
+
+
+HEADS = torch.zeros(2, 3, 4, 5, 16)
+AT = torch.zeros(3, 4, 2)
+
+
+@pytest.mark.parametrize("call, refusal", [
+    (lambda: ct.rotary_nhwc(HEADS.double(), [4, 8]), "float32"),
+    (lambda: ct.rotary_nhwc(HEADS, []), "axes"),
+    (lambda: ct.rotary_nhwc(HEADS, [2, 2, 2, 2]), "axes"),
+    (lambda: ct.rotary_nhwc(HEADS, [3, 8]), "even"),
+    (lambda: ct.rotary_nhwc(HEADS, [2.5, 8]), "even"),
+    (lambda: ct.rotary_nhwc(HEADS, [-2, 8]), "even"),
+    (lambda: ct.rotary_nhwc(HEADS, [10, 8]), "fit"),
+    (lambda: ct.rotary_nhwc(torch.zeros(1, 1, 1, 600), [514]), "fit"),
+    (lambda: ct.rotary_nhwc(HEADS, [4]), "positions"),
+    (lambda: ct.rotary_nhwc(HEADS[0, 0], [4, 8]), "shape"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], pairs="even"), "pairs"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], base=0), "base"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], base=float("nan")), "base"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], positions=AT.double()), "positions"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], positions=AT[:2]), "positions"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], positions=AT[..., :1]), "positions"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], out=HEADS[:1]), "out"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], out=torch.zeros(2, 3, 4, 16, 5).transpose(3, 4)), "neighbours"),
+    (lambda: ct.rotary_nhwc(HEADS[:1], [4, 8], out=HEADS.view(-1)[16:976].view(1, 3, 4, 5, 16)), "overlaps"),
+    (lambda: ct.rotary_nhwc(HEADS, [4, 8], out=HEADS), "CUDA"),
+    (lambda: ct.rotary_nhwc_backward(HEADS, [4, 8], positions=AT, out=HEADS), "CUDA")])
+def test_rotary_binding_refusals(call, refusal):
+    with pytest.raises(ValueError, match=refusal):
+        call()
+
+
+def test_pixel_strides():
+    """Pixels one stride apart are found in slices and permuted layouts."""
+    def of(t):
+        return ct._head_strides(t.shape, t.stride())
+    qkv = torch.zeros(2, 3, 4, 15, 16)
+    assert of(qkv) == (2880, 240, 16) and of(qkv[..., 5:10, :]) == (2880, 240, 16)
+    assert of(qkv[:, :, ::2]) == (2880, 480, 16)           # rows of pixels that go on at the same stride
+    assert of(qkv[:, :, :3]) is None and of(qkv[:, ::2]) is None and of(qkv[..., ::2]) is None
+    assert of(qkv[:, :1, :3]) == (2880, 240, 16) and of(qkv[:, :, :1]) == (2880, 960, 16)
+    assert of(torch.zeros(2, 5, 3, 4, 16).permute(0, 2, 3, 1, 4)) == (960, 16, 192)
+    assert of(torch.zeros(2, 1, 5, 16)) == (80, 0, 16)

@@ -27,4 +27,6 @@ from .ct import (  # noqa: F401
     rms_norm_nhwc,
     rms_norm_nhwc_backward,
     rms_norm_nhwc_e4m3,
+    rotary_nhwc,
+    rotary_nhwc_backward,
 )

@@ -15,6 +15,7 @@
 #include "ct_internal.h"
 #include "group_norm.h"
 #include "rms_norm.h"
+#include "rotary.h"
 
 using namespace ct;
 
@@ -325,6 +326,74 @@ ct_status rms_call(const ct_rms_norm_desc *desc, bool codes, const void *x, cons
     return rms_forward(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// Whether elements at these strides, runs of `run` of them, lie apart: in some
+// order each dimension steps over all that the ones before it span.
+bool lie_apart(const int64_t *sizes, const int64_t *strides, int64_t run) {
+    bool used[3] = {};
+    int64_t span = run;
+    for (int step = 0; step < 3; ++step) {
+        int least = -1;
+        for (int a = 0; a < 3; ++a)
+            if (!used[a] && (least < 0 || strides[a] < strides[least])) least = a;
+        used[least] = true;
+        if (sizes[least] < 2) continue;
+        if (strides[least] < span) return false;
+        span += (sizes[least] - 1) * strides[least];
+    }
+    return true;
+}
+
+constexpr int64_t kMaxStride = kMaxElems / 4;
+
+ct_status resolve_rotary(const ct_rotary_desc *d, RotaryParams *p) {
+    if (!d) return CT_ERR_NULL;
+    if (!known_dtype(d->dtype)) return CT_ERR_DTYPE;
+    if (d->axes < 1 || d->axes > 3) return CT_ERR_SPAN;
+    if (d->pairs != CT_PAIRS_ADJACENT && d->pairs != CT_PAIRS_HALVES) return CT_ERR_ATTR;
+    if (d->inverse != 0 && d->inverse != 1) return CT_ERR_ATTR;
+    if (d->position_type < CT_POSITION_GRID || d->position_type > CT_POSITION_F32) return CT_ERR_ATTR;
+    if (d->position_images != 0 && d->position_images != 1) return CT_ERR_ATTR;
+    if (!(d->base > 0.0) || !isfinite(d->base)) return CT_ERR_ATTR;
+    memset(p, 0, sizeof(*p));
+    if (d->N < 0 || d->N > kMaxDim || d->heads < 0 || d->heads > kMaxDim || d->dim < 1 || d->dim > kMaxDim)
+        return CT_ERR_ATTR;
+    p->N = d->N;
+    p->H = d->heads;
+    p->D = d->dim;
+    p->axes = d->axes;
+    p->S = 1;
+    for (int a = 0; a < d->axes; ++a) {
+        if (d->grid[a] < 0 || d->grid[a] > kMaxDim) return CT_ERR_ATTR;
+        p->grid[a] = d->grid[a];
+        p->S = mul_capped(p->S, d->grid[a]);
+    }
+    if (mul_capped(mul_capped(mul_capped(p->N, p->S), p->H), p->D) < 0) return CT_ERR_ATTR;
+    int64_t rot = 0;
+    for (int a = 0; a < d->axes; ++a) {
+        if (d->sections[a] < 0 || d->sections[a] % 2 != 0 || d->sections[a] > 2 * kRotaryMaxPairs) return CT_ERR_CHANNELS;
+        p->first[a] = (int32_t)(rot / 2);
+        rot += d->sections[a];
+    }
+    if (rot > p->D || rot > 2 * kRotaryMaxPairs) return CT_ERR_CHANNELS;
+    p->rot = (int32_t)rot;
+    // the powers of an axis' ratio one after the other, in 64 bits of mantissa:
+    // 255 products lose 2^-56 (a pow for each would take 2 us of a call)
+    for (int a = 0; a < d->axes; ++a) {
+        const long double ratio = powl((long double)d->base, -2.0L / (long double)d->sections[a]);
+        long double f = 1.0L / 6.283185307179586476925286766559L;
+        for (int64_t j = 0; j < d->sections[a] / 2; ++j, f *= ratio) p->turns[p->first[a] + j] = (double)f;
+    }
+    for (int a = 0; a < 3; ++a) {
+        p->xs[a] = d->x_strides[a];
+        p->ys[a] = d->y_strides[a];
+        if (p->xs[a] > kMaxStride || p->xs[a] < -kMaxStride || p->ys[a] > kMaxStride || p->ys[a] < 0) return CT_ERR_ATTR;
+    }
+    p->pos_image = d->position_images ? p->S * p->axes : 0;
+    p->pos_type = d->position_type;
+    p->sign = d->inverse ? -1.f : 1.f;
+    return CT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -615,6 +684,29 @@ ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *dy, con
     a.dweight = dweight;
     a.ws = (float *)workspace;
     return rms_backward(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_rotary(const ct_rotary_desc *desc, const void *x, const void *positions, void *y, void *stream) {
+    RotaryParams p;
+    ct_status st = resolve_rotary(desc, &p);
+    if (st != CT_OK) return st;
+    if (p.N * p.S * p.H == 0) return CT_OK;
+    const int64_t sizes[3] = {p.N, p.S, p.H};
+    for (int a = 0; a < 3; ++a) {      // no offset leaves 64 bits, in bytes either
+        const int64_t most = kMaxElems / 4 / sizes[a];
+        if (p.xs[a] > most || p.xs[a] < -most || p.ys[a] > most) return CT_ERR_ATTR;
+    }
+    if (!lie_apart(sizes, p.ys, p.D)) return CT_ERR_ATTR;
+    if (!x || !y || (p.pos_type != CT_POSITION_GRID && !positions)) return CT_ERR_NULL;
+    const size_t eb = dtype_bytes(desc->dtype);
+    if (!aligned(x, eb) || !aligned(y, eb) || !aligned(positions, p.pos_type == CT_POSITION_I64 ? 8 : 4))
+        return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    p.x = x;
+    p.y = y;
+    p.positions = positions;
+    return rotary_run(desc->dtype, desc->pairs, p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 ct_status ct_take_device_error(void *stream, int32_t *code) {

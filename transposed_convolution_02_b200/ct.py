@@ -41,7 +41,7 @@ EXPORTED = ["ct_output_shape", "ct_plan", "ct_plan_kernel", "ct_plan_launches",
             "ct_run_noalloc", "ct_plan_destroy", "ct_status_string", "ct_take_device_error",
             "ct_selftest_wait_timeout", "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
             "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
-            "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes"]
+            "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary"]
 
 
 class CtError(RuntimeError):
@@ -75,6 +75,15 @@ class ct_rms_norm_desc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
                 ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("rows", ctypes.c_int64), ("C", ctypes.c_int64), ("eps", ctypes.c_double)]
+
+
+class ct_rotary_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("position_type", ctypes.c_int32),
+                ("position_images", ctypes.c_int32), ("N", ctypes.c_int64),
+                ("grid", ctypes.c_int64 * 3), ("heads", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("sections", ctypes.c_int64 * 3), ("x_strides", ctypes.c_int64 * 3),
+                ("y_strides", ctypes.c_int64 * 3), ("base", ctypes.c_double)]
 
 
 _lib = None
@@ -117,6 +126,7 @@ def lib():
         L.ct_rms_norm.argtypes = [rp, P, P, P, P, P, P, P]
         L.ct_rms_norm_e4m3.argtypes = [rp, P, P, P, P, P, P, P, P]
         L.ct_rms_norm_backward.argtypes = [rp, P, P, P, P, P, P, P, P, P]
+        L.ct_rotary.argtypes = [ctypes.POINTER(ct_rotary_desc), P, P, P, P]
         L.ct_status_string.argtypes = [ctypes.c_int]
         L.ct_status_string.restype = ctypes.c_char_p
         for name in ("ct_output_shape", "ct_plan", "ct_plan_launches", "ct_prepacked_weight_bytes",
@@ -124,7 +134,7 @@ def lib():
                      "ct_run_noalloc", "ct_take_device_error", "ct_selftest_wait_timeout",
                      "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
                      "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
-                     "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes"):
+                     "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -841,3 +851,146 @@ def rms_norm_nhwc_backward(dy, x, rstd, weight=None, *, dsum=None, need_x_grad=T
         return dx, dweight
 
     return _run_on(call, x, stream)
+
+
+# ---- rotary positions ---------------------------------------------------------
+
+PAIRS = {"adjacent": 0, "halves": 1}
+POSITION_DTYPE = {torch.int32: 1, torch.int64: 2, torch.float32: 3}
+
+
+def _head_strides(shape, stride):
+    """(image, pixel, head) strides of [N, D1.., heads, dim], or None where the
+    pixels are not one stride apart or a head's elements are not neighbours."""
+    if shape[-1] > 1 and stride[-1] != 1:
+        return None
+    pixel = span = None
+    for size, step in zip(reversed(shape[1:-2]), reversed(stride[1:-2])):
+        if size == 1:
+            continue
+        if pixel is None:
+            pixel = span = step
+        elif step != span:
+            return None
+        span *= size
+    return stride[0], 0 if pixel is None else pixel, stride[-2]
+
+
+def _extent(t):
+    """First byte of a tensor and the one behind its last (no negative strides)."""
+    a = t.data_ptr()
+    return a, a + (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) * t.element_size()
+
+
+def check_rotary(x, sections, base, pairs, positions):
+    """Refuse arguments that the rotation cannot take."""
+    if x.dtype not in NORM_DTYPE:
+        raise ValueError("X must be float32, float16 or bfloat16, not %s" % x.dtype)
+    if not 1 <= len(sections) <= 3:
+        raise ValueError("sections must name 1 to 3 axes, not %d" % len(sections))
+    if x.dim() < 4:
+        raise ValueError("X must be [N, D.., heads, dim], it has shape %s" % list(x.shape))
+    for v in sections:
+        if v != int(v) or v < 0 or v % 2 != 0:
+            raise ValueError("each section must be an even number of elements, not %r" % (v,))
+    if sum(sections) > min(x.shape[-1], 512):
+        raise ValueError("sections of %d elements do not fit a head of %d (and 512)" % (sum(sections), x.shape[-1]))
+    if pairs not in PAIRS:
+        raise ValueError("pairs must be one of %s, not %r" % (sorted(PAIRS), pairs))
+    if not 0.0 < base < math.inf:
+        raise ValueError("base must be positive and finite, not %r" % (base,))
+    if positions is None:
+        if x.dim() != 3 + len(sections):
+            raise ValueError("X of shape %s does not have the %d pixel axes of sections; give positions"
+                             % (list(x.shape), len(sections)))
+        return
+    if positions.dtype not in POSITION_DTYPE:
+        raise ValueError("positions must be int32, int64 or float32, not %s" % positions.dtype)
+    want = tuple(x.shape[1:-2]) + (len(sections),)
+    if positions.device != x.device or tuple(positions.shape) not in (want, (x.shape[0],) + want):
+        raise ValueError("positions must have shape %s or %s on %s"
+                         % (list(want), [x.shape[0]] + list(want), x.device))
+
+
+_ROTARY = {}
+
+
+def _rotary_of(x, xs, ys, sections, base, pairs, positions, inverse):
+    """The checked arguments' descriptor (made once per sizes and types)."""
+    pos = None if positions is None else (positions.dtype, positions.shape, positions.device == x.device)
+    key = (x.shape, x.dtype, xs, ys, tuple(sections), base, pairs, pos, inverse)
+    try:
+        return _ROTARY[key]
+    except (KeyError, TypeError):
+        pass
+    d = ct_rotary_desc(NORM_DTYPE[x.dtype], len(sections), PAIRS[pairs], inverse)
+    d.N, d.heads, d.dim, d.base = x.shape[0], x.shape[-2], x.shape[-1], float(base)
+    grid = list(x.shape[1:-2])
+    if positions is not None:
+        d.position_type = POSITION_DTYPE[positions.dtype]
+        d.position_images = int(positions.dim() == x.dim() - 1)
+        grid = [math.prod(grid)] + [1] * (len(sections) - 1)
+    for a, v in enumerate(sections):
+        d.grid[a], d.sections[a] = grid[a], int(v)
+    for a in range(3):
+        d.x_strides[a], d.y_strides[a] = xs[a], ys[a]
+    if len(_ROTARY) >= 1024:
+        _ROTARY.clear()
+    _ROTARY[key] = d
+    return d
+
+
+def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
+    check_rotary(x, sections, base, pairs, positions)
+    xs = _head_strides(x.shape, x.stride())
+    ys = None
+    if out is not None:
+        check_like(out, "out", x)
+        ys = _head_strides(out.shape, out.stride())
+        if ys is None:
+            raise ValueError("out's pixels must be one stride apart, and a head's elements neighbours")
+        o0, o1 = _extent(out)
+        for t in (x, positions):
+            if t is None or t.numel() == 0:
+                continue
+            t0, t1 = _extent(t)
+            if t0 < o1 and o0 < t1 and not (t is x and xs == ys and t0 == o0):
+                raise ValueError("out overlaps an input")
+    _check_cuda(x, positions)
+
+    def call(raw):
+        xc, sx = (x, xs) if xs is not None else (x.contiguous(), None)
+        if sx is None:
+            sx = _head_strides(xc.shape, xc.stride())
+        pos = None if positions is None else positions.contiguous()
+        y = torch.empty(xc.shape, dtype=xc.dtype, device=xc.device) if out is None else out
+        sy = _head_strides(y.shape, y.stride()) if ys is None else ys
+        d = _rotary_of(xc, sx, sy, sections, base, pairs, pos, inverse)
+        st = lib().ct_rotary(d, xc.data_ptr(), _addr(pos), y.data_ptr(), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_rotary")
+        return y
+
+    return _run_on(call, x, stream)
+
+
+def rotary_nhwc(x, sections, *, base=10000.0, pairs="adjacent", positions=None, out=None, stream=None):
+    """Rotary positions of heads X[N, D1.., heads, dim] on 1 to 3 axes: the first
+    sum(sections) elements of each head are rotated in pairs, sections[a] of
+    them (even) by the position on axis a; the rest stay as they are.  float32,
+    float16 or bfloat16.  Pair i is elements 2i and 2i + 1 ("adjacent") or i
+    and i + sum(sections) / 2 ("halves"); the first pairs are axis 0's, and the
+    j-th pair of axis a turns by position * base^(-2j / sections[a]).
+
+    Positions are the pixels' indices, or ``positions`` (int32, int64 or
+    float32), [D1.., axes] for all images or [N, D1.., axes].  X may be a slice
+    (the queries and keys of a packed projection) or have its heads outside its
+    pixels in memory, without a copy, where its pixels are one stride apart;
+    other layouts are copied.  ``out`` may be X."""
+    return _rotate(x, sections, base, pairs, positions, out, stream, 0)
+
+
+def rotary_nhwc_backward(dy, sections, *, base=10000.0, pairs="adjacent", positions=None, out=None, stream=None):
+    """The gradient of rotary_nhwc in X at dy (dy rotated back), for the
+    sections, base, pairs and positions of the forward call."""
+    return _rotate(dy, sections, base, pairs, positions, out, stream, 1)
