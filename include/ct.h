@@ -419,6 +419,69 @@ typedef struct ct_rotary_desc {
  * Asynchronous on `stream`. */
 CT_API ct_status ct_rotary(const ct_rotary_desc *desc, const void *x, const void *positions, void *y, void *stream);
 
+/* AdamW over many tensors at once (Loshchilov and Hutter, "Decoupled weight
+ * decay regularization", 2019).  For every element, in fp32:
+ *
+ *     g' = g * grad_scale,   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2,
+ *     p  = p - lr (weight_decay p + m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)).
+ *
+ * Parameters and gradients are dense tensors of their own; the states of all
+ * parameters lie in one buffer for each kind, parameter i's from block
+ * sum_{k < i} ceil(n_k / 256) on, a block being 256 elements (what a parameter
+ * leaves of its last block counts for nothing; updates set it to 0).
+ * Parameters of 16 bits have a master in fp32 that the update works on, in a
+ * buffer of blocks for them alone; the parameter is the master rounded.
+ *
+ * bits = 32: exp_avg (m) and exp_avg_sq (v) are fp32.  bits = 8: they are e4m3
+ * codes with one fp32 scale a block (exp_avg_scale, exp_avg_sq_scale), of m
+ * and of the square root of v; scale = max(max / 448, 2^-126), and a value is
+ * rounded up to the next code with the probability of the part that lies beyond
+ * the last (nearest rounding would drop every change below half a step).  The
+ * random number is 16-bit part i % 8 of Philox4x32-10 (as in dropout) at
+ * (i / 8, step) under the key `seed`, i the element's place in the states.  A
+ * positive root never becomes 0.  A gradient that is not finite makes its
+ * element not finite, with 8-bit states its block. */
+typedef struct ct_param {
+    int64_t n;              /* elements */
+    int32_t dtype;          /* ct_dtype of the parameter */
+    int32_t grad_dtype;     /* of its gradient: dtype or CT_F32 */
+    double weight_decay;    /* read by ct_adamw alone */
+} ct_param;
+
+typedef struct ct_adamw_desc {
+    int32_t bits;           /* 32 or 8 */
+    int32_t reserved;       /* not read */
+    double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps >= 2^-126 */
+    int64_t step;           /* 1 for the first update */
+    uint64_t seed;          /* bits = 8 alone */
+    /* on the device, read by the kernel in place of the numbers above; NULL:
+     * not.  A captured graph so takes another step and rate at each replay. */
+    const float *lr_device;
+    const int64_t *step_device;
+    const float *grad_scale;    /* NULL: 1.  What is no positive finite number skips the update: nothing is written */
+} ct_adamw_desc;
+
+/* One update.  shapes, params and grads are host arrays of `count` entries, read
+ * before the call returns; a NULL gradient leaves its parameter and states as
+ * they are.  params[i] (and grads[i]) may not overlap each other or anything
+ * else of the call.  master may be NULL without parameters of 16 bits, the
+ * scales with bits = 32; states, masters and scales are 256-byte aligned.
+ * Limits: count <= 2^20, at most 2^40 elements (CT_ERR_ATTR).  Asynchronous on
+ * `stream`, a launch for up to 512 tensors. */
+CT_API ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_param *shapes, void *const *params,
+                          const void *const *grads, void *exp_avg, void *exp_avg_sq, float *exp_avg_scale,
+                          float *exp_avg_sq_scale, float *master, void *stream);
+
+/* *norm = the square root of the sum of all gradients' squares (squares in
+ * fp32, sums in 64 bits: a gradient past 1.8e19 counts as infinite), *scale (may
+ * be NULL) = min(1, max_norm / norm), or 0 where the norm is not finite: what
+ * ct_adamw's grad_scale takes to clip, or to skip an update that overflowed.
+ * Of shapes, n and grad_dtype are read; a NULL gradient counts nothing.
+ * max_norm > 0, infinity allowed.  The same call gives the same bits. */
+CT_API ct_status ct_grad_norm_workspace_bytes(int64_t count, size_t *bytes);
+CT_API ct_status ct_grad_norm(int64_t count, const ct_param *shapes, const void *const *grads, double max_norm,
+                              float *norm, float *scale, void *workspace, void *stream);
+
 /* Static, human-readable text for a status code. */
 CT_API const char *ct_status_string(ct_status status);
 

@@ -120,3 +120,45 @@ def rotary_bound(x, y, angles, pairs, dtype):
     both = (x[..., i].abs() + x[..., k].abs()) * off
     e[..., i], e[..., k] = both, both
     return 1.01 * (HALF[dtype] * y.abs() + e) + torch.where(e > 0, TINY[dtype], 0.0)
+
+
+# ---- AdamW --------------------------------------------------------------------
+
+def adamw(p, g, m, v, lr, betas, eps, decay, step):
+    """fp64 -> p, m, v and the update by m / sqrt(v) alone."""
+    m = betas[0] * m + (1 - betas[0]) * g
+    v = betas[1] * v + (1 - betas[1]) * g * g
+    update = lr * (m / (1 - betas[0] ** step)) / (torch.sqrt(v / (1 - betas[1] ** step)) + eps)
+    return p - lr * decay * p - update, m, v, update
+
+
+def adamw_bounds(p, g, m, v, new, lr, betas, eps, decay, step):
+    """(p, m, v) bounds of the fp32 update from the old p, m, v.  m: the
+    gradient's scale, both factors, products and the sum.  v the same with the
+    square.  The update: m's error over the same root, and sqrt (2^-23), the
+    quotient (4 u), the corrections (expm1 and its argument, or rounded once),
+    eps and products: 40 u in all."""
+    pn, mn, vn, update = new
+    em = 6 * U * (betas[0] * m.abs() + (1 - betas[0]) * g.abs())
+    ev = 8 * U * vn
+    slope = (lr / (1 - betas[0] ** step)) / (torch.sqrt(vn / (1 - betas[1] ** step)) + eps)
+    ep = em * slope + 40 * U * update.abs() + 4 * U * lr * decay * p.abs()
+    return 1.01 * (U * pn.abs() + ep) + 2.0 ** -126, em + 2.0 ** -126, ev + 2.0 ** -126
+
+
+def code_steps(x):
+    """The grid below |x| (fp64, at most 448): the code below and the distance to the next."""
+    a = x.abs()
+    step = torch.exp2(torch.floor(torch.log2(a.clamp(min=2.0 ** -6)))) * 2.0 ** -3
+    return torch.floor(a / step) * step, step
+
+
+def random_codes(x, r):
+    """Where x lies between two codes and r's 16 bits choose the upper one ->
+    the code (fp64), and whether the choice is one that rounding can turn: x is
+    good to some 60 u, 2^4 steps of the grid at most, that is 4 of 2^16."""
+    low, step = code_steps(x)
+    part = (x.abs() - low) / step * 65536 + r
+    code = torch.where(part >= 65536, low + step, low).clamp(max=448.0)
+    close = ((part - 65536).abs() < 6) | (part < r + 6) | (part > r + 65530)
+    return torch.copysign(code, x), close

@@ -1,7 +1,9 @@
-"""Root-mean-square norm without a GPU: the plain forms against differences, and
-the refusals of the C entries and the binding."""
+"""Root-mean-square norm, rotary positions and AdamW without a GPU: the plain
+forms against differences and by hand, and the refusals of the C entries and
+the binding."""
 
 import ctypes
+import math
 
 import pytest
 import torch
@@ -143,8 +145,8 @@ def test_rotary_formula(pairs):
     assert torch.allclose(ref.rotary(y, angles, pairs), ref.rotary(x, 2 * angles, pairs))
     differences(lambda v: float((ref.rotary(v, angles, pairs) * dy).sum()), (x,), (ref.rotary(dy, -angles, pairs),))
     i, k = (0, 1) if pairs == "adjacent" else (0, 4)         # a turn by hand: pixel (2, 3), axis 0's first pair
-    assert abs(float(y[1, 2, 3, 4, i]) - float(x[1, 2, 3, 4, i] * torch.cos(torch.tensor(2.0, dtype=torch.float64))
-                                              - x[1, 2, 3, 4, k] * torch.sin(torch.tensor(2.0, dtype=torch.float64)))) < 1e-12
+    a, b = float(x[1, 2, 3, 4, i]), float(x[1, 2, 3, 4, k])
+    assert abs(float(y[1, 2, 3, 4, i]) - (a * math.cos(2.0) - b * math.sin(2.0))) < 1e-12
 
 
 def rotary_desc(**over):
@@ -163,12 +165,14 @@ def rotary_desc(**over):
 
 @pytest.mark.parametrize("over, status", [
     (dict(N=0), 0), (dict(heads=0), 0), (dict(grid=[0, 4, 0]), 0), (dict(dtype=3), 3), (dict(axes=0), 2),
-    (dict(axes=4), 2), (dict(pairs=2), 4), (dict(inverse=2), 4), (dict(position_type=4), 4), (dict(position_images=2), 4),
+    (dict(axes=4), 2), (dict(pairs=2), 4), (dict(inverse=2), 4), (dict(position_type=4), 4),
+    (dict(position_images=2), 4),
     (dict(base=0.0), 4), (dict(base=-1.0), 4), (dict(base=float("nan")), 4), (dict(base=float("inf")), 4),
     (dict(N=-1), 4), (dict(heads=-1), 4), (dict(dim=0), 4), (dict(grid=[3, -1, 0]), 4), (dict(N=1 << 31), 4),
     (dict(N=1 << 30, grid=[1 << 30, 1 << 30, 0]), 4), (dict(sections=[3, 4, 0]), 1), (dict(sections=[-2, 4, 0]), 1),
     (dict(sections=[10, 8, 0]), 1), (dict(dim=600, sections=[500, 14, 0]), 1), (dict(sections=[1 << 40, 8, 0]), 1),
-    (dict(x_strides=[1 << 59, 80, 16]), 4), (dict(x_strides=[-(1 << 58), 80, 16]), 4), (dict(y_strides=[960, 80, -16]), 4),
+    (dict(x_strides=[1 << 59, 80, 16]), 4), (dict(x_strides=[-(1 << 58), 80, 16]), 4),
+    (dict(y_strides=[960, 80, -16]), 4),
     (dict(y_strides=[960, 80, 15]), 4), (dict(y_strides=[960, 79, 16]), 4), (dict(y_strides=[959, 80, 16]), 4),
     (dict(y_strides=[960, 0, 16]), 4), (dict(y_strides=[0, 80, 16]), 4)])
 def test_rotary_desc_refusals(over, status):
@@ -231,3 +235,139 @@ def test_pixel_strides():
     assert of(qkv[:, :1, :3]) == (2880, 240, 16) and of(qkv[:, :, :1]) == (2880, 960, 16)
     assert of(torch.zeros(2, 5, 3, 4, 16).permute(0, 2, 3, 1, 4)) == (960, 16, 192)
     assert of(torch.zeros(2, 1, 5, 16)) == (80, 0, 16)
+
+
+# ---- AdamW and the gradients' norm ------------------------------------------------
+
+def test_adamw_formula():
+    """A constant gradient moves by lr a step whatever its size; decay alone
+    shrinks; the codes' grid is e4m3's and the random choice right on average."""
+    p = m = v = torch.zeros(3, dtype=torch.float64)
+    g = torch.tensor([1e-3, -2.0, 50.0], dtype=torch.float64)
+    for t in range(1, 6):
+        p, m, v, _ = ref.adamw(p, g, m, v, 0.01, (0.9, 0.999), 1e-30, 0.0, t)
+        assert torch.allclose(p, -0.01 * t * g.sign())
+    q = ref.adamw(p, 0 * g, 0 * g, 0 * g, 0.01, (0.9, 0.999), 1e-8, 0.5, 1)[0]
+    assert torch.allclose(q, p * (1 - 0.005))
+    x = torch.linspace(-448, 448, 100001, dtype=torch.float64)
+    x = torch.cat((x, x / 448, x / 448 / 100, x / 448 / 5000))
+    low, step = ref.code_steps(x)
+    for c in (low, low + step):
+        assert torch.equal(c.clamp(max=448).float().to(torch.float8_e4m3fn).double(), c.clamp(max=448))
+    assert bool((low <= x.abs()).all()) and bool((x.abs() < low + step).all())
+    r = torch.arange(65536, dtype=torch.float64)
+    for value in (0.3, 1.07, 100.0, 0.001, 0.017):
+        mean = ref.random_codes(torch.full_like(r, value), r)[0].mean()
+        assert abs(float(mean) - value) <= float(ref.code_steps(torch.tensor(value).double())[1]) / 65536
+
+
+def shapes(*rows):
+    return (ct.ct_param * max(1, len(rows)))(*[ct.ct_param(*r) for r in rows])
+
+
+def addresses(*values):
+    return ct._pointers(list(values) or [0])
+
+
+def adamw_status(desc=None, rows=((10, 0, 0, 0.1),), params=(A,), grads=(A,), m=A, v=A, ms=None, vs=None, master=None,
+                 count=None, **over):
+    d = ct.ct_adamw_desc(32, 0, 1e-3, 0.9, 0.999, 1e-8, 1, 3)
+    for k, x in over.items():
+        setattr(d, k, x)
+    p, g = addresses(*params), addresses(*grads)
+    return ct.lib().ct_adamw(ctypes.byref(d) if desc is None else None, len(rows) if count is None else count,
+                             shapes(*rows), p.buffer_info()[0], g.buffer_info()[0], m, v, ms, vs, master, None)
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(desc=0), 6), (dict(bits=16), 4), (dict(lr=-1.0), 4), (dict(lr=float("nan")), 4), (dict(lr=float("inf")), 4),
+    (dict(beta1=1.0), 4), (dict(beta2=-0.1), 4), (dict(beta2=float("nan")), 4), (dict(eps=0.0), 4),
+    (dict(eps=float("inf")), 4), (dict(step=0), 4), (dict(count=-1), 4), (dict(count=(1 << 20) + 1), 4),
+    (dict(rows=((10, 3, 3, 0.0),)), 3), (dict(rows=((10, 0, 1, 0.0),)), 3), (dict(rows=((10, 1, 2, 0.0),)), 3),
+    (dict(rows=((-1, 0, 0, 0.0),)), 4), (dict(rows=(((1 << 40) + 1, 0, 0, 0.0),)), 4),
+    (dict(rows=((1 << 40, 0, 0, 0.0), (1, 0, 0, 0.0)), params=(A, A), grads=(A, A)), 4),
+    (dict(rows=((10, 0, 0, -0.1),)), 4), (dict(rows=((10, 0, 0, float("nan")),)), 4), (dict(params=(0,)), 6),
+    (dict(params=(A + 2,)), 5), (dict(grads=(A + 2,)), 5), (dict(rows=((10, 1, 1, 0.0),)), 6),
+    (dict(rows=((10, 1, 1, 0.0),), master=A, params=(A + 1,)), 5), (dict(m=None), 6), (dict(v=None), 6),
+    (dict(m=A + 128), 5), (dict(bits=8), 6), (dict(bits=8, ms=A), 6), (dict(bits=8, ms=A, vs=A + 4), 5),
+    (dict(master=A + 4), 5), (dict(lr_device=A + 2), 5), (dict(step_device=A + 4), 5), (dict(grad_scale=A + 2), 5),
+    (dict(grads=(0,), params=(0,), m=None), 0), (dict(rows=((0, 0, 0, 0.0),), m=None), 0), (dict(count=0, m=None), 0)])
+def test_adamw_refusals(over, status):
+    assert adamw_status(**over) == status
+
+
+def test_grad_norm_refusals():
+    L = ct.lib()
+    n = ctypes.c_size_t()
+    assert L.ct_grad_norm_workspace_bytes(5, None) == 6 and L.ct_grad_norm_workspace_bytes(-1, ctypes.byref(n)) == 4
+    assert L.ct_grad_norm_workspace_bytes(600, ctypes.byref(n)) == 0 and n.value >= 8 * 2 * 1184
+    s, g = shapes((10, 0, 0, 0.0)), addresses(A)
+
+    def status(count=1, shapes_=s, grads=g.buffer_info()[0], most=1.0, norm=A, scale=A, ws=A):
+        return L.ct_grad_norm(count, shapes_, grads, most, norm, scale, ws, None)
+
+    assert status(count=-1) == 4 and status(shapes_=None) == 6 and status(grads=None) == 6
+    assert status(most=0.0) == 4 and status(most=-1.0) == 4 and status(most=float("nan")) == 4
+    assert status(norm=None) == 6 and status(ws=None) == 8 and status(ws=A + 8) == 5 and status(scale=A + 1) == 5
+    if not torch.cuda.is_available():
+        assert status() == 7 and status(scale=None, most=float("inf")) == 7 and adamw_status() == 7
+
+
+class Card(torch.Tensor):
+    """A CPU tensor that passes for one on a device, for the binding's checks."""
+    is_cuda = True
+
+
+def card(*size, dtype=torch.float32):
+    return torch.zeros(*size, dtype=dtype).as_subclass(Card)
+
+
+@pytest.mark.parametrize("make, refusal", [
+    (lambda: ct.AdamW([]), "no parameter"),
+    (lambda: ct.AdamW([torch.zeros(3)]), "CUDA"),
+    (lambda: ct.AdamW([card(3, dtype=torch.float64)]), "float32"),
+    (lambda: ct.AdamW([card(3, 4).t()]), "contiguous"),
+    (lambda: ct.AdamW([card(3)], bits=16), "bits"),
+    (lambda: ct.AdamW([card(3)], seed=-1), "seed"),
+    (lambda: ct.AdamW([card(3)], betas=(0.9, 1.0)), "betas"),
+    (lambda: ct.AdamW([card(3)], eps=0.0), "eps"),
+    (lambda: ct.AdamW([card(3)], weight_decay=-0.1), "weight_decay"),
+    (lambda: ct.AdamW([card(3)], weight_decay=[0.1, 0.2]), "weight_decay"),
+    (lambda: ct.AdamW([TWICE, TWICE]), "overlap"),
+    (lambda: ct.AdamW([TWICE[:2], TWICE[1:]]), "overlap"),
+    (lambda: ct.grad_norm([]), "no gradient"),
+    (lambda: ct.grad_norm([None, None]), "no gradient"),
+    (lambda: ct.grad_norm([torch.zeros(3)]), "CUDA"),
+    (lambda: ct.grad_norm([card(3)], max_norm=0.0), "max_norm"),
+    (lambda: ct.grad_norm([card(3)], max_norm=float("nan")), "max_norm"),
+    (lambda: ct.grad_norm([card(3, dtype=torch.int32)]), "float32")])
+def test_adamw_binding_refusals(make, refusal):
+    with pytest.raises(ValueError, match=refusal):
+        make()
+
+
+TWICE = card(3)
+
+
+def test_adamw_step_refusals():
+    p, q = card(2, 3), card(5, dtype=torch.float16)
+    opt = ct.AdamW([p, q])
+    g = [card(2, 3), card(5, dtype=torch.float16)]
+    one = card(1)
+    for grads, how, refusal in [
+            (g[:1], {}, "2 parameters"), ([g[0].view(3, 2), g[1]], {}, "gradient 0"),
+            ([g[0].half(), g[1]], {}, "gradient 0"),
+            ([g[0], card(5, dtype=torch.bfloat16)], {}, "gradient 1"), ([g[0], torch.zeros(5)], {}, "CUDA"),
+            (g, dict(grad_scale=one.double()), "grad_scale"), (g, dict(grad_scale=card(2)), "grad_scale"),
+            (g, dict(step=one), "step")]:
+        with pytest.raises(ValueError, match=refusal):
+            opt.step(grads, **how)
+    for lr in (-1.0, float("nan"), float("inf")):
+        opt.lr = lr
+        with pytest.raises(ValueError, match="lr"):
+            opt.step(g)
+    opt.lr = 1e-3
+    q.data = q.data[:4]
+    with pytest.raises(ValueError, match="parameter 1"):
+        opt.step(g)
+    assert opt.steps == 0

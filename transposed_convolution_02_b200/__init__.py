@@ -4,6 +4,7 @@ include/ct.h) and its thin Python binding.  ``build.build()`` compiles the
 library in-tree; ``workloads`` holds the seeded synthetic inputs."""
 
 from .ct import (  # noqa: F401
+    AdamW,
     ConvTranspose,
     CtError,
     conv_transpose,
@@ -21,6 +22,7 @@ from .ct import (  # noqa: F401
     ct_workspace_bytes,
     dropout,
     dropout_backward,
+    grad_norm,
     group_norm_nhwc,
     group_norm_nhwc_backward,
     make_desc,

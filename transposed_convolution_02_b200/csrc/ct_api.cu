@@ -12,6 +12,7 @@
 
 #include <math.h>
 
+#include "adamw.h"
 #include "ct_internal.h"
 #include "group_norm.h"
 #include "rms_norm.h"
@@ -370,9 +371,10 @@ ct_status resolve_rotary(const ct_rotary_desc *d, RotaryParams *p) {
     if (mul_capped(mul_capped(mul_capped(p->N, p->S), p->H), p->D) < 0) return CT_ERR_ATTR;
     int64_t rot = 0;
     for (int a = 0; a < d->axes; ++a) {
-        if (d->sections[a] < 0 || d->sections[a] % 2 != 0 || d->sections[a] > 2 * kRotaryMaxPairs) return CT_ERR_CHANNELS;
+        const int64_t v = d->sections[a];
+        if (v < 0 || v % 2 != 0 || v > 2 * kRotaryMaxPairs) return CT_ERR_CHANNELS;
         p->first[a] = (int32_t)(rot / 2);
-        rot += d->sections[a];
+        rot += v;
     }
     if (rot > p->D || rot > 2 * kRotaryMaxPairs) return CT_ERR_CHANNELS;
     p->rot = (int32_t)rot;
@@ -386,11 +388,29 @@ ct_status resolve_rotary(const ct_rotary_desc *d, RotaryParams *p) {
     for (int a = 0; a < 3; ++a) {
         p->xs[a] = d->x_strides[a];
         p->ys[a] = d->y_strides[a];
-        if (p->xs[a] > kMaxStride || p->xs[a] < -kMaxStride || p->ys[a] > kMaxStride || p->ys[a] < 0) return CT_ERR_ATTR;
+        if (p->xs[a] > kMaxStride || p->xs[a] < -kMaxStride) return CT_ERR_ATTR;
+        if (p->ys[a] > kMaxStride || p->ys[a] < 0) return CT_ERR_ATTR;
     }
     p->pos_image = d->position_images ? p->S * p->axes : 0;
     p->pos_type = d->position_type;
     p->sign = d->inverse ? -1.f : 1.f;
+    return CT_OK;
+}
+
+constexpr int64_t kMaxTensors = int64_t(1) << 20, kMaxParamElems = int64_t(1) << 40;
+
+// The gradients of an update or a norm: types, sizes, addresses.
+ct_status check_params(int64_t count, const ct_param *shapes, const void *const *grads) {
+    if (count < 0 || count > kMaxTensors) return CT_ERR_ATTR;
+    if (count > 0 && (!shapes || !grads)) return CT_ERR_NULL;
+    int64_t all = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!known_dtype(shapes[i].dtype)) return CT_ERR_DTYPE;
+        if (shapes[i].grad_dtype != CT_F32 && shapes[i].grad_dtype != shapes[i].dtype) return CT_ERR_DTYPE;
+        if (shapes[i].n < 0 || shapes[i].n > kMaxParamElems) return CT_ERR_ATTR;
+        if ((all += shapes[i].n) > kMaxParamElems) return CT_ERR_ATTR;
+        if (!aligned(grads[i], dtype_bytes(shapes[i].grad_dtype))) return CT_ERR_ALIGN;
+    }
     return CT_OK;
 }
 
@@ -707,6 +727,68 @@ ct_status ct_rotary(const ct_rotary_desc *desc, const void *x, const void *posit
     p.y = y;
     p.positions = positions;
     return rotary_run(desc->dtype, desc->pairs, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_param *shapes, void *const *params,
+                   const void *const *grads, void *exp_avg, void *exp_avg_sq, float *exp_avg_scale,
+                   float *exp_avg_sq_scale, float *master, void *stream) {
+    if (!desc) return CT_ERR_NULL;
+    if (desc->bits != 32 && desc->bits != 8) return CT_ERR_ATTR;
+    if (!(desc->lr >= 0.0) || !isfinite(desc->lr)) return CT_ERR_ATTR;
+    if (!(desc->eps >= ldexp(1.0, -126)) || !isfinite(desc->eps)) return CT_ERR_ATTR;   // 0 / eps is 0
+    for (double v : {desc->beta1, desc->beta2})
+        if (!(v >= 0.0 && v < 1.0)) return CT_ERR_ATTR;
+    if (desc->step < 1) return CT_ERR_ATTR;
+    ct_status st = check_params(count, shapes, grads);
+    if (st != CT_OK) return st;
+    bool some = false;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!isfinite(shapes[i].weight_decay) || shapes[i].weight_decay < 0.0) return CT_ERR_ATTR;
+        if (shapes[i].n == 0 || !grads[i]) continue;
+        some = true;
+        if (!params || !params[i]) return CT_ERR_NULL;
+        if (!aligned(params[i], dtype_bytes(shapes[i].dtype))) return CT_ERR_ALIGN;
+        if (shapes[i].dtype != CT_F32 && !master) return CT_ERR_NULL;
+    }
+    if (!some) return CT_OK;
+    if (!exp_avg || !exp_avg_sq || (desc->bits == 8 && (!exp_avg_scale || !exp_avg_sq_scale))) return CT_ERR_NULL;
+    if (!aligned(exp_avg, 256) || !aligned(exp_avg_sq, 256) || !aligned(exp_avg_scale, 256) ||
+        !aligned(exp_avg_sq_scale, 256) || !aligned(master, 256) || !aligned(desc->lr_device, 4) ||
+        !aligned(desc->step_device, 8) || !aligned(desc->grad_scale, 4))
+        return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    AdamWParams p = {};
+    p.lr_dev = desc->lr_device;
+    p.step_dev = desc->step_device;
+    p.grad_scale = desc->grad_scale;
+    p.m = exp_avg;
+    p.v = exp_avg_sq;
+    p.m_scale = exp_avg_scale;
+    p.v_scale = exp_avg_sq_scale;
+    p.master = master;
+    return adamw_run(desc, count, shapes, params, grads, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ct_status ct_grad_norm_workspace_bytes(int64_t count, size_t *bytes) {
+    if (!bytes) return CT_ERR_NULL;
+    if (count < 0 || count > kMaxTensors) return CT_ERR_ATTR;
+    *bytes = (size_t)norm_partials(count) * sizeof(double);
+    return CT_OK;
+}
+
+ct_status ct_grad_norm(int64_t count, const ct_param *shapes, const void *const *grads, double max_norm, float *norm,
+                       float *scale, void *workspace, void *stream) {
+    ct_status st = check_params(count, shapes, grads);
+    if (st != CT_OK) return st;
+    if (!(max_norm > 0.0)) return CT_ERR_ATTR;
+    if (!norm) return CT_ERR_NULL;
+    if (!workspace) return CT_ERR_WORKSPACE;
+    if (!aligned(norm, 4) || !aligned(scale, 4) || !aligned(workspace, 256)) return CT_ERR_ALIGN;
+    st = check_device();
+    if (st != CT_OK) return st;
+    return grad_norm_run(count, shapes, grads, max_norm, norm, scale, (double *)workspace,
+                         reinterpret_cast<cudaStream_t>(stream));
 }
 
 ct_status ct_take_device_error(void *stream, int32_t *code) {

@@ -407,8 +407,10 @@ __global__ void __launch_bounds__(256) rms_columns_kernel(const RmsParams p) {
     const int64_t first = blockIdx.y * each, last = first + each < p.rows ? first + each : p.rows;
     for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < p.C; c += (int64_t)gridDim.x * 256) {
         float s = 0.f;
-        for (int64_t row = first; row < last; ++row)
-            s = fmaf(to_f<T>(((const T *)p.dy)[row * p.C + c]), to_f<T>(((const T *)p.x)[row * p.C + c]) * p.rstd_in[row], s);
+        for (int64_t row = first; row < last; ++row) {
+            const int64_t i = row * p.C + c;
+            s = fmaf(to_f<T>(((const T *)p.dy)[i]), to_f<T>(((const T *)p.x)[i]) * p.rstd_in[row], s);
+        }
         p.ws[blockIdx.y * p.C + c] = s;
     }
 }

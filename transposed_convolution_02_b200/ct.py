@@ -12,6 +12,7 @@ Attribute names follow the ai.onnx.ConvTranspose README ("Attributes");
 weight [C_in, K.., O/groups], padding as (lo, hi) per spatial dim).
 """
 
+import array
 import ctypes
 import functools
 import math
@@ -41,7 +42,8 @@ EXPORTED = ["ct_output_shape", "ct_plan", "ct_plan_kernel", "ct_plan_launches",
             "ct_run_noalloc", "ct_plan_destroy", "ct_status_string", "ct_take_device_error",
             "ct_selftest_wait_timeout", "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
             "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
-            "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary"]
+            "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary",
+            "ct_adamw", "ct_grad_norm", "ct_grad_norm_workspace_bytes"]
 
 
 class CtError(RuntimeError):
@@ -86,6 +88,18 @@ class ct_rotary_desc(ctypes.Structure):
                 ("y_strides", ctypes.c_int64 * 3), ("base", ctypes.c_double)]
 
 
+class ct_param(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("weight_decay", ctypes.c_double)]
+
+
+class ct_adamw_desc(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_int32), ("reserved", ctypes.c_int32), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("lr_device", ctypes.c_void_p),
+                ("step_device", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -127,6 +141,10 @@ def lib():
         L.ct_rms_norm_e4m3.argtypes = [rp, P, P, P, P, P, P, P, P]
         L.ct_rms_norm_backward.argtypes = [rp, P, P, P, P, P, P, P, P, P]
         L.ct_rotary.argtypes = [ctypes.POINTER(ct_rotary_desc), P, P, P, P]
+        L.ct_adamw.argtypes = [ctypes.POINTER(ct_adamw_desc), ctypes.c_int64, ctypes.POINTER(ct_param),
+                               P, P, P, P, P, P, P, P]
+        L.ct_grad_norm_workspace_bytes.argtypes = [ctypes.c_int64, szp]
+        L.ct_grad_norm.argtypes = [ctypes.c_int64, ctypes.POINTER(ct_param), P, f64, P, P, P, P]
         L.ct_status_string.argtypes = [ctypes.c_int]
         L.ct_status_string.restype = ctypes.c_char_p
         for name in ("ct_output_shape", "ct_plan", "ct_plan_launches", "ct_prepacked_weight_bytes",
@@ -134,7 +152,8 @@ def lib():
                      "ct_run_noalloc", "ct_take_device_error", "ct_selftest_wait_timeout",
                      "ct_dropout", "ct_group_norm", "ct_group_norm_backward",
                      "ct_group_norm_workspace_bytes", "ct_rms_norm", "ct_rms_norm_e4m3",
-                     "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary"):
+                     "ct_rms_norm_backward", "ct_rms_norm_workspace_bytes", "ct_rotary",
+                     "ct_adamw", "ct_grad_norm", "ct_grad_norm_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -994,3 +1013,227 @@ def rotary_nhwc_backward(dy, sections, *, base=10000.0, pairs="adjacent", positi
     """The gradient of rotary_nhwc in X at dy (dy rotated back), for the
     sections, base, pairs and positions of the forward call."""
     return _rotate(dy, sections, base, pairs, positions, out, stream, 1)
+
+
+# ---- a training step's end: the gradients' norm, AdamW ---------------------------
+
+BLOCK = 256     # elements of a block of AdamW's states
+
+
+def _pointers(addresses):
+    """A host array of device addresses (keep it while its address is used)."""
+    return array.array("Q", addresses)
+
+
+def _check_grad(g, name):
+    if not g.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if g.dtype not in NORM_DTYPE:
+        raise ValueError("%s must be float32, float16 or bfloat16, not %s" % (name, g.dtype))
+    if g.is_sparse or g.layout != torch.strided:
+        raise ValueError("%s must be a dense tensor" % name)
+
+
+_GRADS = {}
+
+
+def _grads_of(grads):
+    """The descriptors of gradients that lie on one device, and the workspace's
+    size (made once per sizes and types)."""
+    key = tuple([(g.numel(), g.dtype, g.get_device(), g.layout) for g in grads])
+    try:
+        return _GRADS[key]
+    except KeyError:
+        pass
+    for i, g in enumerate(grads):
+        _check_grad(g, "gradient %d" % i)
+        if g.device != grads[0].device:
+            raise ValueError("gradient %d is on %s, the first on %s" % (i, g.device, grads[0].device))
+    shapes = (ct_param * len(grads))(*[ct_param(g.numel(), NORM_DTYPE[g.dtype], NORM_DTYPE[g.dtype], 0.0)
+                                       for g in grads])
+    n = ctypes.c_size_t()
+    st = lib().ct_grad_norm_workspace_bytes(len(grads), ctypes.byref(n))
+    if st != CT_OK:
+        raise CtError(st, "ct_grad_norm_workspace_bytes")
+    if len(_GRADS) >= 64:
+        _GRADS.clear()
+    _GRADS[key] = shapes, n.value
+    return _GRADS[key]
+
+
+def grad_norm(grads, max_norm=None, *, stream=None):
+    """The 2-norm of all gradients together (float32, float16 and bfloat16 may
+    be mixed; None entries count nothing) and the scale that clips it to
+    max_norm, float32 tensors without dimensions on the gradients' device:
+    scale = min(1, max_norm / norm), 0 where the norm is not finite.  Give the
+    scale to AdamW.step: nothing waits for it, and 0 skips the step."""
+    grads = [g for g in grads if g is not None]
+    if not grads:
+        raise ValueError("there is no gradient")
+    if max_norm is None:
+        max_norm = math.inf
+    if not max_norm > 0.0:
+        raise ValueError("max_norm must be positive, not %r" % (max_norm,))
+    shapes, bytes_ = _grads_of(grads)
+
+    def call(raw):
+        dense = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        at = _pointers([g.data_ptr() for g in dense])
+        dev = grads[0].device
+        out = torch.empty(2, dtype=torch.float32, device=dev)
+        ws = torch.empty(bytes_, dtype=torch.uint8, device=dev)
+        st = lib().ct_grad_norm(len(dense), shapes, at.buffer_info()[0], max_norm, out.data_ptr(),
+                                out.data_ptr() + 4, ws.data_ptr(), raw)
+        if st != CT_OK:
+            raise CtError(st, "ct_grad_norm")
+        return out.unbind()
+
+    return _run_on(call, grads[0], stream)
+
+
+class AdamW:
+    """AdamW over many tensors, one launch for up to 512 of them.
+
+    ``params`` are contiguous CUDA tensors (float32, float16, bfloat16; mixed)
+    on one device, updated in place; ``weight_decay`` is a number or one for each.
+    Parameters of 16 bits get float32 masters, which the updates work on.
+    ``bits=8`` holds the states in 8 bits, rounded at random by ``seed``.
+
+    The states are tensors of this object, to be saved and copied back for a
+    restart together with ``steps``: exp_avg and exp_avg_sq, all parameters one
+    after the other, each from a multiple of 256 elements on (float32, or with
+    bits=8 float8_e4m3fn codes of exp_avg and of the square root of exp_avg_sq,
+    under exp_avg_scale and exp_avg_sq_scale, a scale for 256), and master
+    (None without parameters of 16 bits).  ``lr`` may be changed between steps,
+    and be a float32 CUDA tensor of one element, which is read on the device."""
+
+    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32, seed=0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("there is no parameter")
+        if bits not in (32, 8):
+            raise ValueError("bits must be 32 or 8, not %r" % (bits,))
+        if not 0 <= seed < 1 << 64:
+            raise ValueError("seed must be in [0, 2^64)")
+        if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0):
+            raise ValueError("betas must be in [0, 1), not %r" % (betas,))
+        if not 2.0 ** -126 <= eps < math.inf:
+            raise ValueError("eps must be positive and finite, not %r" % (eps,))
+        n = len(self.params)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        if len(decay) != n or not all(0.0 <= v < math.inf for v in decay):
+            raise ValueError("weight_decay must be a number >= 0, or one for each of %d parameters" % n)
+        for i, p in enumerate(self.params):
+            _check_grad(p, "parameter %d" % i)
+            if p.device != self.params[0].device:
+                raise ValueError("parameter %d is on %s, the first on %s" % (i, p.device, self.params[0].device))
+        self.device = self.params[0].device
+        self.lr, self.betas, self.eps, self.bits, self.seed, self.steps = lr, tuple(betas), eps, bits, seed, 0
+        self._sizes = [p.numel() for p in self.params]
+        self._dtypes = [p.dtype for p in self.params]
+        self._shapes = [p.shape for p in self.params]
+        self._at = self._places()
+        self._decay = decay
+        self._meta = self._table = None
+        self._desc = ct_adamw_desc(bits)
+        self._desc.beta1, self._desc.beta2, self._desc.eps, self._desc.seed = betas[0], betas[1], eps, seed
+        blocks = [-(-k // BLOCK) for k in self._sizes]
+        total = sum(blocks)
+        kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        self.exp_avg = torch.zeros(total * BLOCK, dtype=torch.float32 if bits == 32 else torch.uint8,
+                                   device=self.device).view(kind)
+        self.exp_avg_sq = torch.zeros_like(self.exp_avg.view(torch.uint8)).view(kind)
+        self.exp_avg_scale = self.exp_avg_sq_scale = self.master = None
+        if bits == 8:
+            self.exp_avg_scale = torch.zeros(total, dtype=torch.float32, device=self.device)
+            self.exp_avg_sq_scale = torch.zeros_like(self.exp_avg_scale)
+        low = [i for i, p in enumerate(self.params) if p.dtype != torch.float32]
+        if low:
+            self.master = torch.zeros(sum(blocks[i] for i in low) * BLOCK, dtype=torch.float32, device=self.device)
+            at = 0
+            for i in low:
+                self.master[at:at + self._sizes[i]].copy_(self.params[i].detach().reshape(-1))
+                at += blocks[i] * BLOCK
+
+    def _places(self):
+        """The parameters' addresses; they have to be dense and apart."""
+        for i, p in enumerate(self.params):
+            if not p.is_contiguous():
+                raise ValueError("parameter %d must be contiguous" % i)
+            if p.shape != self._shapes[i] or p.dtype != self._dtypes[i] or p.device != self.device:
+                raise ValueError("parameter %d has another shape, type or device than it had" % i)
+        spans = sorted(_extent(p) for p in self.params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("two parameters overlap")
+        return [p.data_ptr() for p in self.params]
+
+    def _grads(self, grads):
+        """Check the gradients and make their descriptors; None entries stay."""
+        kinds = []
+        for i, (g, shape, dtype) in enumerate(zip(grads, self._shapes, self._dtypes)):
+            if g is None:
+                kinds.append(dtype)
+                continue
+            _check_grad(g, "gradient %d" % i)
+            if g.shape != shape or g.device != self.device or g.dtype not in (dtype, torch.float32):
+                raise ValueError("gradient %d must be a %s or float32 tensor of shape %s on %s"
+                                 % (i, dtype, list(shape), self.device))
+            kinds.append(g.dtype)
+        self._table = (ct_param * len(kinds))(*[
+            ct_param(n, NORM_DTYPE[d], NORM_DTYPE[k], w)
+            for n, d, k, w in zip(self._sizes, self._dtypes, kinds, self._decay)])
+
+    def _scalar(self, t, name, dtype):
+        if t.dtype != dtype or t.numel() != 1 or t.device != self.device:
+            raise ValueError("%s must be a %s tensor of one element on %s" % (name, dtype, self.device))
+        return t.data_ptr()
+
+    def step(self, grads, *, grad_scale=None, step=None, stream=None):
+        """One update by ``grads``, a gradient for each parameter in its dtype
+        or float32 (None leaves a parameter and its states as they are).
+
+        ``grad_scale``, a float32 CUDA tensor of one element (grad_norm's),
+        multiplies the gradients; one that is not positive and finite skips the
+        update.  ``steps`` counts the updates, skipped ones too; ``step``, an
+        int64 CUDA tensor of one element, is the number of this update (1 for
+        the first) in its place, read on the device: a captured graph needs it,
+        and counts with it."""
+        grads = list(grads)
+        params = self.params
+        if len(grads) != len(params):
+            raise ValueError("%d gradients for %d parameters" % (len(grads), len(params)))
+        meta = [None if g is None else (g.shape, g.dtype, g.get_device(), g.layout) for g in grads]
+        if meta != self._meta:
+            self._meta = None
+            self._grads(grads)
+            self._meta = meta
+        if ([p.data_ptr() for p in params] != self._at or [p.numel() for p in params] != self._sizes
+                or [p.dtype for p in params] != self._dtypes or not all([p.is_contiguous() for p in params])):
+            self._at = self._places()
+        d, lr = self._desc, self.lr
+        d.grad_scale = None if grad_scale is None else self._scalar(grad_scale, "grad_scale", torch.float32)
+        d.step_device = None if step is None else self._scalar(step, "step", torch.int64)
+        if isinstance(lr, torch.Tensor):
+            d.lr_device, d.lr = self._scalar(lr, "lr", torch.float32), 0.0
+        else:
+            if not 0.0 <= lr < math.inf:
+                raise ValueError("lr must be >= 0 and finite, not %r" % (lr,))
+            d.lr_device, d.lr = None, lr
+        d.step = self.steps + 1
+
+        def call(raw):
+            if step is None and torch.cuda.is_current_stream_capturing():
+                raise ValueError("a captured step would keep its number: give step, a CUDA tensor")
+            dense = [g if g is None or g.is_contiguous() else g.contiguous() for g in grads]
+            at = _pointers([0 if g is None else g.data_ptr() for g in dense])
+            to = _pointers(self._at)
+            st = lib().ct_adamw(d, len(dense), self._table, to.buffer_info()[0], at.buffer_info()[0],
+                                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), _addr(self.exp_avg_scale),
+                                _addr(self.exp_avg_sq_scale), _addr(self.master), raw)
+            if st != CT_OK:
+                raise CtError(st, "ct_adamw")
+
+        _run_on(call, self.exp_avg, stream)
+        if step is None:
+            self.steps += 1
+        torch.autograd.graph.increment_version(params)
