@@ -57,6 +57,15 @@ __device__ __forceinline__ float to_grid(float x, uint32_t random) {
     return copysignf(b, x);
 }
 
+// a / b from b's rounded reciprocal, corrected by the remainder: correctly
+// rounded (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990) where nothing underflows; two operations more
+// than the product, where a division would take ten.
+__device__ __forceinline__ float quotient(float a, float b, float reciprocal) {
+    const float q = a * reciprocal;
+    return fmaf(fmaf(-q, b, a), reciprocal, q);
+}
+
 __device__ __forceinline__ void from_codes(uint2 w, float scale, float (&f)[8]) {
     const uint32_t word[2] = {w.x, w.y};
 #pragma unroll
@@ -135,10 +144,13 @@ __global__ void __launch_bounds__(kThreads)
         float root[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            // each operation rounded, as the formulas stand: what 8-bit codes are
+            // chosen by is then the same wherever it is computed in fp32
             const float a = g[j] * gs;
-            m[j] = fmaf(p.beta1, m[j], p.rest1 * a);
-            v[j] = fmaf(p.beta2, v[j], p.rest2 * (a * a));
-            asm("sqrt.approx.f32 %0, %1;" : "=f"(root[j]) : "f"(v[j]));     // to 2^-23
+            m[j] = __fadd_rn(__fmul_rn(p.beta1, m[j]), __fmul_rn(p.rest1, a));
+            v[j] = __fadd_rn(__fmul_rn(p.beta2, v[j]), __fmul_rn(p.rest2, __fmul_rn(a, a)));
+            if (BITS == 8) root[j] = __fsqrt_rn(v[j]);
+            else asm("sqrt.approx.f32 %0, %1;" : "=f"(root[j]) : "f"(v[j]));     // to 2^-23
             w[j] -= fmaf(lr_wd, w[j], s.lr_c1 * __fdividef(m[j], fmaf(root[j], s.root_c2, p.eps)));
         }
         if (master) {
@@ -161,8 +173,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t r = j & 1 ? bits[j / 2] >> 16 : bits[j / 2] & 0xFFFFu;
-                m[j] = to_grid(m[j] * im, r);
-                const float c = to_grid(root[j] * iv, r);
+                m[j] = to_grid(quotient(m[j], sm, im), r);
+                const float c = to_grid(quotient(root[j], sv, iv), r);
                 v[j] = root[j] > 0.f ? fmaxf(c, kLeastCode) : c;
             }
             *reinterpret_cast<uint2 *>((uint8_t *)p.m + in * kBlock + lane * 8) =

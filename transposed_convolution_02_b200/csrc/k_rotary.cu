@@ -8,6 +8,8 @@
 // turns in 64 bits, where a position of 2^31 still keeps its fraction of a
 // turn to 2^-22, reduced to half a turn and rounded; sincospi takes it from
 // there.  That is some 40 operations a pair, for all heads together.
+#include <type_traits>
+
 #include "ct_cuda_util.h"
 #include "rotary.h"
 #include "vec16.cuh"
@@ -19,13 +21,22 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kHeads = 4;        // of a thread, in flight
 
+// E elements as they are loaded: a 16-byte vector, or one element.
 template <typename T, int E>
-__device__ __forceinline__ void load_e(const T *p, float (&f)[E]) {
+using Raw = std::conditional_t<E == 1, T, uint4>;
+
+template <typename T, int E>
+__device__ __forceinline__ Raw<T, E> load_raw(const T *p) {
+    return *reinterpret_cast<const Raw<T, E> *>(p);
+}
+
+template <typename T, int E>
+__device__ __forceinline__ void of_raw(const Raw<T, E> &r, float (&f)[E]) {
     if constexpr (E == 1) {
-        f[0] = to_f<T>(*p);
+        f[0] = to_f<T>(r);
     } else {
         float2 v[E / 2];
-        unpack(*reinterpret_cast<const uint4 *>(p), v, T());
+        unpack(r, v, T());
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) f[2 * j] = v[j].x, f[2 * j + 1] = v[j].y;
     }
@@ -43,16 +54,39 @@ __device__ __forceinline__ void store_e(T *p, const float (&f)[E]) {
     }
 }
 
-// The position of pixel s of image n on an axis.
-__device__ __forceinline__ double position(const RotaryParams &p, int64_t n, int64_t s, int axis) {
+// The position of pixel s of image n on each axis.
+__device__ __forceinline__ void positions_of(const RotaryParams &p, int64_t n, int64_t s, double (&at)[3]) {
+    at[0] = at[1] = at[2] = 0.0;
     if (p.pos_type == CT_POSITION_GRID) {
-        for (int a = p.axes - 1; a > axis; --a) s /= p.grid[a];
-        return (double)(s % p.grid[axis]);
+        if (p.S <= 0xFFFFFFFFll) {
+            uint32_t r = (uint32_t)s;
+#pragma unroll
+            for (int a = 2; a > 0; --a)
+                if (a < p.axes) {
+                    const uint32_t q = r / (uint32_t)p.grid[a];
+                    at[a] = (double)(r - q * (uint32_t)p.grid[a]);
+                    r = q;
+                }
+            at[0] = (double)r;
+        } else {
+#pragma unroll
+            for (int a = 2; a > 0; --a)
+                if (a < p.axes) {
+                    at[a] = (double)(s % p.grid[a]);
+                    s /= p.grid[a];
+                }
+            at[0] = (double)s;
+        }
+        return;
     }
-    const int64_t i = n * p.pos_image + s * p.axes + axis;
-    if (p.pos_type == CT_POSITION_I32) return (double)((const int32_t *)p.positions)[i];
-    if (p.pos_type == CT_POSITION_I64) return (double)((const int64_t *)p.positions)[i];
-    return (double)((const float *)p.positions)[i];
+    const int64_t i = n * p.pos_image + s * p.axes;
+#pragma unroll
+    for (int a = 0; a < 3; ++a)
+        if (a < p.axes) {
+            if (p.pos_type == CT_POSITION_I32) at[a] = (double)((const int32_t *)p.positions)[i + a];
+            else if (p.pos_type == CT_POSITION_I64) at[a] = (double)((const int64_t *)p.positions)[i + a];
+            else at[a] = (double)((const float *)p.positions)[i + a];
+        }
 }
 
 // E: elements of a vector (1: none).  An item of a head is
@@ -84,12 +118,16 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int first = item * P;                       // pair
     const bool turns = item < turned;
     float c[P], d[P];
+    double where[3];
+    positions_of(p, n, s, where);
 #pragma unroll
     for (int j = 0; j < P; ++j) {
         const int q = first + j;
         if (turns && q < half) {
-            const int axis = p.axes > 2 && q >= p.first[2] ? 2 : p.axes > 1 && q >= p.first[1] ? 1 : 0;
-            const double t = position(p, n, s, axis) * p.turns[q];
+            double t = where[0];
+            if (p.axes > 1 && q >= p.first[1]) t = where[1];
+            if (p.axes > 2 && q >= p.first[2]) t = where[2];
+            t *= p.turns[q];
             sincospif(2.f * (float)(t - rint(t)), &d[j], &c[j]);
             d[j] *= p.sign;
         }
@@ -102,38 +140,41 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     T *y = (T *)p.y + n * p.ys[0] + s * p.ys[1] + at;
     const int64_t h0 = (int64_t)group * p.per, h1 = h0 + p.per < p.H ? h0 + p.per : p.H;
     for (int64_t h = h0; h < h1; h += kHeads) {
-        float a[kHeads][E], b[kHeads][kTwo ? E : 1];
+        Raw<T, E> ra[kHeads], rb[kTwo ? kHeads : 1];
 #pragma unroll
         for (int u = 0; u < kHeads; ++u)
             if (h + u < h1) {
-                load_e<T, E>(x + (h + u) * p.xs[2], a[u]);
+                ra[u] = load_raw<T, E>(x + (h + u) * p.xs[2]);
                 if constexpr (kTwo)
-                    if (turns) load_e<T, E>(x + (h + u) * p.xs[2] + over, b[u]);
+                    if (turns) rb[u] = load_raw<T, E>(x + (h + u) * p.xs[2] + over);
             }
 #pragma unroll
         for (int u = 0; u < kHeads; ++u)
             if (h + u < h1) {
                 T *out = y + (h + u) * p.ys[2];
+                float a[E], b[E];
+                of_raw<T, E>(ra[u], a);
                 if constexpr (kTwo) {
                     if (turns) {
+                        of_raw<T, E>(rb[u], b);
 #pragma unroll
                         for (int j = 0; j < E; ++j) {
-                            const float v = a[u][j], w = b[u][j];
-                            a[u][j] = fmaf(v, c[j], -(w * d[j]));
-                            b[u][j] = fmaf(v, d[j], w * c[j]);
+                            const float v = a[j], w = b[j];
+                            a[j] = fmaf(v, c[j], -(w * d[j]));
+                            b[j] = fmaf(v, d[j], w * c[j]);
                         }
-                        store_e<T, E>(out + over, b[u]);
+                        store_e<T, E>(out + over, b);
                     }
                 } else if (turns) {
 #pragma unroll
                     for (int j = 0; j < P; ++j)
                         if (first + j < half) {
-                            const float v = a[u][2 * j], w = a[u][2 * j + 1];
-                            a[u][2 * j] = fmaf(v, c[j], -(w * d[j]));
-                            a[u][2 * j + 1] = fmaf(v, d[j], w * c[j]);
+                            const float v = a[2 * j], w = a[2 * j + 1];
+                            a[2 * j] = fmaf(v, c[j], -(w * d[j]));
+                            a[2 * j + 1] = fmaf(v, d[j], w * c[j]);
                         }
                 }
-                store_e<T, E>(out, a[u]);
+                store_e<T, E>(out, a);
             }
     }
 }
