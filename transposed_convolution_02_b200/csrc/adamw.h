@@ -14,7 +14,8 @@
 namespace ct {
 
 constexpr int kBlock = 256;           // elements under one scale of 8-bit states
-constexpr int kFewTensors = 32;       // of a launch's table: two sizes, 1.8 KB and 28 KB of arguments
+constexpr int kFewTensors = 32;       // of a launch's table, three sizes: 1.8, 7 and 28 KB of arguments
+constexpr int kSomeTensors = 128;
 constexpr int kManyTensors = 512;
 constexpr int kNormBlocks = 148 * 8;  // of a launch of the norm: partial sums, whatever the device
 

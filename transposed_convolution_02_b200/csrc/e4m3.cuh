@@ -18,7 +18,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax / kE4m3Max, kLeastScale); }
+__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kE4m3Max), kLeastScale); }
 
 // Two codes, to nearest even, at most 448 in magnitude (x in the low byte).
 __device__ __forceinline__ uint32_t codes2(float x, float y) {

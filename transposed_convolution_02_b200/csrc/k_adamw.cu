@@ -18,6 +18,8 @@
 // becomes no code of 0, which would divide m by eps.
 #include <math.h>
 
+#include <type_traits>
+
 #include "adamw.h"
 #include "ct_cuda_util.h"
 #include "e4m3.cuh"
@@ -29,8 +31,6 @@ namespace ct {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr float kLow = 0.015625f;        // 2^-6: below it codes lie 2^-9 apart
-constexpr float kLeastCode = 0.001953125f;   // 2^-9
 
 template <int N>
 __device__ __forceinline__ int find(const TensorTable<N> &table, int64_t block) {
@@ -43,49 +43,67 @@ __device__ __forceinline__ int find(const TensorTable<N> &table, int64_t block) 
     return lo;
 }
 
-// x to e4m3's grid, up or down as 16 random bits say: they are added where the
-// mantissa's three bits end, and what lies below those is cut off.  (The 4 bits
-// below the random ones are dropped: 2^-16 of a step.)  Below 2^-6 values are
-// moved to where codes lie as far apart.  NaN stays; what passes 448 is cut by
-// the conversion.
-__device__ __forceinline__ float to_grid(float x, uint32_t random) {
-    const float a = fabsf(x);
-    const bool low = a < kLow;
-    float b = low ? a + kLow : a;
-    b = __uint_as_float((__float_as_uint(b) + (random << 4)) & ~0xFFFFFu);
-    b = low ? b - kLow : b;
-    return copysignf(b, x);
+// The e4m3 code of |x| (at most 448), up or down as 16 random bits say, in
+// bits 24 to 30.  x * 2^-120 has e4m3's exponents as its own, and its values
+// below 2^-6 among fp32's numbers without one: its bits are the code from 20
+// on, with the part that lies beyond it below.  Shifted up by 4 (the sign is
+// gone), they take the random bits (8 to 23) and carry.  (The lowest 4 bits are
+// dropped: 2^-16 of a step.)
+__device__ __forceinline__ uint32_t code_of(float x, uint32_t random) {
+    return min((__float_as_uint(x) << 4) + random, 0x7EFFFFFFu);
+}
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 // a / b from b's rounded reciprocal, corrected by the remainder: correctly
 // rounded (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990) where nothing underflows; two operations more
 // than the product, where a division would take ten.
-__device__ __forceinline__ float quotient(float a, float b, float reciprocal) {
-    const float q = a * reciprocal;
-    return fmaf(fmaf(-q, b, a), reciprocal, q);
+__device__ __forceinline__ float2 quotient(float2 a, float minus_b, float reciprocal) {
+    const float2 r = make_float2(reciprocal, reciprocal), q = __fmul2_rn(a, r);
+    return __ffma2_rn(__ffma2_rn(q, make_float2(minus_b, minus_b), a), r, q);
 }
 
-__device__ __forceinline__ void from_codes(uint2 w, float scale, float (&f)[8]) {
+// The roots of v >= 0: the estimate of 22 bits and a step of Heron's iteration,
+// which leaves 2^-44 before the rounding.  0 is its own root; infinity and NaN
+// give NaN; below 2^-126, where v holds but a few bits, roots come out smaller.
+__device__ __forceinline__ float2 root_of(float2 v) {
+    float2 r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(v.x, kLeastScale)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(v.y, kLeastScale)));
+    const float2 s = __fmul2_rn(v, r);
+    const float2 rest = __ffma2_rn(make_float2(-s.x, -s.y), s, v);
+    return __ffma2_rn(rest, __fmul2_rn(r, make_float2(0.5f, 0.5f)), s);
+}
+
+__device__ __forceinline__ float reciprocal(float v) {      // to 1 step; v is normal
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ void from_codes(uint2 w, float scale, float2 (&f)[4]) {
     const uint32_t word[2] = {w.x, w.y};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const __nv_fp8x2_storage_t two = (__nv_fp8x2_storage_t)(word[j / 2] >> (16 * (j & 1)));
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        f[2 * j] = v.x * scale;
-        f[2 * j + 1] = v.y * scale;
+        f[j] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&h)), make_float2(scale, scale));
     }
 }
 
 // The scale of a warp's 256 values (magnitudes compare as whole numbers, NaN
-// above all) and its reciprocal.
-__device__ __forceinline__ float warp_scale(const float (&f)[8]) {
+// above all).
+__device__ __forceinline__ float warp_scale(const float2 (&f)[4]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-    return scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)));
+    for (int j = 0; j < 4; ++j)
+        m = max(m, max(__float_as_uint(fabsf(f[j].x)), __float_as_uint(fabsf(f[j].y))));
+    return max_nan(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)) / kE4m3Max, kLeastScale);
 }
+
+__device__ __forceinline__ float2 twice(float f) { return make_float2(f, f); }
 
 struct Step {
     float lr, lr_c1, root_c2;
@@ -102,7 +120,7 @@ __device__ __forceinline__ Step step_of(const AdamWParams &p, uint64_t t) {
 }
 
 template <int BITS, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     adamw_kernel(const __grid_constant__ TensorTable<N> table, const __grid_constant__ AdamWParams p, int per) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t block = (int64_t)blockIdx.x * kWarps * per + warp;
@@ -120,7 +138,7 @@ __global__ void __launch_bounds__(kThreads)
         const int n = e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0;
         const uint32_t pd = e.kind & 3, gd = (e.kind >> 2) & 3;
         float *master = pd != CT_F32 ? p.master + (e.master + block - e.first) * kBlock + lane * 8 : nullptr;
-        float g[8], w[8], m[8], v[8];
+        float2 g[4], w[4], m[4], v[4], root[4];
         load8(e.grad, gd, at, n, e.kind & kGradVec, g);
         if (master) load8_f32(master, w);
         else load8(e.param, CT_F32, at, n, e.kind & kParamVec, w);
@@ -133,25 +151,27 @@ __global__ void __launch_bounds__(kThreads)
             from_codes(cm, p.m_scale[in], m);
             from_codes(cv, p.v_scale[in], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= v[j];
+            for (int j = 0; j < 4; ++j) v[j] = __fmul2_rn(v[j], v[j]);
         }
         if (n < 8) {         // what lies behind the tensor in its last block counts for nothing, and becomes 0
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j >= n) w[j] = m[j] = v[j] = 0.f;
+            for (int j = 0; j < 4; ++j) {
+                if (2 * j >= n) w[j].x = m[j].x = v[j].x = 0.f;
+                if (2 * j + 1 >= n) w[j].y = m[j].y = v[j].y = 0.f;
+            }
         }
-        const float lr_wd = s.lr * e.decay;
-        float root[8];
+        const float decay = s.lr * e.decay;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
             // each operation rounded, as the formulas stand: what 8-bit codes are
             // chosen by is then the same wherever it is computed in fp32
-            const float a = g[j] * gs;
-            m[j] = __fadd_rn(__fmul_rn(p.beta1, m[j]), __fmul_rn(p.rest1, a));
-            v[j] = __fadd_rn(__fmul_rn(p.beta2, v[j]), __fmul_rn(p.rest2, __fmul_rn(a, a)));
-            if (BITS == 8) root[j] = __fsqrt_rn(v[j]);
-            else asm("sqrt.approx.f32 %0, %1;" : "=f"(root[j]) : "f"(v[j]));     // to 2^-23
-            w[j] -= fmaf(lr_wd, w[j], s.lr_c1 * __fdividef(m[j], fmaf(root[j], s.root_c2, p.eps)));
+            const float2 a = __fmul2_rn(g[j], twice(gs));
+            m[j] = __fadd2_rn(__fmul2_rn(m[j], twice(p.beta1)), __fmul2_rn(a, twice(p.rest1)));
+            v[j] = __fadd2_rn(__fmul2_rn(v[j], twice(p.beta2)), __fmul2_rn(__fmul2_rn(a, a), twice(p.rest2)));
+            root[j] = root_of(v[j]);
+            const float2 d = __ffma2_rn(root[j], twice(s.root_c2), twice(p.eps));
+            const float2 u = __fmul2_rn(__fmul2_rn(m[j], make_float2(reciprocal(d.x), reciprocal(d.y))), twice(-s.lr_c1));
+            w[j] = __fadd2_rn(w[j], __ffma2_rn(w[j], twice(-decay), u));
         }
         if (master) {
             store8_f32(master, w);
@@ -170,17 +190,23 @@ __global__ void __launch_bounds__(kThreads)
             philox.c3 = (uint32_t)(t >> 32);
             const uint4 d = philox((uint64_t)(in * (kBlock / 8) + lane));
             const uint32_t bits[4] = {d.x, d.y, d.z, d.w};
+            uint32_t cm[8], cv[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t r = j & 1 ? bits[j / 2] >> 16 : bits[j / 2] & 0xFFFFu;
-                m[j] = to_grid(quotient(m[j], sm, im), r);
-                const float c = to_grid(quotient(root[j], sv, iv), r);
-                v[j] = root[j] > 0.f ? fmaxf(c, kLeastCode) : c;
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t r0 = __byte_perm(bits[j], 0, 0x4104), r1 = __byte_perm(bits[j], 0, 0x4324);
+                const float2 down = twice(0x1p-120f);
+                const float2 x = __fmul2_rn(quotient(m[j], -sm, im), down);
+                const float2 y = __fmul2_rn(quotient(root[j], -sv, iv), down);
+                cm[2 * j] = code_of(x.x, r0) | (__float_as_uint(x.x) & 0x80000000u);
+                cm[2 * j + 1] = code_of(x.y, r1) | (__float_as_uint(x.y) & 0x80000000u);
+                // a root above 0 has bits above 1 << 24
+                cv[2 * j] = max(code_of(y.x, r0), min(__float_as_uint(root[j].x), 1u << 24));
+                cv[2 * j + 1] = max(code_of(y.y, r1), min(__float_as_uint(root[j].y), 1u << 24));
             }
             *reinterpret_cast<uint2 *>((uint8_t *)p.m + in * kBlock + lane * 8) =
-                make_uint2(codes4(m[0], m[1], m[2], m[3]), codes4(m[4], m[5], m[6], m[7]));
+                make_uint2(top_bytes(cm[0], cm[1], cm[2], cm[3]), top_bytes(cm[4], cm[5], cm[6], cm[7]));
             *reinterpret_cast<uint2 *>((uint8_t *)p.v + in * kBlock + lane * 8) =
-                make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
+                make_uint2(top_bytes(cv[0], cv[1], cv[2], cv[3]), top_bytes(cv[4], cv[5], cv[6], cv[7]));
             if (lane == 0) {
                 p.m_scale[in] = sm;
                 p.v_scale[in] = sv;
@@ -208,11 +234,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
             const TensorEntry &e = table.t[i];
             const int64_t at = (block - e.first) * kBlock + lane * 8;
             const int n = e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0;
-            float g[8], q = 0.f;
+            float2 g[4], q = make_float2(0.f, 0.f);
             load8(e.grad, (e.kind >> 2) & 3, at, n, e.kind & kGradVec, g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) q = fmaf(g[j], g[j], q);
-            sum += (double)q;
+            for (int j = 0; j < 4; ++j) q = __ffma2_rn(g[j], g[j], q);
+            sum += (double)(q.x + q.y);
         }
     }
     for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -325,6 +351,14 @@ ct_status norm_tables(int64_t count, const ct_param *shapes, const void *const *
     return CT_OK;
 }
 
+// f(N): the smallest table that holds `count` tensors, or the largest.
+template <typename F>
+ct_status by_count(int64_t count, F f) {
+    if (count <= kFewTensors) return f(std::integral_constant<int, kFewTensors>());
+    if (count <= kSomeTensors) return f(std::integral_constant<int, kSomeTensors>());
+    return f(std::integral_constant<int, kManyTensors>());
+}
+
 }  // namespace
 
 ct_status adamw_run(const ct_adamw_desc *d, int64_t count, const ct_param *shapes, void *const *params,
@@ -343,17 +377,18 @@ ct_status adamw_run(const ct_adamw_desc *d, int64_t count, const ct_param *shape
     p.step = (uint64_t)d->step;
     p.rng.seed = d->seed;
     set_keys(p.rng);
-    if (d->bits == 32)
-        return count <= kFewTensors ? adamw_tables<32, kFewTensors>(count, shapes, params, grads, p, st)
-                                    : adamw_tables<32, kManyTensors>(count, shapes, params, grads, p, st);
-    return count <= kFewTensors ? adamw_tables<8, kFewTensors>(count, shapes, params, grads, p, st)
-                                : adamw_tables<8, kManyTensors>(count, shapes, params, grads, p, st);
+    return by_count(count, [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        return d->bits == 32 ? adamw_tables<32, N>(count, shapes, params, grads, p, st)
+                             : adamw_tables<8, N>(count, shapes, params, grads, p, st);
+    });
 }
 
 ct_status grad_norm_run(int64_t count, const ct_param *shapes, const void *const *grads, double max_norm, float *norm,
                         float *scale, double *ws, cudaStream_t st) {
-    return count <= kFewTensors ? norm_tables<kFewTensors>(count, shapes, grads, max_norm, norm, scale, ws, st)
-                                : norm_tables<kManyTensors>(count, shapes, grads, max_norm, norm, scale, ws, st);
+    return by_count(count, [&](auto n) {
+        return norm_tables<decltype(n)::value>(count, shapes, grads, max_norm, norm, scale, ws, st);
+    });
 }
 
 }  // namespace ct

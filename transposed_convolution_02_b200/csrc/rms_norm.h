@@ -35,7 +35,14 @@ struct RmsGeom {
     int tpr;        // threads per row
     int threads;    // per block
     int64_t blocks;
+    int64_t ring;   // blocks of the forward kernel that stays for many rows; 0: there are few
 };
+
+// Rows of the backward ring for K vectors a thread.
+constexpr int rms_stages(int K) { return K <= 2 ? 4 : K <= 4 ? 2 : 1; }
+
+constexpr int rms_forward_stages(int K) { return K <= 2 ? 4 : 3; }
+constexpr int kRmsFewElements = 16;     // of a thread, with which a forward block may have 1024
 
 constexpr int64_t kRmsMaxC = int64_t(1) << 24;
 

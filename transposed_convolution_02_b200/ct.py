@@ -753,14 +753,15 @@ def _rms_of(x, weight, block, eps):
             _RMS.clear()
         _RMS[key] = r
         return r
-    if weight is not None and (weight.dim() != 1 or weight.numel() != r.c or weight.device != x.device):
+    if weight is not None and (weight.dim() != 1 or weight.numel() != r.c or weight.get_device() != x.get_device()):
         check_rms(x, weight, block)
     return r
 
 
-def _rms_inputs(x, weight, residual, outs):
+def _rms_inputs(x, weight, residual, *outs):
     """Checks of both forward calls; `outs` may be X or the residual."""
-    if residual is not None:
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype
+                                 or residual.get_device() != x.get_device()):
         check_like(residual, "residual", x)
     for t in outs:
         if t is not None:
@@ -784,7 +785,7 @@ def rms_norm_nhwc(x, weight=None, *, eps=1e-6, residual=None, out=None, sum_out=
     r = _rms_of(x, weight, 0, eps)
     if sum_out is not None and residual is None:
         raise ValueError("sum_out needs a residual")
-    _rms_inputs(x, weight, residual, (out, sum_out))
+    _rms_inputs(x, weight, residual, out, sum_out)
 
     def call(raw):
         xc = x.contiguous()
@@ -818,7 +819,7 @@ def rms_norm_nhwc_e4m3(x, weight=None, *, block=None, eps=1e-6, residual=None, s
     r = _rms_of(x, weight, 0 if block is None else block, eps)
     if sum_out is not None and residual is None:
         raise ValueError("sum_out needs a residual")
-    _rms_inputs(x, weight, residual, (sum_out,))
+    _rms_inputs(x, weight, residual, sum_out)
 
     def call(raw):
         xc = x.contiguous()
@@ -931,61 +932,64 @@ def check_rotary(x, sections, base, pairs, positions):
                          % (list(want), [x.shape[0]] + list(want), x.device))
 
 
+class _Rotary:
+    """A rotation's descriptor, for one set of sizes, types and strides."""
+
+    def __init__(self, x, out, sections, base, pairs, positions, inverse):
+        check_rotary(x, sections, base, pairs, positions)
+        xs = _head_strides(x.shape, x.stride())
+        self.copy = xs is None          # X is copied first, to dense heads
+        dense = torch.empty(x.shape, device="meta").stride()
+        if xs is None:
+            xs = _head_strides(x.shape, dense)
+        ys = _head_strides(x.shape, dense if out is None else out.stride())
+        if ys is None:
+            raise ValueError("out's pixels must be one stride apart, and a head's elements neighbours")
+        d = self.desc = ct_rotary_desc(NORM_DTYPE[x.dtype], len(sections), PAIRS[pairs], inverse)
+        d.N, d.heads, d.dim, d.base = x.shape[0], x.shape[-2], x.shape[-1], float(base)
+        grid = list(x.shape[1:-2])
+        if positions is not None:
+            d.position_type = POSITION_DTYPE[positions.dtype]
+            d.position_images = int(positions.dim() == x.dim() - 1)
+            grid = [math.prod(grid)] + [1] * (len(sections) - 1)
+        for a, v in enumerate(sections):
+            d.grid[a], d.sections[a] = grid[a], int(v)
+        for a in range(3):
+            d.x_strides[a], d.y_strides[a] = xs[a], ys[a]
+
+
 _ROTARY = {}
 
 
-def _rotary_of(x, xs, ys, sections, base, pairs, positions, inverse):
-    """The checked arguments' descriptor (made once per sizes and types)."""
-    pos = None if positions is None else (positions.dtype, positions.shape, positions.device == x.device)
-    key = (x.shape, x.dtype, xs, ys, tuple(sections), base, pairs, pos, inverse)
-    try:
-        return _ROTARY[key]
-    except (KeyError, TypeError):
-        pass
-    d = ct_rotary_desc(NORM_DTYPE[x.dtype], len(sections), PAIRS[pairs], inverse)
-    d.N, d.heads, d.dim, d.base = x.shape[0], x.shape[-2], x.shape[-1], float(base)
-    grid = list(x.shape[1:-2])
-    if positions is not None:
-        d.position_type = POSITION_DTYPE[positions.dtype]
-        d.position_images = int(positions.dim() == x.dim() - 1)
-        grid = [math.prod(grid)] + [1] * (len(sections) - 1)
-    for a, v in enumerate(sections):
-        d.grid[a], d.sections[a] = grid[a], int(v)
-    for a in range(3):
-        d.x_strides[a], d.y_strides[a] = xs[a], ys[a]
-    if len(_ROTARY) >= 1024:
-        _ROTARY.clear()
-    _ROTARY[key] = d
-    return d
-
-
 def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
-    check_rotary(x, sections, base, pairs, positions)
-    xs = _head_strides(x.shape, x.stride())
-    ys = None
     if out is not None:
         check_like(out, "out", x)
-        ys = _head_strides(out.shape, out.stride())
-        if ys is None:
-            raise ValueError("out's pixels must be one stride apart, and a head's elements neighbours")
+    key = (x.shape, x.stride(), x.dtype, tuple(sections), base, pairs, inverse,
+           None if out is None else out.stride(), None if positions is None else (positions.shape, positions.dtype))
+    try:
+        r = _ROTARY[key]
+    except (KeyError, TypeError):
+        r = _Rotary(x, out, sections, base, pairs, positions, inverse)
+        if len(_ROTARY) >= 1024:
+            _ROTARY.clear()
+        _ROTARY[key] = r
+    if positions is not None and positions.device != x.device:
+        check_rotary(x, sections, base, pairs, positions)
+    if out is not None:
         o0, o1 = _extent(out)
         for t in (x, positions):
             if t is None or t.numel() == 0:
                 continue
             t0, t1 = _extent(t)
-            if t0 < o1 and o0 < t1 and not (t is x and xs == ys and t0 == o0):
+            if t0 < o1 and o0 < t1 and not (t is x and t0 == o0 and x.stride() == out.stride()):
                 raise ValueError("out overlaps an input")
     _check_cuda(x, positions)
 
     def call(raw):
-        xc, sx = (x, xs) if xs is not None else (x.contiguous(), None)
-        if sx is None:
-            sx = _head_strides(xc.shape, xc.stride())
+        xc = x.contiguous() if r.copy else x
         pos = None if positions is None else positions.contiguous()
         y = torch.empty(xc.shape, dtype=xc.dtype, device=xc.device) if out is None else out
-        sy = _head_strides(y.shape, y.stride()) if ys is None else ys
-        d = _rotary_of(xc, sx, sy, sections, base, pairs, pos, inverse)
-        st = lib().ct_rotary(d, xc.data_ptr(), _addr(pos), y.data_ptr(), raw)
+        st = lib().ct_rotary(r.desc, xc.data_ptr(), _addr(pos), y.data_ptr(), raw)
         if st != CT_OK:
             raise CtError(st, "ct_rotary")
         return y
@@ -1020,6 +1024,13 @@ def rotary_nhwc_backward(dy, sections, *, base=10000.0, pairs="adjacent", positi
 BLOCK = 256     # elements of a block of AdamW's states
 
 
+# What a step asks of each of its tensors, as functions that map() runs over a
+# list: a step of dozens of small tensors is bound by these questions.
+_shape, _dtype = torch.Tensor.shape.__get__, torch.Tensor.dtype.__get__
+_numel, _device, _dense, _where = (torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous,
+                                   torch.Tensor.data_ptr)
+
+
 def _pointers(addresses):
     """A host array of device addresses (keep it while its address is used)."""
     return array.array("Q", addresses)
@@ -1030,7 +1041,7 @@ def _check_grad(g, name):
         raise ValueError("%s must be a CUDA tensor" % name)
     if g.dtype not in NORM_DTYPE:
         raise ValueError("%s must be float32, float16 or bfloat16, not %s" % (name, g.dtype))
-    if g.is_sparse or g.layout != torch.strided:
+    if g.layout != torch.strided:
         raise ValueError("%s must be a dense tensor" % name)
 
 
@@ -1040,7 +1051,7 @@ _GRADS = {}
 def _grads_of(grads):
     """The descriptors of gradients that lie on one device, and the workspace's
     size (made once per sizes and types)."""
-    key = tuple([(g.numel(), g.dtype, g.get_device(), g.layout) for g in grads])
+    key = (tuple(map(_numel, grads)), tuple(map(_dtype, grads)), tuple(map(_device, grads)))
     try:
         return _GRADS[key]
     except KeyError:
@@ -1077,8 +1088,8 @@ def grad_norm(grads, max_norm=None, *, stream=None):
     shapes, bytes_ = _grads_of(grads)
 
     def call(raw):
-        dense = [g if g.is_contiguous() else g.contiguous() for g in grads]
-        at = _pointers([g.data_ptr() for g in dense])
+        dense = grads if all(map(_dense, grads)) else [g.contiguous() for g in grads]
+        at = _pointers(map(_where, dense))
         dev = grads[0].device
         out = torch.empty(2, dtype=torch.float32, device=dev)
         ws = torch.empty(bytes_, dtype=torch.uint8, device=dev)
@@ -1202,13 +1213,15 @@ class AdamW:
         params = self.params
         if len(grads) != len(params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(params)))
-        meta = [None if g is None else (g.shape, g.dtype, g.get_device(), g.layout) for g in grads]
-        if meta != self._meta:
+        try:
+            meta = [list(map(_shape, grads)), list(map(_dtype, grads)), list(map(_device, grads))]
+        except TypeError:       # None entries
+            meta = None
+        if meta is None or meta != self._meta:
             self._meta = None
             self._grads(grads)
             self._meta = meta
-        if ([p.data_ptr() for p in params] != self._at or [p.numel() for p in params] != self._sizes
-                or [p.dtype for p in params] != self._dtypes or not all([p.is_contiguous() for p in params])):
+        if list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes:
             self._at = self._places()
         d, lr = self._desc, self.lr
         d.grad_scale = None if grad_scale is None else self._scalar(grad_scale, "grad_scale", torch.float32)
@@ -1224,8 +1237,12 @@ class AdamW:
         def call(raw):
             if step is None and torch.cuda.is_current_stream_capturing():
                 raise ValueError("a captured step would keep its number: give step, a CUDA tensor")
-            dense = [g if g is None or g.is_contiguous() else g.contiguous() for g in grads]
-            at = _pointers([0 if g is None else g.data_ptr() for g in dense])
+            if meta is None:
+                dense = [None if g is None else g.contiguous() for g in grads]
+                at = _pointers([0 if g is None else g.data_ptr() for g in dense])
+            else:
+                dense = grads if all(map(_dense, grads)) else [g.contiguous() for g in grads]
+                at = _pointers(map(_where, dense))
             to = _pointers(self._at)
             st = lib().ct_adamw(d, len(dense), self._table, to.buffer_info()[0], at.buffer_info()[0],
                                 self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), _addr(self.exp_avg_scale),
