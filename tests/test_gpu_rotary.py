@@ -103,6 +103,18 @@ def test_layouts(pairs, dtype):
         ct.rotary_nhwc(qkv, sections, out=torch.zeros(64, dtype=t, device="cuda").expand(qkv.shape))
 
 
+@pytest.mark.parametrize("base", [1e-4, 0.5, 1.0, 1e30])
+def test_bases(base):
+    """Frequencies above a turn a position, none that differ, and vanishing ones; positions around 2^24, where
+    floats stop holding them."""
+    x = normal([1, 9, 2, 40], 17)
+    for kind in (torch.int64, torch.float32):
+        at = torch.tensor([[0], [1], [77], [-1000], [(1 << 24) - 1], [1 << 24], [-(1 << 24) - 2], [(1 << 25) + 4],
+                           [1 << 30]], device="cuda").to(kind)
+        for pairs in ("adjacent", "halves"):
+            compare(x, [32], pairs, positions=at, base=base)
+
+
 def test_special_values():
     """Position 0 turns nothing, infinities and NaN stay in their pairs."""
     x = normal([1, 6, 2, 24], 21)

@@ -383,8 +383,19 @@ ct_status resolve_rotary(const ct_rotary_desc *d, RotaryParams *p) {
     for (int a = 0; a < d->axes; ++a) {
         const long double ratio = powl((long double)d->base, -2.0L / (long double)d->sections[a]);
         long double f = 1.0L / 6.283185307179586476925286766559L;
-        for (int64_t j = 0; j < d->sections[a] / 2; ++j, f *= ratio) p->turns[p->first[a] + j] = (double)f;
+        for (int64_t j = 0; j < d->sections[a] / 2; ++j, f *= ratio) {
+            const int64_t q = p->first[a] + j;
+            p->turns[q] = (double)f;
+            p->parts[q][0] = (float)p->turns[q];
+            p->parts[q][1] = (float)(p->turns[q] - (double)p->parts[q][0]);
+        }
     }
+    // 24 bits, and at most 2^22 turns, so that what is left of them has its bits
+    double fastest = 0.0;
+    for (int64_t q = 0; q < rot / 2; ++q) fastest = fmax(fastest, p->turns[q]);
+    p->near = (float)fmin(16777216.0, fastest > 0.0 ? 4194304.0 / fastest : 16777216.0);
+    p->small_grid = 1;
+    for (int a = 0; a < d->axes; ++a) p->small_grid = p->small_grid && (double)d->grid[a] <= (double)p->near;
     for (int a = 0; a < 3; ++a) {
         p->xs[a] = d->x_strides[a];
         p->ys[a] = d->y_strides[a];

@@ -5,9 +5,10 @@
 // Bound: HBM, x in and y out.  A thread has the pairs of one vector (or of two,
 // one in each half of the head) of one pixel, makes their sines and cosines
 // once and walks the heads with them in registers.  The angle is formed in
-// turns in 64 bits, where a position of 2^31 still keeps its fraction of a
-// turn to 2^-22, reduced to half a turn and rounded; sincospi takes it from
-// there.  That is some 40 operations a pair, for all heads together.
+// turns.  A position of up to 24 bits times a frequency of two floats (48 bits)
+// gives the fraction of a turn to 2^-26 in fp32: the product's rounding is known
+// exactly (fused multiply-add), and so is the part left of whole turns.  Larger
+// positions, and frequencies above a turn a position, take 64 bits.
 #include <type_traits>
 
 #include "ct_cuda_util.h"
@@ -19,7 +20,10 @@ namespace ct {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kHeads = 4;        // of a thread, in flight
+
+// Heads of a thread in flight: elements alone need more of them for the same bytes.
+template <int E>
+constexpr int kHeads = E == 1 ? 8 : 4;
 
 // E elements as they are loaded: a 16-byte vector, or one element.
 template <typename T, int E>
@@ -54,39 +58,101 @@ __device__ __forceinline__ void store_e(T *p, const float (&f)[E]) {
     }
 }
 
-// The position of pixel s of image n on each axis.
-__device__ __forceinline__ void positions_of(const RotaryParams &p, int64_t n, int64_t s, double (&at)[3]) {
-    at[0] = at[1] = at[2] = 0.0;
-    if (p.pos_type == CT_POSITION_GRID) {
-        if (p.S <= 0xFFFFFFFFll) {
-            uint32_t r = (uint32_t)s;
+// The position of pixel s of image n on each axis, as a float and, where that
+// does not hold it, in 64 bits.
+struct Positions {
+    float near[3];
+    double far[3];
+    bool is_far;
+};
+
+__device__ __forceinline__ void positions_of(const RotaryParams &p, int64_t n, int64_t s, Positions &at) {
+    at.is_far = false;
+    at.near[0] = at.near[1] = at.near[2] = 0.f;
+    if (p.pos_type == CT_POSITION_GRID && p.small && p.small_grid) {
+        int rest = (int)s;
 #pragma unroll
-            for (int a = 2; a > 0; --a)
-                if (a < p.axes) {
-                    const uint32_t q = r / (uint32_t)p.grid[a];
-                    at[a] = (double)(r - q * (uint32_t)p.grid[a]);
-                    r = q;
-                }
-            at[0] = (double)r;
-        } else {
+        for (int a = 2; a > 0; --a)
+            if (a < p.axes) {
+                const int q = divq(rest, p.by_grid[a]);
+                at.near[a] = (float)(rest - q * (int)p.grid[a]);
+                rest = q;
+            }
+        at.near[0] = (float)rest;
+        return;
+    }
+    if (p.pos_type == CT_POSITION_F32) {
+        const float *from = (const float *)p.positions + n * p.pos_image + s * p.axes;
 #pragma unroll
-            for (int a = 2; a > 0; --a)
-                if (a < p.axes) {
-                    at[a] = (double)(s % p.grid[a]);
-                    s /= p.grid[a];
-                }
-            at[0] = (double)s;
+        for (int a = 0; a < 3; ++a) {
+            if (a < p.axes) at.near[a] = from[a];
+            if (fabsf(at.near[a]) > p.near) at.is_far = true;
+            at.far[a] = (double)at.near[a];
         }
         return;
     }
-    const int64_t i = n * p.pos_image + s * p.axes;
+    int64_t whole[3] = {0, 0, 0};
+    if (p.pos_type == CT_POSITION_GRID) {
 #pragma unroll
-    for (int a = 0; a < 3; ++a)
-        if (a < p.axes) {
-            if (p.pos_type == CT_POSITION_I32) at[a] = (double)((const int32_t *)p.positions)[i + a];
-            else if (p.pos_type == CT_POSITION_I64) at[a] = (double)((const int64_t *)p.positions)[i + a];
-            else at[a] = (double)((const float *)p.positions)[i + a];
-        }
+        for (int a = 2; a > 0; --a)
+            if (a < p.axes) {
+                const int64_t q = s / p.grid[a];
+                whole[a] = s - q * p.grid[a];
+                s = q;
+            }
+        whole[0] = s;
+    } else {
+        const int64_t i = n * p.pos_image + s * p.axes;
+#pragma unroll
+        for (int a = 0; a < 3; ++a)
+            if (a < p.axes)
+                whole[a] = p.pos_type == CT_POSITION_I32 ? ((const int32_t *)p.positions)[i + a]
+                                                         : ((const int64_t *)p.positions)[i + a];
+    }
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+        at.near[a] = (float)whole[a];
+        if (fabsf(at.near[a]) > p.near || whole[a] > 16777216 || whole[a] < -16777216) at.is_far = true;
+    }
+    if (at.is_far)
+        for (int a = 0; a < 3; ++a) at.far[a] = (double)whole[a];
+}
+
+__device__ __forceinline__ float2 twice(float f) { return make_float2(f, f); }
+
+// Cosine and sine of two angles of f turns, |f| <= 1: to the nearest quarter
+// turn, and Taylor's polynomials of what is left, an eighth of a turn at most
+// (the first terms left out are below 2^-29).  Adding 3 * 2^22 rounds to a whole
+// number of quarters, which then are the sum's last bits.
+__device__ __forceinline__ void turn(float2 f, float2 &c, float2 &s) {
+    const float2 z = __ffma2_rn(f, twice(4.f), twice(12582912.f));
+    const float2 g = __ffma2_rn(__fadd2_rn(z, twice(-12582912.f)), twice(-0.25f), f);
+    const float2 x = __fmul2_rn(g, twice(6.2831853f)), q = __fmul2_rn(x, x);
+    float2 a = __ffma2_rn(q, twice(1.f / 362880), twice(-1.f / 5040));
+    a = __ffma2_rn(a, q, twice(1.f / 120));
+    a = __ffma2_rn(a, q, twice(-1.f / 6));
+    a = __ffma2_rn(__fmul2_rn(a, q), x, x);
+    float2 b = __ffma2_rn(q, twice(-1.f / 3628800), twice(1.f / 40320));
+    b = __ffma2_rn(b, q, twice(-1.f / 720));
+    b = __ffma2_rn(b, q, twice(1.f / 24));
+    b = __ffma2_rn(b, q, twice(-0.5f));
+    b = __ffma2_rn(b, q, twice(1.f));
+    auto place = [](uint32_t n, float sine, float cosine, float &to_c, float &to_s) {
+        const bool odd = n & 1;
+        const uint32_t high = n << 30, both = high ^ n << 31;      // bit 1 of n, and of n + 1, on top
+        to_s = __uint_as_float((high & 0x80000000u) ^ __float_as_uint(odd ? cosine : sine));
+        to_c = __uint_as_float((both & 0x80000000u) ^ __float_as_uint(odd ? sine : cosine));
+    };
+    place(__float_as_uint(z.x), a.x, b.x, c.x, s.x);
+    place(__float_as_uint(z.y), a.y, b.y, c.y, s.y);
+}
+
+// Positions times frequencies (as high and low parts) in turns, without the whole ones.
+__device__ __forceinline__ float2 turns_of(float2 pos, float2 hi, float2 lo) {
+    const float2 t = __fmul2_rn(pos, hi), minus = make_float2(-t.x, -t.y);
+    const float2 rest = __ffma2_rn(pos, lo, __ffma2_rn(pos, hi, minus));
+    const float2 whole = __fadd2_rn(__fadd2_rn(t, twice(12582912.f)), twice(-12582912.f));
+    return __fadd2_rn(__fadd2_rn(t, make_float2(-whole.x, -whole.y)), rest);
 }
 
 // E: elements of a vector (1: none).  An item of a head is
@@ -100,83 +166,113 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     constexpr bool kTwo = HALVES || E == 1;             // two loads
     const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (id >= p.threads) return;
-    int64_t row;
+    int64_t row, n, s;
     int item, group;
-    if (p.threads <= 0xFFFFFFFFll) {
-        const uint32_t r = (uint32_t)id / (uint32_t)p.items;
-        item = (int)((uint32_t)id - r * (uint32_t)p.items);
-        row = r / (uint32_t)p.groups;
-        group = (int)(r - (uint32_t)row * (uint32_t)p.groups);
+    if (p.small) {
+        const int r = divq((int)id, p.by_items), w = divq(r, p.by_groups), im = divq(w, p.by_s);
+        item = (int)id - r * p.items;
+        group = r - w * p.groups;
+        row = w;
+        n = im;
+        s = w - im * (int)p.S;
     } else {
         const int64_t r = id / p.items;
         item = (int)(id - r * p.items);
         row = r / p.groups;
         group = (int)(r - row * p.groups);
+        n = row / p.S;
+        s = row - n * p.S;
     }
-    const int64_t n = row / p.S, s = row - n * p.S;
     const int half = p.rot / 2, turned = kTwo ? half / E : (p.rot + E - 1) / E;    // items with a pair that turns
     const int first = item * P;                       // pair
     const bool turns = item < turned;
-    float c[P], d[P];
-    double where[3];
-    positions_of(p, n, s, where);
+    constexpr int Q = (P + 1) / 2;
+    float2 cs[Q], sn[Q];                              // two pairs together
+    if (turns) {
+        Positions where;
+        positions_of(p, n, s, where);
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int q = first + j;
-        if (turns && q < half) {
-            double t = where[0];
-            if (p.axes > 1 && q >= p.first[1]) t = where[1];
-            if (p.axes > 2 && q >= p.first[2]) t = where[2];
-            t *= p.turns[q];
-            sincospif(2.f * (float)(t - rint(t)), &d[j], &c[j]);
-            d[j] *= p.sign;
+        for (int j = 0; j < Q; ++j) {
+            const int q = first + 2 * j;
+            // P is even, but for single elements, whose second pair is no one's
+            const float4 f = P > 1 ? *reinterpret_cast<const float4 *>(p.parts[q])
+                                   : make_float4(p.parts[q][0], p.parts[q][1], 0.f, 0.f);
+            auto axis = [&](int i) { return p.axes > 1 && i >= p.first[1] ? p.axes > 2 && i >= p.first[2] ? 2 : 1 : 0; };
+            const int a0 = axis(q), a1 = axis(q + 1);
+            float2 r;
+            if (!where.is_far) {
+                const float2 pos = make_float2(a0 == 2 ? where.near[2] : a0 == 1 ? where.near[1] : where.near[0],
+                                               a1 == 2 ? where.near[2] : a1 == 1 ? where.near[1] : where.near[0]);
+                r = turns_of(pos, make_float2(f.x, f.z), make_float2(f.y, f.w));
+            } else {
+                const double t0 = (a0 == 2 ? where.far[2] : a0 == 1 ? where.far[1] : where.far[0]) * p.turns[q];
+                const double t1 = P == 1 ? 0.0 : (a1 == 2 ? where.far[2] : a1 == 1 ? where.far[1] : where.far[0]) *
+                                                     p.turns[q + 1];
+                r = make_float2((float)(t0 - rint(t0)), (float)(t1 - rint(t1)));
+            }
+            turn(r, cs[j], sn[j]);
+            sn[j] = __fmul2_rn(sn[j], twice(p.sign));
         }
     }
+    auto c = [&](int j) { return j & 1 ? cs[j / 2].y : cs[j / 2].x; };
+    auto d = [&](int j) { return j & 1 ? sn[j / 2].y : sn[j / 2].x; };
     // where the item's elements are in a head
     const int64_t at = turns ? (HALVES ? (int64_t)first : E == 1 ? 2 * (int64_t)first : (int64_t)item * E)
                              : kTwo ? p.rot + (int64_t)(item - turned) * E : (int64_t)item * E;
     const int64_t over = HALVES ? half : 1;
     const T *x = (const T *)p.x + n * p.xs[0] + s * p.xs[1] + at;
     T *y = (T *)p.y + n * p.ys[0] + s * p.ys[1] + at;
-    const int64_t h0 = (int64_t)group * p.per, h1 = h0 + p.per < p.H ? h0 + p.per : p.H;
-    for (int64_t h = h0; h < h1; h += kHeads) {
-        Raw<T, E> ra[kHeads], rb[kTwo ? kHeads : 1];
+    const int64_t h0 = (int64_t)group * p.per;
+    int left = p.H - h0 < p.per ? (int)(p.H - h0) : p.per;
+    x += h0 * p.xs[2];
+    y += h0 * p.ys[2];
+    const int64_t xh = p.xs[2], yh = p.ys[2];
+    // the next heads: all U of them there, or the `left` last ones
+    auto heads = [&](auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        constexpr int U = kHeads<E>;
+        Raw<T, E> ra[U], rb[kTwo ? U : 1];
+        const T *from = x;
 #pragma unroll
-        for (int u = 0; u < kHeads; ++u)
-            if (h + u < h1) {
-                ra[u] = load_raw<T, E>(x + (h + u) * p.xs[2]);
-                if constexpr (kTwo)
-                    if (turns) rb[u] = load_raw<T, E>(x + (h + u) * p.xs[2] + over);
-            }
+        for (int u = 0; u < U; ++u) {
+            if (!ALL && u >= left) break;
+            ra[u] = load_raw<T, E>(from);
+            if constexpr (kTwo)
+                if (turns) rb[u] = load_raw<T, E>(from + over);
+            from += xh;
+        }
+        x = from;
 #pragma unroll
-        for (int u = 0; u < kHeads; ++u)
-            if (h + u < h1) {
-                T *out = y + (h + u) * p.ys[2];
-                float a[E], b[E];
-                of_raw<T, E>(ra[u], a);
-                if constexpr (kTwo) {
-                    if (turns) {
-                        of_raw<T, E>(rb[u], b);
+        for (int u = 0; u < U; ++u) {
+            if (!ALL && u >= left) break;
+            float a[E], b[E];
+            of_raw<T, E>(ra[u], a);
+            if constexpr (kTwo) {
+                if (turns) {
+                    of_raw<T, E>(rb[u], b);
 #pragma unroll
-                        for (int j = 0; j < E; ++j) {
-                            const float v = a[j], w = b[j];
-                            a[j] = fmaf(v, c[j], -(w * d[j]));
-                            b[j] = fmaf(v, d[j], w * c[j]);
-                        }
-                        store_e<T, E>(out + over, b);
+                    for (int j = 0; j < E; ++j) {
+                        const float v = a[j], w = b[j];
+                        a[j] = fmaf(v, c(j), -(w * d(j)));
+                        b[j] = fmaf(v, d(j), w * c(j));
                     }
-                } else if (turns) {
-#pragma unroll
-                    for (int j = 0; j < P; ++j)
-                        if (first + j < half) {
-                            const float v = a[2 * j], w = a[2 * j + 1];
-                            a[2 * j] = fmaf(v, c[j], -(w * d[j]));
-                            a[2 * j + 1] = fmaf(v, d[j], w * c[j]);
-                        }
+                    store_e<T, E>(y + over, b);
                 }
-                store_e<T, E>(out, a);
+            } else if (turns) {
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    if (first + j < half) {
+                        const float v = a[2 * j], w = a[2 * j + 1];
+                        a[2 * j] = fmaf(v, c(j), -(w * d(j)));
+                        a[2 * j + 1] = fmaf(v, d(j), w * c(j));
+                    }
             }
-    }
+            store_e<T, E>(y, a);
+            y += yh;
+        }
+    };
+    for (; left >= kHeads<E>; left -= kHeads<E>) heads(std::true_type());
+    if (left > 0) heads(std::false_type());
 }
 
 template <typename T, int E, bool HALVES>
@@ -190,6 +286,13 @@ ct_status launch(RotaryParams &p, cudaStream_t st) {
     p.per = (int32_t)ceil_div(p.H, groups);
     p.groups = (int32_t)ceil_div(p.H, (int64_t)p.per);
     p.threads = threads * p.groups;
+    p.small = p.threads < 0x7FFFFFFF;
+    if (p.small) {
+        p.by_items = make_magic((uint32_t)p.items);
+        p.by_groups = make_magic((uint32_t)p.groups);
+        p.by_s = make_magic((uint32_t)p.S);
+        for (int a = 0; a < p.axes; ++a) p.by_grid[a] = make_magic((uint32_t)p.grid[a]);
+    }
     const int64_t blocks = ceil_div(p.threads, (int64_t)kThreads);
     if (blocks > 0x7FFFFFFF) return CT_ERR_ATTR;
     rotary_kernel<T, E, HALVES><<<(unsigned)blocks, kThreads, 0, st>>>(p);

@@ -3,6 +3,7 @@
 
 #include <stdint.h>
 
+#include "ct_divmagic.h"
 #include "ct_internal.h"
 
 namespace ct {
@@ -20,11 +21,17 @@ struct RotaryParams {
     int32_t first[3];            // each axis' first pair
     int32_t pos_type;            // ct_position_type
     float sign;                  // -1: the inverse
+    float near;                  // positions up to it take frequencies of two floats
+    int32_t small_grid;          // all indices of the grid are
     // set by rotary_run
     int32_t items;               // of a head, each one thread's
     int32_t groups, per;         // heads are cut into groups of `per`, one thread each
     int64_t threads;             // in all
-    double turns[kRotaryMaxPairs];   // frequency of each pair / 2 pi
+    int32_t small;               // every index below fits 31 bits: divisions by multiplication
+    DivMagic by_items, by_groups, by_s, by_grid[3];
+    // Frequency of each pair / 2 pi, also as two floats (high, low).
+    double turns[kRotaryMaxPairs];
+    alignas(16) float parts[kRotaryMaxPairs][2];
 };
 
 ct_status rotary_run(int dtype, int pairs, RotaryParams &p, cudaStream_t st);
