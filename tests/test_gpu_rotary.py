@@ -29,6 +29,7 @@ CASES = [   # dims, heads, dim, sections
     ([3, 5], 2, 16, [8, 8]), ([6, 7], 7, 72, [24, 40]), ([1, 9], 3, 20, [2, 14]), ([5, 1], 4, 128, [64, 64]),
     ([33, 35], 5, 80, [16, 64]), ([2, 3], 1, 26, [0, 26]), ([8, 8], 6, 48, [30, 2]),
     ([2, 3, 4], 3, 32, [8, 8, 16]), ([3, 1, 5], 24, 128, [16, 56, 56]), ([4, 4, 4], 2, 38, [4, 6, 10]),
+    ([7, 3], 5, 36, [12, 20]), ([90], 9, 44, [44]), ([110], 17, 28, [24]), ([30, 40], 12, 72, [20, 50]),
     ([9, 17, 19], 2, 64, [16, 24, 24]), ([1, 1, 1], 8, 96, [32, 32, 32]), ([5, 6, 7], 1, 51, [2, 2, 46]),
 ]
 
