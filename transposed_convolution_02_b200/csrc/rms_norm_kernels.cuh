@@ -608,50 +608,51 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && K * E <= kRmsFewEle
 
 // Backward of other rows, element by element.
 template <typename T, int K>
-__global__ void __launch_bounds__(kMaxThreads) rms_backward_ones_kernel(const RmsParams p) {
+__global__ void __launch_bounds__(kMaxThreads, K <= 8 ? 2 : 1) rms_backward_ones_kernel(const RmsParams p) {
     __shared__ float4 parts[2][kMaxThreads / 128];
     extern __shared__ uint4 ring[];
     const Place<K, true> at(p.tpr_log2);
-    const int nv = (int)p.C;
     const int rpb = blockDim.x >> p.tpr_log2;
-    float dw[K][1];
+    const int own = (int)p.C - at.first;              // element k is there where 32 k < own
+    float w[K], dw[K][1];
 #pragma unroll
-    for (int k = 0; k < K; ++k) dw[k][0] = 0.f;
+    for (int k = 0; k < K; ++k) {
+        float f[1] = {0.f};
+        if (32 * k < own) load_weight<T, 1>(p, at.first + 32 * k, f);
+        w[k] = f[0];
+        dw[k][0] = 0.f;
+    }
     int turn = 0;
     for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < p.rows; row0 += (int64_t)gridDim.x * rpb, turn ^= 1) {
-        const int64_t row = row0 + at.slot;
-        const bool live = row < p.rows;
-        const float rstd = live ? p.rstd_in[row] : 0.f;
+        const int64_t row = row0 + at.slot, e0 = row * p.C + at.first;
+        const int mine = row < p.rows ? own : 0;
+        const T *dy = (const T *)p.dy + e0, *x = (const T *)p.x + e0, *dsum = (const T *)p.dsum + e0;
+        const float rstd = mine > 0 ? p.rstd_in[row] : 0.f;
         T rd[K], rh[K], ra[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = at.first + k * at.step;
             rd[k] = rh[k] = ra[k] = from_f<T>(0.f);
-            if (live && v < nv) {
-                rd[k] = ((const T *)p.dy)[row * p.C + v];
-                rh[k] = ((const T *)p.x)[row * p.C + v];
-                if (p.dsum) ra[k] = ((const T *)p.dsum)[row * p.C + v];
+            if (32 * k < mine) {
+                rd[k] = dy[32 * k];
+                rh[k] = x[32 * k];
+                if (p.dsum) ra[k] = dsum[32 * k];
             }
         }
-        float w[K][1], dot = 0.f;
+        float dot = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int v = at.first + k * at.step;
-            w[k][0] = 0.f;
-            if (v < nv) load_weight<T, 1>(p, v, w[k]);
             const float d = to_f<T>(rd[k]), h = to_f<T>(rh[k]) * rstd;
             dw[k][0] = fmaf(d, h, dw[k][0]);
-            dot = v < nv ? fmaf(d * w[k][0], h, dot) : dot;
+            dot = 32 * k < mine ? fmaf(d * w[k], h, dot) : dot;
         }
         if (!p.dx) continue;
         const float mean = across<Add>(dot, p.tpr_log2, parts[turn]) * p.inv_c;
+        T *dx = (T *)p.dx + e0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int v = at.first + k * at.step;
-            if (live && v < nv)
-                ((T *)p.dx)[row * p.C + v] = from_f<T>(
-                    fmaf(rstd, fmaf(-(to_f<T>(rh[k]) * rstd), mean, to_f<T>(rd[k]) * w[k][0]), to_f<T>(ra[k])));
-        }
+        for (int k = 0; k < K; ++k)
+            if (32 * k < mine)
+                dx[32 * k] = from_f<T>(fmaf(rstd, fmaf(-(to_f<T>(rh[k]) * rstd), mean, to_f<T>(rd[k]) * w[k]),
+                                            to_f<T>(ra[k])));
     }
     sm100::griddep_launch_dependents();
     if (p.ws) store_dw<1, K>(p, at, dw, (float *)ring);

@@ -988,7 +988,12 @@ def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
     def call(raw):
         xc = x.contiguous() if r.copy else x
         pos = None if positions is None else positions.contiguous()
-        y = torch.empty(xc.shape, dtype=xc.dtype, device=xc.device) if out is None else out
+        if out is not None:
+            y = out
+        elif xc.is_contiguous():
+            y = torch.empty_like(xc)
+        else:
+            y = torch.empty(xc.shape, dtype=xc.dtype, device=xc.device)
         st = lib().ct_rotary(r.desc, xc.data_ptr(), _addr(pos), y.data_ptr(), raw)
         if st != CT_OK:
             raise CtError(st, "ct_rotary")
