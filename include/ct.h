@@ -439,8 +439,9 @@ CT_API ct_status ct_rotary(const ct_rotary_desc *desc, const void *x, const void
  * the last (nearest rounding would drop every change below half a step).  The
  * random number is 16-bit part i % 8 of Philox4x32-10 (as in dropout) at
  * (i / 8, step) under the key `seed`, i the element's place in the states.  A
- * positive root never becomes 0.  A gradient that is not finite makes its
- * element not finite, with 8-bit states its block. */
+ * positive root never becomes 0.  A gradient that is not finite, or past
+ * 1.8e19 (its square is not), makes its element not finite, with 8-bit states
+ * its block; v below 2^-126 has a smaller root than it should. */
 typedef struct ct_param {
     int64_t n;              /* elements */
     int32_t dtype;          /* ct_dtype of the parameter */
@@ -472,10 +473,10 @@ CT_API ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_par
                           const void *const *grads, void *exp_avg, void *exp_avg_sq, float *exp_avg_scale,
                           float *exp_avg_sq_scale, float *master, void *stream);
 
-/* *norm = the square root of the sum of all gradients' squares (squares in
- * fp32, sums in 64 bits: a gradient past 1.8e19 counts as infinite), *scale (may
- * be NULL) = min(1, max_norm / norm), or 0 where the norm is not finite: what
- * ct_adamw's grad_scale takes to clip, or to skip an update that overflowed.
+/* *norm = the square root of the sum of all gradients' squares (squares and
+ * sums in 64 bits), *scale (may be NULL) = min(1, max_norm / norm), or 0 where
+ * the norm is not finite in fp32: what ct_adamw's grad_scale takes to clip, or
+ * to skip an update that overflowed.
  * Of shapes, n and grad_dtype are read; a NULL gradient counts nothing.
  * max_norm > 0, infinity allowed.  The same call gives the same bits. */
 CT_API ct_status ct_grad_norm_workspace_bytes(int64_t count, size_t *bytes);

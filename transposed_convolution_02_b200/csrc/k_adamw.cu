@@ -56,6 +56,13 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
+// The sum of two floats each.  A product and a sum of two floats (__fmul2_rn,
+// __fadd2_rn) become one operation, of one rounding, where they meet; these do
+// not.
+__device__ __forceinline__ float2 plus(float2 a, float2 b) {
+    return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
+}
+
 // a / b from b's rounded reciprocal, corrected by the remainder: correctly
 // rounded (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990) where nothing underflows; two operations more
@@ -104,9 +111,7 @@ __device__ __forceinline__ float warp_scale(const float2 (&f)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         m = max(m, max(__float_as_uint(fabsf(f[j].x)), __float_as_uint(fabsf(f[j].y))));
-    // the largest / 448, rounded as quotient() does it
-    const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)), q = most * (1.f / kE4m3Max);
-    return max_nan(fmaf(fmaf(-q, kE4m3Max, most), 1.f / kE4m3Max, q), kLeastScale);
+    return scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)));
 }
 
 __device__ __forceinline__ float2 twice(float f) { return make_float2(f, f); }
@@ -198,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 4)
             // each operation rounded, as the formulas stand: what 8-bit codes are
             // chosen by is then the same wherever it is computed in fp32
             const float2 a = __fmul2_rn(g[j], twice(gs));
-            m[j] = __fadd2_rn(__fmul2_rn(m[j], twice(p.beta1)), __fmul2_rn(a, twice(p.rest1)));
-            v[j] = __fadd2_rn(__fmul2_rn(v[j], twice(p.beta2)), __fmul2_rn(__fmul2_rn(a, a), twice(p.rest2)));
+            m[j] = plus(__fmul2_rn(m[j], twice(p.beta1)), __fmul2_rn(a, twice(p.rest1)));
+            v[j] = plus(__fmul2_rn(v[j], twice(p.beta2)), __fmul2_rn(__fmul2_rn(a, a), twice(p.rest2)));
             root[j] = root_of(v[j]);
             const float2 q = __ffma2_rn(root[j], twice(s.root_c2), twice(p.eps));
             const float2 u = __fmul2_rn(__fmul2_rn(m[j], make_float2(reciprocal(q.x), reciprocal(q.y))), twice(-s.lr_c1));
@@ -245,16 +250,16 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ---- the gradients' norm ------------------------------------------------------
 
-// Squares and sums of eight in fp32, from there on in 64 bits: a step has
-// billions of them.  A thread block has a run of blocks; its order and that of
-// the join depend on sizes alone.
+// Squares and sums in 64 bits: a step has billions of them, and no square of
+// fp32 is out of range.  A thread block has a run of blocks; its order and that
+// of the join depend on sizes alone.
 template <int N>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ TensorTable<N> table, double *partial) {
     __shared__ double side[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t each = (table.blocks + gridDim.x - 1) / gridDim.x;
     const int64_t first = blockIdx.x * each, last = first + each < table.blocks ? first + each : table.blocks;
-    double sum = 0.0;
+    double sum = 0.0, other = 0.0;
     if (first + warp < last) {
         int i = find(table, first + warp);
         for (int64_t block = first + warp; block < last; block += kWarps) {
@@ -262,13 +267,16 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
             const TensorEntry &e = table.t[i];
             const int64_t at = (block - e.first) * kBlock + lane * 8;
             const int n = e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0;
-            float2 g[4], q = make_float2(0.f, 0.f);
+            float2 g[4];
             load8(e.grad, (e.kind >> 2) & 3, at, n, e.kind & kGradVec, g);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q = __ffma2_rn(g[j], g[j], q);
-            sum += (double)(q.x + q.y);
+            for (int j = 0; j < 4; ++j) {
+                sum = fma((double)g[j].x, (double)g[j].x, sum);
+                other = fma((double)g[j].y, (double)g[j].y, other);
+            }
         }
     }
+    sum += other;
     for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) side[warp] = sum;
     __syncthreads();
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int w = 1; w < kWarps; ++w) sum += side[w];
     const double root = sqrt(sum);
     *norm = (float)root;
-    // a norm that fp32 does not hold is no norm to scale by
+    // a norm that fp32 does not hold is none to scale by
     const bool finite = (float)root <= 3.4028234e38f;
     if (scale) *scale = !finite ? 0.f : root > max_norm ? (float)(max_norm / root) : 1.f;
 }
