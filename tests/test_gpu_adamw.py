@@ -418,3 +418,18 @@ def test_training_step_together():
         off = torch.linalg.vector_norm(got.double() - want) / torch.linalg.vector_norm(want)
         assert float(off) < 7.5 * 2.0 ** -8
     assert abs(float(norm) / float(torch.linalg.vector_norm(dw.double())) - 1) < 8 * ref.U
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_grad_norm_of_wide_ranges(dtype):
+    """Sums of 16-bit squares over many orders, whole blocks and rests: to the
+    rounding of the result."""
+    g = normal([3 * 8192 + 77], 5) * torch.exp2(torch.linspace(-24, 12, 3 * 8192 + 77, device="cuda"))
+    for scale in (1.0, 2.0 ** -100, 2.0 ** 90) if dtype == "bf16" else (1.0, 0.01):
+        t = (g * scale).to(TYPES[dtype])
+        norm, _ = ct.grad_norm([t, t[1:], t[:5]])
+        want = float(torch.linalg.vector_norm(torch.cat((t, t[1:], t[:5])).double()))
+        assert abs(float(norm) - want) <= 1.01 * ref.U * want
+    bad = t.clone()
+    bad[5000] = float("nan")
+    assert math.isnan(float(ct.grad_norm([bad])[0]))

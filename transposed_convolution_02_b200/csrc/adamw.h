@@ -17,7 +17,7 @@ constexpr int kBlock = 256;           // elements under one scale of 8-bit state
 constexpr int kFewTensors = 32;       // of a launch's table, three sizes: 1.8, 7 and 28 KB of arguments
 constexpr int kSomeTensors = 128;
 constexpr int kManyTensors = 512;
-constexpr int kNormBlocks = 148 * 8;  // of a launch of the norm: partial sums, whatever the device
+constexpr int kNormBlocks = 148 * 4;  // of a launch of the norm: partial sums, whatever the device
 
 struct TensorEntry {
     void *param;

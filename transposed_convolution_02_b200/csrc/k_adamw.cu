@@ -106,11 +106,14 @@ __device__ __forceinline__ void from_codes(uint2 w, float scale, float2 (&f)[4])
 
 // The scale of a warp's 256 values (magnitudes compare as whole numbers, NaN
 // above all).
+template <bool SIGNED>
 __device__ __forceinline__ float warp_scale(const float2 (&f)[4]) {
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        m = max(m, max(__float_as_uint(fabsf(f[j].x)), __float_as_uint(fabsf(f[j].y))));
+        m = SIGNED ? max(m, max(__float_as_uint(f[j].x) << 1, __float_as_uint(f[j].y) << 1))
+                   : max(m, max(__float_as_uint(f[j].x), __float_as_uint(f[j].y)));
+    if (SIGNED) m >>= 1;
     return scale_of(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m)));
 }
 
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             store8_f32((float *)p.m + in * kBlock + lane * 8, m);
             store8_f32((float *)p.v + in * kBlock + lane * 8, v);
         } else {
-            const float sm = warp_scale(m), sv = warp_scale(root);
+            const float sm = warp_scale<true>(m), sv = warp_scale<false>(root);
             const float im = fine_reciprocal(sm), iv = fine_reciprocal(sv);
             const uint32_t bits[4] = {d.x, d.y, d.z, d.w};
             uint32_t cm[8], cv[8];
@@ -250,33 +253,99 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 // ---- the gradients' norm ------------------------------------------------------
 
-// Squares and sums in 64 bits: a step has billions of them, and no square of
-// fp32 is out of range.  A thread block has a run of blocks; its order and that
-// of the join depend on sizes alone.
+// The sum of squares to 48 bits and more: a step has billions of them, and its
+// scale is to be the same however they are added up.  fp32's squares take 64
+// bits.  Those of 16-bit types are exact in fp32; they are added to a sum of two
+// floats, each addition with its error (Knuth's sum of two, 1969), and that goes
+// to 64 bits after 32 of them (134M bf16 64 us; 78 with a conversion each).
+struct Squares {
+    double sum = 0.0;
+
+    __device__ __forceinline__ void wide(const float2 (&g)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sum += fma((double)g[j].x, (double)g[j].x, (double)g[j].y * (double)g[j].y);
+    }
+    // U times eight elements of a type
+    template <int U>
+    __device__ __forceinline__ void add(const float2 (&g)[U][4], bool narrow) {
+        float most = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) most = fmaxf(most, fmaxf(fabsf(g[u][j].x), fabsf(g[u][j].y)));
+        // within 2^-50 .. 2^60 no square leaves fp32, nor loses what counts
+        if (narrow && most >= 0x1p-50f && most <= 0x1p60f) {
+            float2 high = make_float2(0.f, 0.f), low = high;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 q = __fmul2_rn(g[u][j], g[u][j]), s = __fadd2_rn(high, q);
+                    const float2 part = minus(s, high), rest = minus(q, part);
+                    low = __fadd2_rn(low, __fadd2_rn(minus(high, minus(s, part)), rest));
+                    high = s;
+                }
+            sum += ((double)high.x + (double)high.y) + ((double)low.x + (double)low.y);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) wide(g[u]);
+        }
+    }
+    static __device__ __forceinline__ float2 minus(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
+};
+
+// A thread block has a run of blocks; its order and that of the join depend on
+// sizes alone.
 template <int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ TensorTable<N> table, double *partial) {
+__global__ void __launch_bounds__(kThreads, 4) norm_kernel(const __grid_constant__ TensorTable<N> table, double *partial) {
     __shared__ double side[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t each = (table.blocks + gridDim.x - 1) / gridDim.x;
     const int64_t first = blockIdx.x * each, last = first + each < table.blocks ? first + each : table.blocks;
-    double sum = 0.0, other = 0.0;
+    Squares squares;
     if (first + warp < last) {
         int i = find(table, first + warp);
-        for (int64_t block = first + warp; block < last; block += kWarps) {
+        int64_t block = first + warp;
+        while (block < last) {
             while (i + 1 < table.count && table.t[i + 1].first <= block) ++i;
             const TensorEntry &e = table.t[i];
             const int64_t at = (block - e.first) * kBlock + lane * 8;
-            const int n = e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0;
-            float2 g[4];
-            load8(e.grad, (e.kind >> 2) & 3, at, n, e.kind & kGradVec, g);
+            const uint32_t gd = (e.kind >> 2) & 3;
+            // whole blocks of one tensor, four on their way; the next ones' lines go
+            // to L2, one a lane
+            constexpr int U = 4, kStep = kWarps * kBlock;
+            const int64_t rel = block - e.first;
+            if ((rel + (U - 1) * kWarps + 1) * kBlock <= e.n && block + (U - 1) * kWarps < last && (e.kind & kGradVec)) {
+                const int lines = gd == CT_F32 ? 8 : 4, ahead = lane / lines;
+                if (ahead < U && (rel + (2 * U - 1) * kWarps + 1) * kBlock <= e.n)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        (const char *)e.grad + ((rel + (U + ahead) * kWarps) * lines + lane % lines) * 128));
+                float2 g[U][4];
+                if (gd == CT_F32) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sum = fma((double)g[j].x, (double)g[j].x, sum);
-                other = fma((double)g[j].y, (double)g[j].y, other);
+                    for (int u = 0; u < U; ++u) load8_f32((const float *)e.grad + at + u * kStep, g[u]);
+                } else {
+                    uint4 raw[U];        // all loaded before the first is looked at
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        raw[u] = *reinterpret_cast<const uint4 *>((const uint16_t *)e.grad + at + u * kStep);
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (gd == CT_F16) unpack(raw[u], g[u], __half());
+                        else unpack(raw[u], g[u], __nv_bfloat16());
+                }
+                squares.add<U>(g, gd != CT_F32);
+                block += U * kWarps;
+            } else {
+                float2 g[1][4];
+                load8(e.grad, gd, at, e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0, e.kind & kGradVec, g[0]);
+                squares.add<1>(g, gd != CT_F32);
+                block += kWarps;
             }
         }
     }
-    sum += other;
+    double sum = squares.sum;
     for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) side[warp] = sum;
     __syncthreads();
