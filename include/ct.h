@@ -1,6 +1,8 @@
 /*
  * ct.h -- C ABI of the B200 (sm_100a) ONNX ConvTranspose library (libct.so),
- * and of the group norm and dropout that follow it in a decoder.
+ * of the group norm and dropout that follow it in a decoder, and of what stands
+ * around the matrix products of a decoder's blocks: root-mean-square norm,
+ * rotary positions, and the training step's end (gradient norm, AdamW).
  *
  * The operation (ai.onnx.ConvTranspose README, "Description", "Inputs",
  * "Outputs", "Attributes" and "Type constraints"): Y is the transposed
@@ -68,8 +70,7 @@ typedef enum ct_status {
     CT_ERR_NOMEM = 10      /* host allocation of the plan failed */
 } ct_status;
 
-/* ConvTranspose takes CT_F32 and CT_F16; the group norm and dropout also
- * CT_BF16. */
+/* ConvTranspose takes CT_F32 and CT_F16; all other operators also CT_BF16. */
 typedef enum ct_dtype { CT_F32 = 0, CT_F16 = 1, CT_BF16 = 2 } ct_dtype;
 typedef enum ct_layout { CT_NCHW = 0, CT_NHWC = 1 } ct_layout;
 

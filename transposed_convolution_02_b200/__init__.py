@@ -1,6 +1,7 @@
 """B200 (sm_100a) ONNX ConvTranspose, with the group norm and dropout that
-follow it in a decoder: a C-ABI CUDA library (libct.so, declared in
-include/ct.h) and its thin Python binding.  ``build.build()`` compiles the
+follow it in a decoder, the norm and positions of its blocks and the training
+step's AdamW: a C-ABI CUDA library (libct.so, declared in include/ct.h) and its
+thin Python binding.  ``build.build()`` compiles the
 library in-tree; ``workloads`` holds the seeded synthetic inputs."""
 
 from .ct import (  # noqa: F401

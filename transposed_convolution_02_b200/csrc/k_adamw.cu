@@ -5,8 +5,10 @@
 //     p  = p - lr (wd p + m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps))
 //
 // Bound: HBM; 28 bytes an element in fp32, 16 with 8-bit states, against some
-// 20 operations, 80 with 8-bit states.  Warps take blocks of 256 elements,
+// 20 operations, 60 with 8-bit states.  Warps take blocks of 256 elements,
 // eight neighbours a lane, so that each tensor's part is one access.
+// Measured (GPU time; against the measured copy rate): 67M fp32 271 us (1.06),
+// with 8-bit states 186 (0.89: instructions issue in 0.70 of the cycles).
 //
 // 8-bit states.  A block holds its m, and the square roots of its v (half the
 // exponents), as e4m3 codes under an fp32 scale each, largest magnitude / 448.

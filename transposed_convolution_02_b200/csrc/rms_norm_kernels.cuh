@@ -8,6 +8,11 @@
 // tensor is read once.  h is formed in fp32; what goes out as `sum` is rounded,
 // y comes from the unrounded values.  Sums are fp32, joined in an order that
 // only the sizes set: lanes, warps, then (dw) rows of a block, blocks.
+// Measured (GPU time; against the measured copy rate): [8,64x64,1024] bf16 with
+// a residual 42 us (0.98), e4m3 [32768,4096] fp16 with a residual 149 (0.96),
+// [32768,4096] bf16 without 96 (0.85), backward [16,112x112,512] fp16 with the
+// sum's gradient 124 (1.01), rows of 511 bf16 forward 116 (0.71), backward 134
+// (0.61).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -520,7 +525,9 @@ __device__ __forceinline__ void store_dw(const RmsParams &p, const P &at, const 
 // of its block, their weights and sums of dw in registers; dy, x and dsum come
 // through a ring of S rows in shared memory, filled S - 1 rows ahead by
 // asynchronous copies, so that the bytes in flight do not cost registers.  A
-// thread reads what it copied itself: the ring needs no barrier.
+// thread reads what it copied itself: the ring needs no barrier.  ([16,112x112,
+// 512] fp16 124 us; 207 with loads to registers.  16 elements a thread, two
+// blocks an SM: 8 elements take 155, three blocks with three rows 129.)
 template <typename T, int E, int K, int S, bool DSUM, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && K * E <= kRmsFewElements ? 2 : 1) rms_backward_kernel(const RmsParams p) {
     constexpr int N = DSUM ? 3 : 2;                  // tensors
@@ -606,7 +613,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && K * E <= kRmsFewEle
     store_dw<E, K>(p, at, dw, (float *)ring);
 }
 
-// Backward of other rows, element by element.
+// Backward of other rows, element by element (rows of 511 bf16: weights held
+// and a row's addresses made once 134 us, made for each element 192).
 template <typename T, int K>
 __global__ void __launch_bounds__(kMaxThreads, K <= 8 ? 2 : 1) rms_backward_ones_kernel(const RmsParams p) {
     __shared__ float4 parts[2][kMaxThreads / 128];
