@@ -367,6 +367,15 @@ def test_adamw_step_refusals():
         with pytest.raises(ValueError, match="lr"):
             opt.step(g)
     opt.lr = 1e-3
+    kept = opt.exp_avg
+    for other in (kept[:256], kept.half(), torch.zeros(2, 512)[:, ::2].reshape(-1)[::2], None):
+        opt.exp_avg = other
+        with pytest.raises(ValueError, match="exp_avg"):
+            opt.step(g)
+    opt.exp_avg, opt.master = kept, None
+    with pytest.raises(ValueError, match="master"):
+        opt.step(g)
+    opt.master = torch.zeros(256)
     q.data = q.data[:4]
     with pytest.raises(ValueError, match="parameter 1"):
         opt.step(g)

@@ -433,3 +433,25 @@ def test_grad_norm_of_wide_ranges(dtype):
     bad = t.clone()
     bad[5000] = float("nan")
     assert math.isnan(float(ct.grad_norm([bad])[0]))
+
+
+def test_restart():
+    """States copied, or put in their place, go on as the ones they come from; changed settings take effect."""
+    params, grads = make(120)
+    a = ct.AdamW(params, lr=1e-2, bits=8, seed=3)
+    a.step(grads)
+    b = ct.AdamW([p.clone() for p in params], lr=1e-2, bits=8, seed=3)
+    for name in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"):
+        getattr(b, name).copy_(getattr(a, name))
+    b.master = a.master.clone()
+    b.steps = a.steps
+    for opt in (a, b):
+        opt.step(grads)
+        opt.betas, opt.eps = (0.5, 0.6), 1e-3
+        opt.step(grads)
+    assert same(everything(a), everything(b))
+    c = ct.AdamW([p.clone() for p in params], lr=1e-2, bits=32)
+    old = held(c)
+    c.betas, c.eps = (0.5, 0.6), 1e-3
+    c.step(grads)
+    check_step(c, old, grads, 1.0, 1, 1e-2, "changed settings")

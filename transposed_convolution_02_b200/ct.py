@@ -1144,15 +1144,14 @@ class AdamW:
             if p.device != self.params[0].device:
                 raise ValueError("parameter %d is on %s, the first on %s" % (i, p.device, self.params[0].device))
         self.device = self.params[0].device
-        self.lr, self.betas, self.eps, self.bits, self.seed, self.steps = lr, tuple(betas), eps, bits, seed, 0
+        self.lr, self.betas, self.eps, self.bits, self.seed, self.steps = lr, tuple(betas), eps, int(bits), seed, 0
         self._sizes = [p.numel() for p in self.params]
         self._dtypes = [p.dtype for p in self.params]
         self._shapes = [p.shape for p in self.params]
         self._at = self._places()
         self._decay = decay
         self._meta = self._table = None
-        self._desc = ct_adamw_desc(bits)
-        self._desc.beta1, self._desc.beta2, self._desc.eps, self._desc.seed = betas[0], betas[1], eps, seed
+        self._desc = ct_adamw_desc(int(bits))
         blocks = [-(-k // BLOCK) for k in self._sizes]
         total = sum(blocks)
         kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
@@ -1170,6 +1169,22 @@ class AdamW:
             for i in low:
                 self.master[at:at + self._sizes[i]].copy_(self.params[i].detach().reshape(-1))
                 at += blocks[i] * BLOCK
+        self._kept = [t.numel() if t is not None else 0 for t in self._states()]
+        self._kept_at = self._kept_places()
+
+    def _states(self):
+        return self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.master
+
+    def _kept_places(self):
+        """The states' addresses; a tensor in the place of one has to be like it."""
+        kind = torch.float32 if self.bits == 32 else torch.float8_e4m3fn
+        for t, n, name, dtype in zip(self._states(), self._kept,
+                                     ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master"),
+                                     (kind, kind) + 3 * (torch.float32,)):
+            if (0 if t is None else t.numel()) != n or t is not None and (
+                    t.dtype != dtype or t.device != self.device or not t.is_contiguous()):
+                raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (name, dtype, n, self.device))
+        return [_addr(t) for t in self._states()]
 
     def _places(self):
         """The parameters' addresses; they have to be dense and apart."""
@@ -1213,7 +1228,7 @@ class AdamW:
         update.  ``steps`` counts the updates, skipped ones too; ``step``, an
         int64 CUDA tensor of one element, is the number of this update (1 for
         the first) in its place, read on the device: a captured graph needs it,
-        and counts with it."""
+        and counts with it.  Gradients may not overlap parameters or states."""
         grads = list(grads)
         params = self.params
         if len(grads) != len(params):
@@ -1228,7 +1243,13 @@ class AdamW:
             self._meta = meta
         if list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes:
             self._at = self._places()
+        states = self._states()
+        if ([_addr(t) for t in states] != self._kept_at
+                or [0 if t is None else t.numel() for t in states] != self._kept):
+            self._kept_at = self._kept_places()
         d, lr = self._desc, self.lr
+        d.beta1, d.beta2 = self.betas
+        d.eps, d.seed = self.eps, self.seed
         d.grad_scale = None if grad_scale is None else self._scalar(grad_scale, "grad_scale", torch.float32)
         d.step_device = None if step is None else self._scalar(step, "step", torch.int64)
         if isinstance(lr, torch.Tensor):
@@ -1250,8 +1271,7 @@ class AdamW:
                 at = _pointers(map(_where, dense))
             to = _pointers(self._at)
             st = lib().ct_adamw(d, len(dense), self._table, to.buffer_info()[0], at.buffer_info()[0],
-                                self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), _addr(self.exp_avg_scale),
-                                _addr(self.exp_avg_sq_scale), _addr(self.master), raw)
+                                *self._kept_at, raw)
             if st != CT_OK:
                 raise CtError(st, "ct_adamw")
 
