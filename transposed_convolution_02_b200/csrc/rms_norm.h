@@ -1,11 +1,11 @@
 // Root-mean-square norm: arguments and geometry, shared by the C entry points
 // and the kernels.
 //
-// A row (a pixel, a token, a head) of C channels belongs to `tpr` threads, a
-// power of two from 1 to 512; a thread holds K vectors of E elements of it in
-// registers, so that every tensor is read once.  E is a vector of 16 bytes
-// where all rows start on one, else a single element.  Rows longer than 512
-// threads hold are walked twice by kernels of their own.
+// A row (a pixel, a token, a head) of C channels belongs to some lanes of a warp
+// or to some warps; a thread holds K vectors of E elements of it in registers, so
+// that every tensor is read once.  E is a vector of 16 bytes where the tensors
+// start on one, else a single element.  Rows longer than a block holds are walked
+// twice by kernels of their own.
 #pragma once
 
 #include <stdint.h>
@@ -30,12 +30,15 @@ struct RmsArgs {
 };
 
 struct RmsGeom {
-    int vec;        // 16-byte vectors, else single elements
-    int K;          // vectors of a row per thread; 0: the row is walked
-    int tpr;        // threads per row
-    int threads;    // per block
+    bool vec;           // 16-byte vectors, else single elements
+    bool shift;         // rows start inside vectors
+    int K;              // vectors of a row per thread; 0: the row is walked
+    int lanes_log2;     // of a row: 5 where it has whole warps
+    int warps;          // of a row
+    int rpb;            // rows of a block
+    int threads;        // per block
     int64_t blocks;
-    int64_t ring;   // blocks of the forward kernel that stays for many rows; 0: there are few
+    int64_t ring;       // blocks of the forward kernel that stays for many rows; 0: not that one
 };
 
 // Rows of the backward ring for K vectors a thread.

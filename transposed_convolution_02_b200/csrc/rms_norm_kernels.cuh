@@ -9,10 +9,10 @@
 // y comes from the unrounded values.  Sums are fp32, joined in an order that
 // only the sizes set: lanes, warps, then (dw) rows of a block, blocks.
 // Measured (GPU time; against the measured copy rate): [8,64x64,1024] bf16 with
-// a residual 42 us (0.98), e4m3 [32768,4096] fp16 with a residual 149 (0.96),
-// [32768,4096] bf16 without 96 (0.85), backward [16,112x112,512] fp16 with the
-// sum's gradient 124 (1.01), rows of 511 bf16 forward 116 (0.71), backward 134
-// (0.61).
+// a residual 42 us (0.98), e4m3 [32768,4096] fp16 with a residual 139 (1.04),
+// [32768,4096] bf16 without 90 (0.91), backward [16,112x112,512] fp16 with the
+// sum's gradient 124 (1.01), rows of 511 bf16 forward 100 (0.82), backward 132
+// (0.62).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -39,7 +39,9 @@ struct RmsParams {
     float *ws;
     int64_t rows, C;
     float eps, inv_c;
-    int32_t tpr_log2, wide;                  // wide: the weight is fp32
+    int32_t lanes_log2, warps, rpb;          // of a row: lanes (32 in `warps` warps); rows of a block
+    int32_t per_warp, room_log2;             // 65536 / warps, rounded up; floats in shared memory for a row's warps
+    int32_t wide;                            // the weight is fp32
     int32_t block, block_log2, blocks_c;     // blocks_c: scales per row
     int64_t parts;
 };
@@ -112,44 +114,89 @@ struct Max {
     __device__ static float of(float a, float b) { return max_nan(a, b); }
 };
 
-// One value of all threads of a row, the same in each of them.  `parts`: a
-// float for every warp of the block; a block that comes here again uses
-// another array in between.
-template <typename Op>
-__device__ __forceinline__ float across(float v, int tpr_log2, float4 *parts) {
-    const int lanes = tpr_log2 < 5 ? 1 << tpr_log2 : 32;
-    for (int o = lanes / 2; o > 0; o /= 2) v = Op::of(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    if (tpr_log2 <= 5) return v;
-    float *const each = reinterpret_cast<float *>(parts);
-    const int warp = threadIdx.x >> 5, warps = 1 << (tpr_log2 - 5);
-    if ((threadIdx.x & 31) == 0) each[warp] = v;
+// A thread's place in its row: warps take runs of K vectors a lane, so that a
+// block of up to 128 channels lies in one warp.  FIXED: a row has whole warps,
+// or one vector a thread.  WHOLE: it has whole warps (of single elements: more
+// than one a thread; rows of 67 fp32 elements 67 % of the floor, 58 when asked).
+template <int K, bool FIXED, bool WHOLE = false>
+struct Place {
+    int slot, warp;    // row of the block; warp of the row
+    int first;         // vector k of this thread is first + k * step
+    int step;
+    bool lead;         // the row's first thread
+    __device__ explicit Place(const RmsParams &p) {
+        if (WHOLE || p.lanes_log2 == 5) {
+            warp = threadIdx.x >> 5;
+            slot = warp * p.per_warp >> 16;
+            warp -= slot * p.warps;
+            first = warp * 32 * K + (threadIdx.x & 31);
+            step = 32;
+        } else {
+            warp = 0;
+            slot = threadIdx.x >> p.lanes_log2;
+            first = threadIdx.x & ((1 << p.lanes_log2) - 1);
+            step = FIXED ? 32 : 1 << p.lanes_log2;
+        }
+        lead = first == 0;
+    }
+    static constexpr bool whole = WHOLE;
+};
+
+// Room for one value of each warp, a row's from a power of two on: what is left
+// between them is 0, for good.
+__device__ __forceinline__ void clear(const RmsParams &p, float4 *parts, int n) {
+    if (p.warps != 1 << p.room_log2) {
+        for (int i = threadIdx.x; i < n; i += blockDim.x) parts[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncthreads();
+    }
+}
+
+// One value of all threads of a row, the same in each of them.  A block that
+// comes here again uses another `parts` in between.
+template <typename Op, typename P>
+__device__ __forceinline__ float across(float v, const RmsParams &p, const P &at, float4 *parts) {
+    if (P::whole || p.lanes_log2 == 5) {
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) v = Op::of(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    } else {
+        for (int o = (1 << p.lanes_log2) / 2; o > 0; o /= 2) v = Op::of(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    }
+    if (p.warps == 1) return v;
+    float *const each = reinterpret_cast<float *>(parts) + (at.slot << p.room_log2);
+    if ((threadIdx.x & 31) == 0) each[at.warp] = v;
     __syncthreads();
-    const int first = warp & ~(warps - 1);
-    if (warps == 2) return Op::of(each[first], each[first + 1]);
-    float4 a = parts[first / 4];
+    if (p.warps == 2) return Op::of(each[0], each[1]);
+    const float4 *const all = reinterpret_cast<const float4 *>(each);
+    float4 a = all[0];
     v = Op::of(Op::of(a.x, a.y), Op::of(a.z, a.w));
-    for (int w = 1; w < warps / 4; ++w) {
-        a = parts[first / 4 + w];
+    for (int w = 1; w < 1 << p.room_log2 >> 2; ++w) {
+        a = all[w];
         v = Op::of(v, Op::of(Op::of(a.x, a.y), Op::of(a.z, a.w)));
     }
     return v;
 }
 
-// A thread's place in its row: warps take runs of K vectors a lane, so that a
-// block of up to 128 channels lies in one warp.  FIXED: a row has whole warps,
-// or one vector a thread.
-template <int K, bool FIXED>
-struct Place {
-    int slot;     // row of the block
-    int first;    // vector k of this thread is first + k * step
-    int step;
-    bool lead;    // the row's first thread
-    __device__ explicit Place(int tpr_log2) {
-        const int t = threadIdx.x & ((1 << tpr_log2) - 1), lanes = FIXED || tpr_log2 > 5 ? 5 : tpr_log2;
-        slot = threadIdx.x >> tpr_log2;
-        step = 1 << lanes;
-        first = FIXED && K == 1 ? t : (t >> lanes << lanes) * K + (t & (step - 1));
-        lead = t == 0;
+// A row that starts inside a vector, at its element s, as rows of no whole
+// number of vectors do.  All rows of a slot start alike: the host steps by as
+// many rows as bring the start back.
+template <int E, bool SHIFT>
+struct Cut {
+    int s = 0, nv, tail = E;
+    __device__ Cut(const RmsParams &p, int64_t row) {
+        if (SHIFT) {
+            s = (int)(row * p.C & (E - 1));
+            nv = (int)(s + p.C + E - 1) / E;
+            tail = (int)(s + p.C) - (nv - 1) * E;
+        } else {
+            nv = (int)(p.C / E);
+        }
+    }
+    // which elements of vector v are the row's
+    __device__ __forceinline__ uint32_t bits(int v) const {
+        uint32_t b = (1u << E) - 1;
+        if (SHIFT && v == 0) b &= ~((1u << s) - 1);
+        if (SHIFT && v == nv - 1) b &= (1u << tail) - 1;
+        return b;
     }
 };
 
@@ -210,6 +257,20 @@ struct Elements {
             *reinterpret_cast<uint4 *>(to) = pack(p, T());
         }
     }
+    // elements of vector k that are not in `bits` become 0
+    __device__ __forceinline__ void keep(int k, uint32_t bits) {
+        if (bits == (1u << E) - 1) return;
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if (!((bits >> j) & 1)) put(k, j, 0.f);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(int k, T *to, uint32_t bits) const {
+        if (bits == (1u << E) - 1) return store(k, to);
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            if ((bits >> j) & 1) to[j] = from_f<T>(at(k, j));
+    }
     // element j of vector k
     __device__ __forceinline__ float at(int k, int j) const {
         const int i = k * E + j;
@@ -231,9 +292,10 @@ __device__ __forceinline__ float inverse_root(float a) {
 // What a thread makes of its part of a row, h, once the row's sum is known: y
 // or its codes.  `mine`: vectors k with k * step < mine are there; e0: where the
 // part starts; w: the weights.
-template <typename T, int E, int K, bool Q, bool FULL, typename P>
-__device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, int64_t row, int mine, int64_t e0,
-                                           Elements<E, K> &h, float sum, const Elements<E, K> &w, float4 *parts) {
+template <typename T, int E, int K, bool Q, bool FULL, bool SHIFT, typename P>
+__device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, const Cut<E, SHIFT> &cut, int64_t row,
+                                           int mine, int64_t e0, Elements<E, K> &h, float sum,
+                                           const Elements<E, K> &w, float4 *parts) {
     const float rstd = inverse_root(fmaf(sum, p.inv_c, p.eps));
     if (p.rstd && (FULL || mine > 0) && at.lead) p.rstd[row] = rstd;
     const float2 r2 = make_float2(rstd, rstd);
@@ -242,7 +304,10 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, int6
     if constexpr (!Q) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (FULL || k * at.step < mine) h.store(k, (T *)p.y + e0 + k * at.step * E);
+            if (FULL || k * at.step < mine) {
+                if (SHIFT) h.store(k, (T *)p.y + e0 + k * at.step * E, cut.bits(at.first + k * at.step));
+                else h.store(k, (T *)p.y + e0 + k * at.step * E);
+            }
         return;
     }
     float m[K];
@@ -250,14 +315,17 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, int6
     for (int k = 0; k < K; ++k) {
         m[k] = 0.f;
         // what is not there is 0, or 0 * infinity: not looked at
-        if (FULL || k * at.step < mine)
+        if (FULL || k * at.step < mine) {
+            const uint32_t bits = SHIFT ? cut.bits(at.first + k * at.step) : (1u << E) - 1;
 #pragma unroll
-            for (int j = 0; j < E; ++j) m[k] = max_nan(m[k], fabsf(h.at(k, j)));
+            for (int j = 0; j < E; ++j)
+                if (!SHIFT || (bits >> j) & 1) m[k] = max_nan(m[k], fabsf(h.at(k, j)));
+        }
     }
-    if (p.block == 0) {
+    if (SHIFT || p.block == 0) {
 #pragma unroll
         for (int k = 1; k < K; ++k) m[0] = max_nan(m[0], m[k]);
-        m[0] = scale_of(across<Max>(m[0], p.tpr_log2, parts));
+        m[0] = scale_of(across<Max>(m[0], p, at, parts));
         if ((FULL || mine > 0) && at.lead) p.scale[row] = m[0];
     } else {
         block_max<E, K>(m, p.block);
@@ -273,7 +341,7 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, int6
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         if (!FULL && k * at.step >= mine) continue;
-        const float inv = p.block == 0 || k == 0 ? inv0 : 1.f / m[k];
+        const float inv = SHIFT || p.block == 0 || k == 0 ? inv0 : 1.f / m[k];
         uint8_t *q = (uint8_t *)p.y + e0 + k * at.step * E;
         if constexpr (E == 1) {
             *q = (uint8_t)codes2(h.at(k, 0) * inv, 0.f);
@@ -285,25 +353,44 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, int6
                 const float2 a = __fmul2_rn(h.v[k * E / 2 + 2 * j], i2), b = __fmul2_rn(h.v[k * E / 2 + 2 * j + 1], i2);
                 c[j] = codes4(a.x, a.y, b.x, b.y);
             }
-            if constexpr (E == 8) *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
-            else *reinterpret_cast<uint32_t *>(q) = c[0];
+            const uint32_t bits = cut.bits(at.first + k * at.step);
+            if (SHIFT && bits != (1u << E) - 1) {
+#pragma unroll
+                for (int j = 0; j < E; ++j)
+                    if ((bits >> j) & 1) q[j] = (uint8_t)(c[j / 4] >> (8 * (j & 3)));
+            } else if constexpr (E == 8) {
+                *reinterpret_cast<uint2 *>(q) = make_uint2(c[0], c[1]);
+            } else {
+                *reinterpret_cast<uint32_t *>(q) = c[0];
+            }
         }
     }
 }
 
 // The weights of a thread's channels; 0 where it has none.
-template <typename T, int E, int K, typename P>
-__device__ __forceinline__ void weights_of(const RmsParams &p, const P &at, Elements<E, K> &w) {
+template <typename T, int E, int K, bool SHIFT, typename P>
+__device__ __forceinline__ void weights_of(const RmsParams &p, const P &at, const Cut<E, SHIFT> &cut,
+                                           Elements<E, K> &w) {
 #pragma unroll
     for (int i = 0; i < w.N; ++i) w.v[i] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int v = at.first + k * at.step;
-        if (v >= (int)(p.C / E)) continue;
-        float f[E];
-        load_weight<T, E>(p, (int64_t)v * E, f);
+        if (v >= cut.nv) continue;
+        if constexpr (SHIFT) {
+            const uint32_t bits = cut.bits(v);
 #pragma unroll
-        for (int j = 0; j < E; ++j) w.put(k, j, f[j]);
+            for (int j = 0; j < E; ++j) {
+                float f[1] = {0.f};
+                if ((bits >> j) & 1) load_weight<T, 1>(p, (int64_t)v * E + j - cut.s, f);
+                w.put(k, j, f[0]);
+            }
+        } else {
+            float f[E];
+            load_weight<T, E>(p, (int64_t)v * E, f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) w.put(k, j, f[j]);
+        }
     }
 }
 
@@ -315,20 +402,35 @@ __device__ __forceinline__ float squares(const Elements<E, K> &h) {
     return both.x + both.y;
 }
 
+// Registers of a thread of rms_forward_kernel.  The fewer, the more blocks read
+// while others sum up.  bf16 with a residual, of the floor: e4m3 of 1024 channels
+// 94 % with 40, 91 with 48, 84 with 64; 8192 channels, without codes, 95 with 40
+// (three blocks an SM), 86 with 48 (two); 1024 channels 97 with 40, 98 with 48.
+// 256 channels, 8 elements a thread, as e4m3: 90 with 32, 83 with 40.
+constexpr int rms_forward_registers(int E, int K, bool res, bool codes, bool full, bool wide) {
+    if (E == 1) return K <= 4 ? 32 : K == 8 ? (codes ? 48 : 40) : K == 16 ? 64 : 128;
+    if (K * E <= 8) return 32;
+    if (K * E <= kRmsFewElements) return full && (E == 8 ? codes || wide : codes && !res) ? 40 : 48;
+    return K * E <= 24 ? (full ? 56 : 64) : 128;
+}
+
 // Forward, a row's tensors loaded into registers.  FULL: every thread has K
 // vectors of some row, and weights of type W; what is not asked then is most of
-// the e4m3 form's work ([32768,4096] fp16 149 us, 178 when it asks).
-template <typename T, int E, int K, bool RES, bool Q, typename W>
-__global__ void __launch_bounds__(K * E <= kRmsFewElements ? 1024 : kMaxThreads) rms_forward_kernel(const RmsParams p) {
+// the e4m3 form's work ([32768,4096] fp16, each with 64 registers: 149 us, 178
+// when it asks).  WIDE: more than 256 threads.
+template <typename T, int E, int K, bool RES, bool Q, typename W, bool WIDE = false>
+__global__ void __maxnreg__(rms_forward_registers(E, K, RES, Q, !std::is_same_v<W, void>, WIDE))
+    rms_forward_kernel(const RmsParams p) {
     constexpr bool FULL = !std::is_same_v<W, void>;
-    __shared__ float4 parts[2][2][1024 / 128];
-    const Place<K, FULL || E == 1> at(p.tpr_log2);
-    const int nv = (int)(p.C / E);
-    const int64_t rpb = blockDim.x >> p.tpr_log2;
+    __shared__ float4 parts[4][1024 / 128];
+    const Place<K, FULL || E == 1, FULL || (E == 1 && K > 1)> at(p);
+    const Cut<E, false> cut(p, 0);
+    clear(p, parts[0], sizeof(parts) / 16);
+    const int64_t rpb = p.rpb;
     int turn = 0;
     for (int64_t row0 = blockIdx.x * rpb; row0 < p.rows; row0 += gridDim.x * rpb, turn ^= 1) {
         const int64_t row = row0 + at.slot;
-        const int mine = row < p.rows ? nv - at.first : 0;
+        const int mine = row < p.rows ? cut.nv - at.first : 0;
         const int64_t e0 = row * p.C + (int64_t)at.first * E;
         const T *x = (const T *)p.x + e0, *res = (const T *)p.residual + e0;
         Raw<T, E> rx[K], rr[RES ? K : 1];
@@ -356,9 +458,9 @@ __global__ void __launch_bounds__(K * E <= kRmsFewElements ? 1024 : kMaxThreads)
                 for (int k = 0; k < K; ++k)
                     if (FULL || k * at.step < mine) h.store(k, (T *)p.sum + e0 + k * at.step * E);
         }
-        const float sum = across<Add>(squares(h), p.tpr_log2, parts[turn][0]);
+        const float sum = across<Add>(squares(h), p, at, parts[2 * turn]);
         if constexpr (!FULL) {
-            weights_of<T, E, K>(p, at, w);
+            weights_of<T, E, K>(p, at, cut, w);
         } else if constexpr (std::is_same_v<W, T>) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
@@ -373,62 +475,95 @@ __global__ void __launch_bounds__(K * E <= kRmsFewElements ? 1024 : kMaxThreads)
                 w.v[i + 1] = make_float2(f.z, f.w);
             }
         }
-        finish_row<T, E, K, Q, FULL>(p, at, row, mine, e0, h, sum, w, parts[turn][1]);
+        finish_row<T, E, K, Q, FULL>(p, at, cut, row, mine, e0, h, sum, w, parts[2 * turn + 1]);
     }
 }
 
 __device__ __forceinline__ uint32_t shared_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// 16 bytes from global to shared memory, past the registers.
+// 16 bytes from global to shared memory, past the registers; of the last vector
+// of a tensor what there is, and zeros.
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_some(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Forward of many rows of whole vectors, without a residual: a block stays for
-// row after row, its weights in registers.  The rows come through a ring of S of them in shared
-// memory, filled S - 1 ahead by asynchronous copies, so that the bytes in
-// flight do not cost registers.  A thread reads what it copied itself: the ring
-// needs no barrier.
-template <typename T, int E, int K, int S>
+// Forward of many rows: a block stays for row after row, its weights in
+// registers.  The rows come through a ring of S of them in shared memory, filled
+// S - 1 ahead by asynchronous copies, so that the bytes in flight do not cost
+// registers.  A thread reads what it copied itself: the ring needs no barrier.
+template <typename T, int K, int S, bool RES, bool Q, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads) rms_forward_ring_kernel(const RmsParams p) {
-    __shared__ float4 parts[2][kMaxThreads / 128];
-    extern __shared__ uint4 ring[];                  // [S][K][threads]
-    const Place<K, false> at(p.tpr_log2);
-    const int nv = (int)(p.C / E);
-    const int rpb = blockDim.x >> p.tpr_log2;
-    const int64_t stride = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
+    constexpr int E = kVec<T>, N = RES ? 2 : 1;      // tensors
+    __shared__ float4 parts[4][kMaxThreads / 128];
+    extern __shared__ uint4 ring[];                  // [S][N][K][threads]
+    const Place<K, false> at(p);
+    clear(p, parts[0], sizeof(parts) / 16);
+    const int64_t stride = (int64_t)gridDim.x * p.rpb, first = (int64_t)blockIdx.x * p.rpb;
     const int64_t rounds = first < p.rows ? (p.rows - first + stride - 1) / stride : 0;
+    const Cut<E, SHIFT> cut(p, first + at.slot);
+    const int64_t all = p.rows * p.C;
     uint4 *const own = ring + threadIdx.x;
     const int line = blockDim.x;
     auto fetch = [&](int64_t i, int s) {
         const int64_t row = first + i * stride + at.slot;
         if (i < rounds && row < p.rows) {
-            const T *x = (const T *)p.x + row * p.C + (int64_t)at.first * E;
+            const int64_t e0 = row * p.C - cut.s + (int64_t)at.first * E;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (k * at.step < nv - at.first) copy16(shared_address(own + (s * K + k) * line), x + k * at.step * E);
+            for (int k = 0; k < K; ++k) {
+                if (k * at.step >= cut.nv - at.first) continue;
+                const int64_t e = e0 + k * at.step * E;
+                const uint32_t to = shared_address(own + (s * N * K + k) * line);
+                const int64_t rest = (all - e) * (int)sizeof(T);
+                if (SHIFT && rest < 16) {
+                    copy_some(to, (const T *)p.x + e, (int)rest);
+                    if (RES) copy_some(to + K * line * 16, (const T *)p.residual + e, (int)rest);
+                } else {
+                    copy16(to, (const T *)p.x + e);
+                    if (RES) copy16(to + K * line * 16, (const T *)p.residual + e);
+                }
+            }
         }
         copies_end();
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(i, i);
     Elements<E, K> w;
-    weights_of<T, E, K>(p, at, w);
+    weights_of<T, E, K>(p, at, cut, w);
     int s = 0;
     for (int64_t i = 0; i < rounds; ++i) {
         fetch(i + S - 1, s == 0 ? S - 1 : s - 1);
         const int64_t row = first + i * stride + at.slot;
-        const int mine = row < p.rows ? nv - at.first : 0;
+        const int mine = row < p.rows ? cut.nv - at.first : 0;
+        const int64_t e0 = row * p.C - cut.s + (int64_t)at.first * E;
         copies_wait<S - 1>();
         Elements<E, K> h;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            h.template set<T>(k, k * at.step < mine ? own[(s * K + k) * line] : make_uint4(0, 0, 0, 0));
-        const float sum = across<Add>(squares(h), p.tpr_log2, parts[i & 1]);
-        finish_row<T, E, K, false, false>(p, at, row, mine, row * p.C + (int64_t)at.first * E, h, sum, w, nullptr);
+            h.template set<T>(k, k * at.step < mine ? own[(s * N * K + k) * line] : make_uint4(0, 0, 0, 0));
+        if (RES) {
+            Elements<E, K> r;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                r.template set<T>(k, k * at.step < mine ? own[((s * N + 1) * K + k) * line] : make_uint4(0, 0, 0, 0));
+#pragma unroll
+            for (int j = 0; j < h.N; ++j) h.v[j] = __fadd2_rn(h.v[j], r.v[j]);
+        }
+        if (SHIFT)
+#pragma unroll
+            for (int k = 0; k < K; ++k) h.keep(k, cut.bits(at.first + k * at.step));
+        if (RES && p.sum)
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k * at.step < mine)
+                    h.store(k, (T *)p.sum + e0 + k * at.step * E, cut.bits(at.first + k * at.step));
+        const float sum = across<Add>(squares(h), p, at, parts[2 * (i & 1)]);
+        finish_row<T, E, K, Q, false>(p, at, cut, row, mine, e0, h, sum, w, parts[2 * (i & 1) + 1]);
         s = s == S - 1 ? 0 : s + 1;
     }
 }
@@ -439,7 +574,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_ring_kernel(const Rms
 template <typename T, bool RES, bool Q>
 __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const RmsParams p) {
     __shared__ float4 parts[2][kMaxThreads / 128];
-    constexpr int kLog2 = 9;
+    const Place<1, true> at(p);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T *x = (const T *)p.x + row * p.C, *r = RES ? (const T *)p.residual + row * p.C : nullptr;
         auto h = [&](int64_t c) { return RES ? to_f<T>(x[c]) + to_f<T>(r[c]) : to_f<T>(x[c]); };
@@ -450,7 +585,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const Rms
         };
         float sum = 0.f;
         for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) sum = fmaf(h(c), h(c), sum);
-        sum = across<Add>(sum, kLog2, parts[0]);
+        sum = across<Add>(sum, p, at, parts[0]);
         const float rstd = inverse_root(fmaf(sum, p.inv_c, p.eps));
         if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
         if (!Q) {
@@ -464,7 +599,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const Rms
             if (p.block == 0) {
                 float m = 0.f;
                 for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) m = max_nan(m, fabsf(y(c, h(c), rstd)));
-                const float scale = scale_of(across<Max>(m, kLog2, parts[1])), inv = 1.f / scale;
+                const float scale = scale_of(across<Max>(m, p, at, parts[1])), inv = 1.f / scale;
                 if (threadIdx.x == 0) p.scale[row] = scale;
                 for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) {
                     const float v = h(c);
@@ -502,21 +637,19 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const Rms
 // A block's sums of dw: its rows' one after the other, to its line of the workspace.
 template <int E, int K, typename P>
 __device__ __forceinline__ void store_dw(const RmsParams &p, const P &at, const float (&dw)[K][E], float *slots) {
-    const int rpb = blockDim.x >> p.tpr_log2;
-    const int64_t nv = p.C / E;
-    float *out = rpb > 1 ? slots + (int64_t)at.slot * p.C : p.ws + (int64_t)blockIdx.x * p.C;
+    float *out = p.rpb > 1 ? slots + (int64_t)at.slot * p.C : p.ws + (int64_t)blockIdx.x * p.C;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int v = at.first + k * at.step;
-        if (v < nv)
+        if (v < (int)(p.C / E))
 #pragma unroll
             for (int j = 0; j < E; ++j) out[(int64_t)v * E + j] = dw[k][j];
     }
-    if (rpb == 1) return;
+    if (p.rpb == 1) return;
     __syncthreads();
     for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
         float s = slots[c];
-        for (int r = 1; r < rpb; ++r) s += slots[(int64_t)r * p.C + c];
+        for (int r = 1; r < p.rpb; ++r) s += slots[(int64_t)r * p.C + c];
         p.ws[(int64_t)blockIdx.x * p.C + c] = s;
     }
 }
@@ -528,16 +661,18 @@ __device__ __forceinline__ void store_dw(const RmsParams &p, const P &at, const 
 // thread reads what it copied itself: the ring needs no barrier.  ([16,112x112,
 // 512] fp16 124 us; 207 with loads to registers.  16 elements a thread, two
 // blocks an SM: 8 elements take 155, three blocks with three rows 129.)
-template <typename T, int E, int K, int S, bool DSUM, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 && K * E <= kRmsFewElements ? 2 : 1) rms_backward_kernel(const RmsParams p) {
-    constexpr int N = DSUM ? 3 : 2;                  // tensors
+template <typename T, int K, int S, bool DSUM, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && K * kVec<T> <= kRmsFewElements ? 2 : 1)
+    rms_backward_kernel(const RmsParams p) {
+    constexpr int E = kVec<T>, N = DSUM ? 3 : 2;     // tensors
     __shared__ float4 parts[2][kMaxThreads / 128];
     extern __shared__ uint4 ring[];                  // [S][N][K][threads]; then dw's slots
-    const Place<K, false> at(p.tpr_log2);
-    const int nv = (int)(p.C / E);
-    const int rpb = blockDim.x >> p.tpr_log2;
+    const Place<K, false> at(p);
+    clear(p, parts[0], sizeof(parts) / 16);
+    const int rpb = p.rpb;
     const int64_t stride = (int64_t)gridDim.x * rpb, first = (int64_t)blockIdx.x * rpb;
     const int64_t rounds = first < p.rows ? (p.rows - first + stride - 1) / stride : 0;
+    const int nv = (int)(p.C / E);
     auto slot = [&](int s, int n, int k) { return ring + ((s * N + n) * K + k) * blockDim.x + threadIdx.x; };
     auto fetch = [&](int64_t i) {
         const int64_t row = first + i * stride + at.slot;
@@ -592,7 +727,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && K * E <= kRmsFewEle
             }
         }
         if (!p.dx) continue;
-        const float mean = across<Add>(dot, p.tpr_log2, parts[i & 1]) * p.inv_c;
+        const float mean = across<Add>(dot, p, at, parts[i & 1]) * p.inv_c;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int v = at.first + k * at.step;
@@ -619,8 +754,9 @@ template <typename T, int K>
 __global__ void __launch_bounds__(kMaxThreads, K <= 8 ? 2 : 1) rms_backward_ones_kernel(const RmsParams p) {
     __shared__ float4 parts[2][kMaxThreads / 128];
     extern __shared__ uint4 ring[];
-    const Place<K, true> at(p.tpr_log2);
-    const int rpb = blockDim.x >> p.tpr_log2;
+    const Place<K, true, (K > 1)> at(p);
+    clear(p, parts[0], sizeof(parts) / 16);
+    const int rpb = p.rpb;
     const int own = (int)p.C - at.first;              // element k is there where 32 k < own
     float w[K], dw[K][1];
 #pragma unroll
@@ -654,7 +790,7 @@ __global__ void __launch_bounds__(kMaxThreads, K <= 8 ? 2 : 1) rms_backward_ones
             dot = 32 * k < mine ? fmaf(d * w[k], h, dot) : dot;
         }
         if (!p.dx) continue;
-        const float mean = across<Add>(dot, p.tpr_log2, parts[turn]) * p.inv_c;
+        const float mean = across<Add>(dot, p, at, parts[turn]) * p.inv_c;
         T *dx = (T *)p.dx + e0;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -670,6 +806,7 @@ __global__ void __launch_bounds__(kMaxThreads, K <= 8 ? 2 : 1) rms_backward_ones
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) rms_backward_walk_kernel(const RmsParams p) {
     __shared__ float4 parts[kMaxThreads / 128];
+    const Place<1, true> at(p);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
         const T *x = (const T *)p.x + row * p.C, *dy = (const T *)p.dy + row * p.C;
         const float rstd = p.rstd_in[row];
@@ -680,7 +817,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_backward_walk_kernel(const Rm
         };
         float dot = 0.f;
         for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) dot = fmaf(t(c), to_f<T>(x[c]) * rstd, dot);
-        const float mean = across<Add>(dot, 9, parts) * p.inv_c;
+        const float mean = across<Add>(dot, p, at, parts) * p.inv_c;
         for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) {
             const float d = p.dsum ? to_f<T>(((const T *)p.dsum)[row * p.C + c]) : 0.f;
             ((T *)p.dx)[row * p.C + c] = from_f<T>(fmaf(rstd, fmaf(-(to_f<T>(x[c]) * rstd), mean, t(c)), d));
@@ -738,7 +875,11 @@ RmsParams params_of(const RmsArgs &a, const RmsGeom &g) {
     p.rows = a.rows; p.C = a.C;
     p.eps = a.eps;
     p.inv_c = (float)(1.0 / (double)a.C);
-    while ((1 << p.tpr_log2) < g.tpr) ++p.tpr_log2;
+    p.lanes_log2 = g.lanes_log2;
+    p.warps = g.warps;
+    p.per_warp = (65536 + g.warps - 1) / g.warps;
+    while (1 << p.room_log2 < g.warps) ++p.room_log2;
+    p.rpb = g.rpb;
     p.wide = a.param_dtype == CT_F32;
     p.block = a.block != 0 && a.block < a.C ? a.block : 0;
     while ((1 << p.block_log2) < p.block) ++p.block_log2;
@@ -751,22 +892,16 @@ struct Int {
     static constexpr int value = V;
 };
 
-// f(elements, vectors a thread) with each as a type.
-template <typename T, typename F>
-void by_geom(const RmsGeom &g, F f) {
-    if (g.vec) {
-        constexpr int E = kVec<T>;
-        if (g.K == 1) f(Int<E>(), Int<1>());
-        else if (g.K == 2) f(Int<E>(), Int<2>());
-        else if (g.K == 4) f(Int<E>(), Int<4>());
-        else f(Int<E>(), Int<8>());
-    } else {
-        if (g.K == 1) f(Int<1>(), Int<1>());
-        else if (g.K == 2) f(Int<1>(), Int<2>());
-        else if (g.K == 4) f(Int<1>(), Int<4>());
-        else if (g.K == 8) f(Int<1>(), Int<8>());
-        else f(Int<1>(), Int<32>());
-    }
+// f(vectors a thread) with the number as a type.
+template <typename F>
+void by_k(int K, F f) {
+    if (K == 1) f(Int<1>());
+    else if (K == 2) f(Int<2>());
+    else if (K == 3) f(Int<3>());
+    else if (K == 4) f(Int<4>());
+    else if (K == 8) f(Int<8>());
+    else if (K == 16) f(Int<16>());
+    else f(Int<32>());
 }
 
 template <typename T, bool RES, bool Q>
@@ -777,26 +912,42 @@ ct_status forward_launch(const RmsParams &p, const RmsGeom &g, cudaStream_t st) 
         return launch_status();
     }
     bool fine = true;
-    by_geom<T>(g, [&](auto e, auto k) -> void {
-        constexpr int E = decltype(e)::value, K = decltype(k)::value;
-        if constexpr (E > 1 && K * E <= kRmsFewElements && !RES && !Q) {
+    auto direct = [&](auto kernel) { kernel<<<(unsigned)g.blocks, g.threads, 0, st>>>(p); };
+    by_k(g.K, [&](auto k) -> void {
+        constexpr int K = decltype(k)::value, E = kVec<T>;
+        if (!g.vec) {
+            if constexpr (K != 3) direct(rms_forward_kernel<T, 1, K, RES, Q, void>);
+            return;
+        }
+        if constexpr (K <= 4) {
             if (g.ring > 0) {
                 constexpr int S = rms_forward_stages(K);
-                const size_t smem = (size_t)S * K * g.threads * 16;
-                auto kernel = rms_forward_ring_kernel<T, E, K, S>;
-                static std::atomic<int> ready[64];
-                fine = allow_smem(kernel, ready, 224 * 1024);
-                if (fine) kernel<<<(unsigned)g.ring, g.threads, smem, st>>>(p);
+                const size_t smem = (size_t)S * (RES ? 2 : 1) * K * g.threads * 16;
+                auto stay = [&](auto kernel, std::atomic<int> *ready) {
+                    fine = allow_smem(kernel, ready, 224 * 1024);
+                    if (fine) kernel<<<(unsigned)g.ring, g.threads, smem, st>>>(p);
+                };
+                static std::atomic<int> ready[2][64];
+                if (g.shift) {
+                    if constexpr (E == 8) stay(rms_forward_ring_kernel<T, K, S, RES, Q, true>, ready[0]);
+                } else if constexpr (!RES && !Q) {
+                    stay(rms_forward_ring_kernel<T, K, S, RES, Q, false>, ready[1]);
+                }
                 return;
             }
+            if constexpr (K * E <= 24) {
+                const bool full = g.lanes_log2 == 5 && p.C == (int64_t)32 * g.warps * K * E && p.rows % g.rpb == 0;
+                constexpr bool WIDE = E == 8 && K == 2 && !Q;
+                if (full && p.weight) {
+                    if (WIDE && g.threads > 256)
+                        return p.wide ? direct(rms_forward_kernel<T, E, K, RES, Q, float, WIDE>)
+                                      : direct(rms_forward_kernel<T, E, K, RES, Q, T, WIDE>);
+                    return p.wide ? direct(rms_forward_kernel<T, E, K, RES, Q, float>)
+                                  : direct(rms_forward_kernel<T, E, K, RES, Q, T>);
+                }
+            }
         }
-        auto direct = [&](auto kernel) { kernel<<<(unsigned)g.blocks, g.threads, 0, st>>>(p); };
-        if constexpr (E > 1 && K * E <= kRmsFewElements) {
-            const bool full = g.tpr >= 32 && p.C == (int64_t)g.tpr * K * E && p.rows % (g.threads / g.tpr) == 0;
-            if (full && p.weight && p.wide) return direct(rms_forward_kernel<T, E, K, RES, Q, float>);
-            if (full && p.weight) return direct(rms_forward_kernel<T, E, K, RES, Q, T>);
-        }
-        direct(rms_forward_kernel<T, E, K, RES, Q, void>);
+        if constexpr (K <= 8) direct(rms_forward_kernel<T, E, K, RES, Q, void>);
     });
     return fine ? launch_status() : CT_ERR_DEVICE;
 }
@@ -825,27 +976,28 @@ ct_status backward_t(const RmsArgs &a, const RmsGeom &g, cudaStream_t st) {
         }
     } else if (a.rows > 0) {
         p.parts = g.blocks;
-        const size_t slots = p.ws && g.threads > g.tpr ? (size_t)(g.threads / g.tpr) * p.C * 4 : 0;
-        by_geom<T>(g, [&](auto e, auto k) {
-            constexpr int E = decltype(e)::value, K = decltype(k)::value;
-            if constexpr (E == 1) {
-                rms_backward_ones_kernel<T, K><<<(unsigned)g.blocks, g.threads, slots, st>>>(p);
+        const size_t slots = p.ws && g.rpb > 1 ? (size_t)g.rpb * p.C * 4 : 0;
+        by_k(g.K, [&](auto k) -> void {
+            constexpr int K = decltype(k)::value, E = kVec<T>;
+            if (!g.vec) {
+                if constexpr (K != 3)
+                    rms_backward_ones_kernel<T, K><<<(unsigned)g.blocks, g.threads, slots, st>>>(p);
             } else if constexpr (K * E <= 32) {
                 constexpr int S = rms_stages(K);
                 const size_t ring = (size_t)S * (p.dsum ? 3 : 2) * K * g.threads * 16;
                 const size_t smem = ring > slots ? ring : slots;
                 auto go = [&](auto kernel, std::atomic<int> *ready) {
-                    if (!allow_smem(kernel, ready, 224 * 1024)) return false;
-                    kernel<<<(unsigned)g.blocks, g.threads, smem, st>>>(p);
-                    return true;
+                    fine = allow_smem(kernel, ready, 224 * 1024);
+                    if (fine) kernel<<<(unsigned)g.blocks, g.threads, smem, st>>>(p);
                 };
                 static std::atomic<int> ready[4][64];
-                if (g.threads == 256)
-                    fine = p.dsum ? go(rms_backward_kernel<T, E, K, S, true, 256>, ready[0])
-                                  : go(rms_backward_kernel<T, E, K, S, false, 256>, ready[1]);
-                else
-                    fine = p.dsum ? go(rms_backward_kernel<T, E, K, S, true, 512>, ready[2])
-                                  : go(rms_backward_kernel<T, E, K, S, false, 512>, ready[3]);
+                if (g.threads <= 256) {
+                    if (p.dsum) go(rms_backward_kernel<T, K, S, true, 256>, ready[0]);
+                    else go(rms_backward_kernel<T, K, S, false, 256>, ready[1]);
+                } else {
+                    if (p.dsum) go(rms_backward_kernel<T, K, S, true, 512>, ready[2]);
+                    else go(rms_backward_kernel<T, K, S, false, 512>, ready[3]);
+                }
             }
         });
         if (!fine) return CT_ERR_DEVICE;
