@@ -18,6 +18,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The largest magnitude of three, NaN likewise.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kE4m3Max), kLeastScale); }
 
 // Two codes, to nearest even, at most 448 in magnitude (x in the low byte).

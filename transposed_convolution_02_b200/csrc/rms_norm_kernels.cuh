@@ -316,10 +316,17 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, cons
         m[k] = 0.f;
         // what is not there is 0, or 0 * infinity: not looked at
         if (FULL || k * at.step < mine) {
-            const uint32_t bits = SHIFT ? cut.bits(at.first + k * at.step) : (1u << E) - 1;
+            if constexpr (SHIFT) {
+                const uint32_t bits = cut.bits(at.first + k * at.step);
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-                if (!SHIFT || (bits >> j) & 1) m[k] = max_nan(m[k], fabsf(h.at(k, j)));
+                for (int j = 0; j < E; ++j)
+                    if ((bits >> j) & 1) m[k] = max_nan(m[k], fabsf(h.at(k, j)));
+            } else if constexpr (E == 1) {
+                m[k] = fabsf(h.at(k, 0));
+            } else {
+#pragma unroll
+                for (int j = 0; j < E; j += 2) m[k] = max_abs_nan(m[k], h.at(k, j), h.at(k, j + 1));
+            }
         }
     }
     if (SHIFT || p.block == 0) {
@@ -415,7 +422,7 @@ constexpr int rms_forward_registers(int E, int K, bool res, bool codes, bool ful
 }
 
 // Forward, a row's tensors loaded into registers.  FULL: every thread has K
-// vectors of some row, and weights of type W; what is not asked then is most of
+// vectors of one row, of at most 2^31, and weights of type W; what is not asked then is most of
 // the e4m3 form's work ([32768,4096] fp16, each with 64 registers: 149 us, 178
 // when it asks).  WIDE: more than 256 threads.
 template <typename T, int E, int K, bool RES, bool Q, typename W, bool WIDE = false>
@@ -426,12 +433,14 @@ __global__ void __maxnreg__(rms_forward_registers(E, K, RES, Q, !std::is_same_v<
     const Place<K, FULL || E == 1, FULL || (E == 1 && K > 1)> at(p);
     const Cut<E, false> cut(p, 0);
     clear(p, parts[0], sizeof(parts) / 16);
-    const int64_t rpb = p.rpb;
+    // FULL: a row for every slot of the grid
+    const int64_t rpb = p.rpb, last = FULL ? 1 : p.rows;
     int turn = 0;
-    for (int64_t row0 = blockIdx.x * rpb; row0 < p.rows; row0 += gridDim.x * rpb, turn ^= 1) {
-        const int64_t row = row0 + at.slot;
+    for (int64_t row0 = FULL ? 0 : blockIdx.x * rpb; row0 < last; row0 += FULL ? 1 : gridDim.x * rpb, turn ^= 1) {
+        const int64_t row = FULL ? (int64_t)(blockIdx.x * (uint32_t)p.rpb + at.slot) : row0 + at.slot;
         const int mine = row < p.rows ? cut.nv - at.first : 0;
-        const int64_t e0 = row * p.C + (int64_t)at.first * E;
+        const int64_t e0 = (FULL ? (int64_t)((uint64_t)(uint32_t)row * (uint32_t)p.C) : row * p.C) +
+                           (int64_t)at.first * E;
         const T *x = (const T *)p.x + e0, *res = (const T *)p.residual + e0;
         Raw<T, E> rx[K], rr[RES ? K : 1];
 #pragma unroll
@@ -936,7 +945,8 @@ ct_status forward_launch(const RmsParams &p, const RmsGeom &g, cudaStream_t st) 
                 return;
             }
             if constexpr (K * E <= 24) {
-                const bool full = g.lanes_log2 == 5 && p.C == (int64_t)32 * g.warps * K * E && p.rows % g.rpb == 0;
+                const bool full = g.lanes_log2 == 5 && p.C == (int64_t)32 * g.warps * K * E && p.rows % g.rpb == 0 &&
+                                  p.rows <= 0x7FFFFFFF;
                 constexpr bool WIDE = E == 8 && K == 2 && !Q;
                 if (full && p.weight) {
                     if (WIDE && g.threads > 256)
