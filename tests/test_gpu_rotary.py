@@ -104,6 +104,28 @@ def test_layouts(pairs, dtype):
         ct.rotary_nhwc(qkv, sections, out=torch.zeros(64, dtype=t, device="cuda").expand(qkv.shape))
 
 
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("heads", [1, 2, 3, 4])
+def test_images_that_share_positions(heads, dtype):
+    """More images than heads, with one grid, given positions for all or for
+    each: to the bit what each image gives alone; slices of images, one image
+    for all, images behind pixels."""
+    t = TYPES[dtype]
+    g = torch.Generator().manual_seed(5)
+    for n, pairs, sections in ((5, "halves", [16, 24, 24]), (19, "adjacent", [10, 6]), (33, "halves", [50])):
+        dims = {3: [3, 2, 4], 2: [3, 7], 1: [11]}[len(sections)]
+        x = normal([n] + dims + [heads, 72], 17 + n, t)
+        at = torch.randint(-99, 1 << 18, [n] + dims + [len(sections)], generator=g).cuda()
+        turned = x.movedim(0, -3).contiguous().movedim(-3, 0)
+        for images, positions in ((x, None), (x, at[0]), (x, at), (x[::2], None), (x[1::2], at[0]),
+                                  (x[:1].expand(x.shape), at[1]), (turned, None)):
+            y = compare(images, sections, pairs, positions=positions)
+            for i in (0, len(images) - 1):
+                own = positions[i:i + 1] if positions is at else positions
+                assert torch.equal(y[i:i + 1], ct.rotary_nhwc(images[i:i + 1], sections, pairs=pairs, positions=own))
+        compare(x, sections, pairs, positions=at[0], backward=True)
+
+
 @pytest.mark.parametrize("base", [1e-4, 0.5, 1.0, 1e30])
 def test_bases(base):
     """Frequencies above a turn a position, none that differ, and vanishing ones; positions around 2^24, where

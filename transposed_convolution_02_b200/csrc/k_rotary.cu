@@ -4,7 +4,7 @@
 //
 // Bound: HBM, x in and y out.  A thread has the pairs of one vector (or of two,
 // one in each half of the head) of one pixel, makes their sines and cosines
-// once and walks the heads with them in registers.  The angle is formed in
+// once and walks the heads (or images) with them in registers.  The angle is formed in
 // turns.  A position of up to 24 bits times a frequency of two floats (48 bits)
 // gives the fraction of a turn to 2^-26 in fp32: the product's rounding is known
 // exactly (fused multiply-add), and so is the part left of whole turns.  Larger
@@ -12,9 +12,10 @@
 // Measured (GPU time; against the measured copy rate): [2,16x32x32,24,128] bf16
 // 65 us (0.95; 185 with angles in 64 bits and divisions for every pair),
 // [3,57x91,5,72] fp32 10.5 (0.65: two rounds of blocks), one head of 64 at
-// [16,64x64x16] bf16 97 (0.42: nothing shares the angles), heads of 72 with
+// [16,64x64x16] bf16 44 (0.93: the images share the angles), heads of 72 with
 // sides 35 apart 60 (0.57: single elements).
 #include <type_traits>
+#include <utility>
 
 #include "ct_cuda_util.h"
 #include "rotary.h"
@@ -343,6 +344,14 @@ ct_status run(int pairs, RotaryParams &p, cudaStream_t st) {
 }  // namespace
 
 ct_status rotary_run(int dtype, int pairs, RotaryParams &p, cudaStream_t st) {
+    // Images whose positions are the same share angles as heads do: where heads
+    // are few, a thread walks the images ([16,64x64x16,1,64] bf16 44 us, 97 with
+    // each image's angles made again).
+    if (p.H < kHeads<8> && p.N > p.H && p.N < 1 << 24 && (p.pos_type == CT_POSITION_GRID || p.pos_image == 0)) {
+        std::swap(p.N, p.H);
+        std::swap(p.xs[0], p.xs[2]);
+        std::swap(p.ys[0], p.ys[2]);
+    }
     if (dtype == CT_F32) return run<float, 4>(pairs, p, st);
     if (dtype == CT_F16) return run<__half, 8>(pairs, p, st);
     return run<__nv_bfloat16, 8>(pairs, p, st);
