@@ -109,6 +109,50 @@ def test_channels(c, dtype):
                  pdtype=[torch.float32, t][(i + k) % 2], block=[0, 32, 64, 128][(i + 3 * k) % 4])
 
 
+WARPS = [320, 384, 448, 640, 768, 896, 1152, 1280, 1536, 1792, 2304, 2560, 3584, 5120, 6144, 7168, 10240, 12288, 14336]
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("c", WARPS)
+def test_rows_of_any_number_of_warps(c, dtype):
+    """Rows of 3, 5, 6, 7 ... warps and of 24 elements a thread: whole ones, and with rows that no slot has."""
+    for k, rows in enumerate((1, 6, 7, 1200 if c < 2000 else 450)):
+        all_ways([rows, c], TYPES[dtype], c + k, residual=k % 2 == 0, weight=k != 2,
+                 pdtype=[torch.float32, TYPES[dtype]][k // 2], block=[0, 128, 32, 0][k])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("c", [32, 33, 34, 36, 100, 255, 1001, 2047, 8191, 12001, 16381, 24001, 32765])
+def test_neighbours_in_a_vector(c, residual, dtype):
+    """Rows that share vectors with their neighbours: NaN and infinities in those leave a row to the bit what it
+    is beside zeros, and what is not written stays; one round of blocks and several."""
+    t = TYPES[dtype]
+    for rows in (3, 11, 60000 if c <= 100 else 3000 if c <= 1001 else 301):
+        x, r, w, _, _ = inputs([rows, c], t, c + rows)
+        r = r if residual else None
+        for first in (0, 1):
+            clean, foul = x.clone(), x.clone()
+            clean[1 - first::2] = 0
+            foul[1 - first::2] = float("nan")
+            foul[1 - first::4] = float("inf")
+            own = slice(first, None, 2)
+            for call in (ct.rms_norm_nhwc, ct.rms_norm_nhwc_e4m3):
+                a, b = (call(v, w, eps=EPS, residual=r, return_rstd=True) for v in (clean, foul))
+                for p, q in zip(a, b):
+                    p, q = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (p, q))
+                    assert torch.equal(p[own], q[own])
+        flat = torch.full((rows * c + 16,), 7.0, dtype=t, device="cuda")
+        out = flat[8:-8].view(rows, c)
+        ct.rms_norm_nhwc(x, w, eps=EPS, residual=r, out=out)
+        assert bool((flat[:8] == 7).all()) and bool((flat[-8:] == 7).all())
+        want = ct.rms_norm_nhwc(x, w, eps=EPS, residual=r)
+        assert torch.equal(out, want[0] if residual else want)
+        over, into = x.clone(), None if r is None else r.clone()               # in place
+        ct.rms_norm_nhwc(over, w, eps=EPS, residual=into, out=over, sum_out=into)
+        assert torch.equal(over, out) and (r is None or torch.equal(into, want[1]))
+
+
 @pytest.mark.parametrize("dtype", sorted(TYPES))
 @pytest.mark.parametrize("block", [0, 32, 64, 128])
 @pytest.mark.parametrize("c", [32, 33, 100, 128, 200, 264, 511, 1024, 2056, 16400, 33000])
