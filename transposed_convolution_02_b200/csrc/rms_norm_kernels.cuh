@@ -433,13 +433,17 @@ __global__ void __maxnreg__(rms_forward_registers(E, K, RES, Q, !std::is_same_v<
     const Place<K, FULL || E == 1, FULL || (E == 1 && K > 1)> at(p);
     const Cut<E, false> cut(p, 0);
     clear(p, parts[0], sizeof(parts) / 16);
-    // FULL: a row for every slot of the grid
-    const int64_t rpb = p.rpb, last = FULL ? 1 : p.rows;
+    // FULL: the grid has a slot for every row, and no loop is needed; where the
+    // codes' kernel has 16 elements in 40 registers, its addresses crowd them
+    // ([32768,4096] fp16 with a residual 141 us, 139 with the loop; 256 bf16
+    // channels without a residual 60 % of the floor, 50 with it).
+    constexpr bool ONCE = FULL && !(Q && K * E == kRmsFewElements && (RES || E == 4));
+    const int64_t rpb = p.rpb, last = ONCE ? 1 : p.rows;
     int turn = 0;
-    for (int64_t row0 = FULL ? 0 : blockIdx.x * rpb; row0 < last; row0 += FULL ? 1 : gridDim.x * rpb, turn ^= 1) {
-        const int64_t row = FULL ? (int64_t)(blockIdx.x * (uint32_t)p.rpb + at.slot) : row0 + at.slot;
+    for (int64_t row0 = ONCE ? 0 : blockIdx.x * rpb; row0 < last; row0 += ONCE ? 1 : gridDim.x * rpb, turn ^= 1) {
+        const int64_t row = ONCE ? (int64_t)(blockIdx.x * (uint32_t)p.rpb + at.slot) : row0 + at.slot;
         const int mine = row < p.rows ? cut.nv - at.first : 0;
-        const int64_t e0 = (FULL ? (int64_t)((uint64_t)(uint32_t)row * (uint32_t)p.C) : row * p.C) +
+        const int64_t e0 = (ONCE ? (int64_t)((uint64_t)(uint32_t)row * (uint32_t)p.C) : row * p.C) +
                            (int64_t)at.first * E;
         const T *x = (const T *)p.x + e0, *res = (const T *)p.residual + e0;
         Raw<T, E> rx[K], rr[RES ? K : 1];
