@@ -66,9 +66,9 @@ const int kVectors[] = {1, 2, 3, 4, 8, 0}, kSingle[] = {1, 2, 4, 8, 16, 32, 0};
 // three 77, 16 in two, one of them half empty, 66; without codes 97, 94, 83.
 double cost_codes(int e) { return e < 8 ? 1.4 : e < 12 ? 1.1 : e <= 16 ? 1.0 : e <= 24 ? 1.08 : e <= 32 ? 1.2 : 1.4; }
 double cost_plain(int e) { return e < 8 ? 1.4 : e < 12 ? 1.1 : e <= 16 ? 1.0 : e <= 24 ? 1.03 : e <= 32 ? 1.2 : 1.4; }
-// The ring of 16-bit elements: as above without what fills a warp (bf16 of 256
-// channels 83 % either way).
-double cost_ring(int e) { return e < 12 ? 1.2 : e <= 16 ? 1.0 : e <= 24 ? 1.03 : e <= 32 ? 1.2 : 1.4; }
+// The ring of 16-bit elements: eight of them keep little in flight (1280 channels
+// 61 %, 16 with a sixth of the places empty 72).
+double cost_ring(int e) { return e < 12 ? 1.45 : e <= 16 ? 1.0 : e <= 24 ? 1.03 : e <= 32 ? 1.2 : 1.4; }
 // fp32 elements: 16 or as many as there are (320 channels 87 %, 12: 81).
 double cost_ring32(int e) { return e < 12 ? 1.5 : e < 16 ? 1.4 : e == 16 ? 1.0 : 1.6; }
 // Rows that start inside a vector: the masks weigh less on more of them (1001
@@ -101,24 +101,32 @@ RmsGeom rms_forward_geom(const RmsArgs &a, bool aligned) {
     g.shift = aligned && V == 8 && a.C % V != 0 && a.C >= 32 && !blocks;
     g.vec = aligned && (a.C % V == 0 || g.shift);
     // Blocks that stay for many rows.  With one tensor to read they keep more bytes
-    // in flight (bf16 of 4096 channels 80 % of the floor, 75 without; 1536 82 and
-    // 61, 16384 87 and 49); with a residual (190 us, 157 without, for [32768,4096])
+    // in flight (bf16 of 8192 channels 77 % of the floor, 68 without; 16384 87 and
+    // 49; 320 64 and 56); with a residual (190 us, 157 without, for [32768,4096])
     // and for codes (34 %, 41 without) they do not, nor with fp32 elements (83 %,
-    // 98 without) but in short rows (64 channels 87 and 65).
-    const bool stays = g.shift || (!a.residual && !codes && (V == 8 || a.C < 128));
+    // 98 without) but in short rows (64 channels 87 and 65), nor where 16-bit rows
+    // of at most 256 threads fill them with 16 elements each, which takes but 32
+    // registers (1024 channels 83 %, 87 without; 4096 80 and 82).
+    bool stays = g.shift || (!a.residual && !codes && (V == 8 || a.C < 128));
     if (g.vec) {
         // Eight neighbours at least read 128 bytes together; a block's channels lie
         // in one warp.  Blocks of 128 threads: e4m3 of 1536 channels 93 %, of 256
         // threads 76.
-        Choice c = {kVectors, blocks && a.block / V > 8 ? a.block / V : 8, 1024, codes ? cost_codes : cost_plain,
-                    0.87, 128};
-        if (stays) {
-            c.cost = g.shift ? cost_shift : V == 8 ? cost_ring : cost_ring32;
-            c.whole = 1.0;
-            c.most = kMaxTpr;
-        }
+        const Choice direct = {kVectors, blocks && a.block / V > 8 ? a.block / V : 8, 1024,
+                               codes ? cost_codes : cost_plain, 0.87, 128};
+        Choice ring = direct;
+        ring.cost = g.shift ? cost_shift : V == 8 ? cost_ring : cost_ring32;
+        ring.whole = 1.0;
+        ring.most = kMaxTpr;
         // a row that starts inside a vector has one vector more
-        spread(g, g.shift ? (a.C + 2 * V - 2) / V : a.C / V, V, c);
+        const int64_t n = g.shift ? (a.C + 2 * V - 2) / V : a.C / V;
+        if (!g.shift) {
+            spread(g, n, V, direct);
+            if (stays && V == 8 && g.K == 2 && g.threads <= 256 && n == (int64_t)64 * g.warps && g.lanes_log2 == 5 &&
+                a.weight && a.rows % g.rpb == 0)
+                stays = false;
+        }
+        if (stays) spread(g, n, V, ring);
         if (g.shift && (g.K == 0 || g.K > 4)) g.vec = g.shift = false;
     }
     if (!g.vec) {

@@ -10,7 +10,7 @@
 // only the sizes set: lanes, warps, then (dw) rows of a block, blocks.
 // Measured (GPU time; against the measured copy rate): [8,64x64,1024] bf16 with
 // a residual 42 us (0.98), e4m3 [32768,4096] fp16 with a residual 139 (1.04),
-// [32768,4096] bf16 without 90 (0.91), backward [16,112x112,512] fp16 with the
+// [32768,4096] bf16 without 85 (0.96), backward [16,112x112,512] fp16 with the
 // sum's gradient 124 (1.01), rows of 511 bf16 forward 100 (0.82), backward 132
 // (0.62).
 #pragma once
@@ -413,10 +413,13 @@ __device__ __forceinline__ float squares(const Elements<E, K> &h) {
 // while others sum up.  bf16 with a residual, of the floor: e4m3 of 1024 channels
 // 94 % with 40, 91 with 48, 84 with 64; 8192 channels, without codes, 95 with 40
 // (three blocks an SM), 86 with 48 (two); 1024 channels 97 with 40, 98 with 48.
-// 256 channels, 8 elements a thread, as e4m3: 90 with 32, 83 with 40.
+// 256 channels, 8 elements a thread, as e4m3: 90 with 32, 83 with 40.  Without a
+// residual 1024 channels 87 with 32, 85 with 40; as e4m3, 62 with 40, 52 with 32
+// (spilled).
 constexpr int rms_forward_registers(int E, int K, bool res, bool codes, bool full, bool wide) {
     if (E == 1) return K <= 4 ? 32 : K == 8 ? (codes ? 48 : 40) : K == 16 ? 64 : 128;
     if (K * E <= 8) return 32;
+    if (full && E == 8 && K == 2 && !res && !codes && !wide) return 32;
     if (K * E <= kRmsFewElements) return full && (E == 8 ? codes || wide : codes && !res) ? 40 : 48;
     return K * E <= 24 ? (full ? 56 : 64) : 128;
 }
