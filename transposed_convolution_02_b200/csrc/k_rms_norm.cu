@@ -58,7 +58,12 @@ void spread(RmsGeom &g, int64_t n, int V, const Choice &c) {
     g.threads = g.rpb * tpr;
 }
 
-const int kVectors[] = {1, 2, 3, 4, 8, 0}, kSingle[] = {1, 2, 4, 8, 16, 32, 0};
+// Numbers of vectors a thread that some row's lowest cost is: the kernels have
+// no others.
+const int kDirect16[] = {1, 2, 3, 8, 0}, kDirect32[] = {1, 2, 3, 4, 0};
+const int kRing16[] = {1, 2, 3, 4, 8, 0}, kRing32[] = {1, 4, 0};
+const int kBack16[] = {1, 2, 4, 0}, kBack32[] = {1, 2, 3, 4, 8, 0};
+const int kSingle[] = {1, 2, 4, 8, 16, 0}, kBackSingle[] = {1, 2, 4, 8, 16, 32, 0};
 
 // Costs, from what part of the floor each way reached with the others' places
 // as full.  16 elements a thread are best where nothing else decides (e4m3 of
@@ -112,9 +117,10 @@ RmsGeom rms_forward_geom(const RmsArgs &a, bool aligned) {
         // Eight neighbours at least read 128 bytes together; a block's channels lie
         // in one warp.  Blocks of 128 threads: e4m3 of 1536 channels 93 %, of 256
         // threads 76.
-        const Choice direct = {kVectors, blocks && a.block / V > 8 ? a.block / V : 8, 1024,
+        const Choice direct = {V == 8 ? kDirect16 : kDirect32, blocks && a.block / V > 8 ? a.block / V : 8, 1024,
                                codes ? cost_codes : cost_plain, 0.87, 128};
         Choice ring = direct;
+        ring.vectors = V == 8 ? kRing16 : kRing32;
         ring.cost = g.shift ? cost_shift : V == 8 ? cost_ring : cost_ring32;
         ring.whole = 1.0;
         ring.most = kMaxTpr;
@@ -165,13 +171,12 @@ int64_t rms_parts(int64_t rows, int64_t C) {
 }
 
 RmsGeom rms_backward_geom(const RmsArgs &a, bool aligned) {
-    static const int vec8[] = {1, 2, 3, 4, 0};
     RmsGeom g = {};
     const int V = a.dtype == CT_F32 ? 4 : 8;
     g.vec = aligned && a.C % V == 0;
     // blocks of 256 threads (1536 channels 78 %, of 128: 56)
-    if (g.vec) spread(g, a.C / V, V, {V == 8 ? vec8 : kVectors, 8, kMaxTpr, cost_back, 1.0, 256});
-    else spread(g, a.C, 1, {kSingle, 32, kMaxTpr, cost_single, 1.0, 256});
+    if (g.vec) spread(g, a.C / V, V, {V == 8 ? kBack16 : kBack32, 8, kMaxTpr, cost_back, 1.0, 256});
+    else spread(g, a.C, 1, {kBackSingle, 32, kMaxTpr, cost_single, 1.0, 256});
     const int64_t rounds = ceil_div(a.rows, (int64_t)g.rpb);
     // one round of resident blocks, as the ring lets them be
     int64_t parts = rms_parts(a.rows, a.C);

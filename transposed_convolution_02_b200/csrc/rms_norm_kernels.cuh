@@ -932,7 +932,7 @@ ct_status forward_launch(const RmsParams &p, const RmsGeom &g, cudaStream_t st) 
     by_k(g.K, [&](auto k) -> void {
         constexpr int K = decltype(k)::value, E = kVec<T>;
         if (!g.vec) {
-            if constexpr (K != 3) direct(rms_forward_kernel<T, 1, K, RES, Q, void>);
+            if constexpr (K != 3 && K <= 16) direct(rms_forward_kernel<T, 1, K, RES, Q, void>);
             return;
         }
         if constexpr (K <= 4) {
@@ -946,7 +946,7 @@ ct_status forward_launch(const RmsParams &p, const RmsGeom &g, cudaStream_t st) 
                 static std::atomic<int> ready[2][64];
                 if (g.shift) {
                     if constexpr (E == 8) stay(rms_forward_ring_kernel<T, K, S, RES, Q, true>, ready[0]);
-                } else if constexpr (!RES && !Q) {
+                } else if constexpr (!RES && !Q && (E == 8 || K == 1 || K == 4)) {
                     stay(rms_forward_ring_kernel<T, K, S, RES, Q, false>, ready[1]);
                 }
                 return;
@@ -964,7 +964,9 @@ ct_status forward_launch(const RmsParams &p, const RmsGeom &g, cudaStream_t st) 
                 }
             }
         }
-        if constexpr (K <= 8) direct(rms_forward_kernel<T, E, K, RES, Q, void>);
+        // four vectors of 16-bit elements: rows of the ring that are too few for it
+        if constexpr (E == 8 ? K <= 3 || K == 8 || (K == 4 && !RES && !Q) : K <= 4)
+            direct(rms_forward_kernel<T, E, K, RES, Q, void>);
     });
     return fine ? launch_status() : CT_ERR_DEVICE;
 }
@@ -999,7 +1001,7 @@ ct_status backward_t(const RmsArgs &a, const RmsGeom &g, cudaStream_t st) {
             if (!g.vec) {
                 if constexpr (K != 3)
                     rms_backward_ones_kernel<T, K><<<(unsigned)g.blocks, g.threads, slots, st>>>(p);
-            } else if constexpr (K * E <= 32) {
+            } else if constexpr (K * E <= 32 && (E == 4 || K != 3)) {
                 constexpr int S = rms_stages(K);
                 const size_t ring = (size_t)S * (p.dsum ? 3 : 2) * K * g.threads * 16;
                 const size_t smem = ring > slots ? ring : slots;
