@@ -1,0 +1,53 @@
+"""Root-mean-square norm, rotary positions and AdamW without a GPU: calls that
+the binding has to refuse, and settings that may not be kept by what they are."""
+
+import ctypes
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from test_blocks_host import FLAT, HEADS, OUT, R, X, Card, card, rotary_desc
+from transposed_convolution_02_b200 import ct
+
+
+def test_parameters_that_change_where_they_lie():
+    """Everything that the kernel relies on is looked at again: a parameter at its old address with other strides,
+    another type or another number of elements, and lists that lost or gained one."""
+    def made():
+        p, q = card(4, 4), card(6, dtype=torch.float16)
+        return p, q, ct.AdamW([p, q]), [card(4, 4), card(6, dtype=torch.float16)]
+
+    p, q, opt, g = made()
+    p.data = p.data.t()
+    with pytest.raises(ValueError, match="parameter 0"):
+        opt.step(g)
+    p, q, opt, g = made()
+    q.data = q.data.view(torch.bfloat16)
+    with pytest.raises(ValueError, match="parameter 1"):
+        opt.step(g)
+    p, q, opt, g = made()
+    p.data = p.data.view(torch.float16)[:, ::2]                    # 16 elements, 2 bytes each, at the same address
+    with pytest.raises(ValueError, match="parameter 0"):
+        opt.step(g)
+    p, q, opt, g = made()
+    with pytest.raises(ValueError, match="parameters"):
+        opt.params.pop(0)
+        opt.step(g[1:])
+    p, q, opt, g = made()
+    opt.params.append(card(3))
+    with pytest.raises(ValueError, match="parameters"):
+        opt.step(g + [card(3)])
+
+
+def test_states_that_change_where_they_lie():
+    opt = ct.AdamW([card(40)])
+    kept = opt.exp_avg
+    for other in (kept.view(torch.int32), kept.view(16, 16).t()):
+        opt.exp_avg = other
+        with pytest.raises(ValueError, match="exp_avg"):
+            opt.step([card(40)])
+    opt = ct.AdamW([card(40)], bits=8)
+    opt.exp_avg_sq = opt.exp_avg_sq.view(torch.uint8)
+    with pytest.raises(ValueError, match="exp_avg_sq"):
+        opt.step([card(40)])

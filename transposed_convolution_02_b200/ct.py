@@ -1171,9 +1171,14 @@ class AdamW:
                 at += blocks[i] * BLOCK
         self._kept = [t.numel() if t is not None else 0 for t in self._states()]
         self._kept_at = self._kept_places()
+        self._kept_as = self._kept_looks()
 
     def _states(self):
         return self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.master
+
+    def _kept_looks(self):
+        """What tells whether the states still are those that _kept_places saw."""
+        return [None if t is None else (t.data_ptr(), t.numel(), t.dtype, t.is_contiguous()) for t in self._states()]
 
     def _kept_places(self):
         """The states' addresses; a tensor in the place of one has to be like it."""
@@ -1231,6 +1236,8 @@ class AdamW:
         and counts with it.  Gradients may not overlap parameters or states."""
         grads = list(grads)
         params = self.params
+        if len(params) != len(self._sizes):
+            raise ValueError("%d parameters, not the %d that the states are for" % (len(params), len(self._sizes)))
         if len(grads) != len(params):
             raise ValueError("%d gradients for %d parameters" % (len(grads), len(params)))
         try:
@@ -1241,12 +1248,13 @@ class AdamW:
             self._meta = None
             self._grads(grads)
             self._meta = meta
-        if list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes:
+        # all that the kernel relies on: a parameter can become another at its old address
+        if (list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes
+                or list(map(_dtype, params)) != self._dtypes or not all(map(_dense, params))):
             self._at = self._places()
-        states = self._states()
-        if ([_addr(t) for t in states] != self._kept_at
-                or [0 if t is None else t.numel() for t in states] != self._kept):
+        if self._kept_looks() != self._kept_as:
             self._kept_at = self._kept_places()
+            self._kept_as = self._kept_looks()
         d, lr = self._desc, self.lr
         d.beta1, d.beta2 = self.betas
         d.eps, d.seed = self.eps, self.seed
