@@ -457,10 +457,12 @@ typedef struct ct_adamw_desc {
     int64_t step;           /* 1 for the first update */
     uint64_t seed;          /* bits = 8 alone */
     /* on the device, read by the kernel in place of the numbers above; NULL:
-     * not.  A captured graph so takes another step and rate at each replay. */
+     * not.  A captured graph so takes another step and rate at each replay.
+     * A rate that is negative or not finite, a step below 1 and a grad_scale
+     * that is no positive finite number skip the update: nothing is written. */
     const float *lr_device;
     const int64_t *step_device;
-    const float *grad_scale;    /* NULL: 1.  What is no positive finite number skips the update: nothing is written */
+    const float *grad_scale;    /* NULL: 1 */
 } ct_adamw_desc;
 
 /* One update.  shapes, params and grads are host arrays of `count` entries, read

@@ -145,6 +145,9 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (!(gs > 0.f && gs <= 3.4028234e38f)) return;      // nothing is touched
     const uint64_t t = p.step_dev ? (uint64_t)*p.step_dev : p.step;
     const Step s = step_of(p, t);
+    // nor by a step or a rate on the device that the host's numbers may not be
+    // (1 - b^0 is no divisor)
+    if ((int64_t)t < 1 || !(s.lr >= 0.f && s.lr <= 3.4028234e38f)) return;
     int i = find(table, block);
     for (int k = 0; k < per && block < table.blocks; ++k, block += kWarps) {
         while (i + 1 < table.count && table.t[i + 1].first <= block) ++i;

@@ -1233,7 +1233,9 @@ class AdamW:
         update.  ``steps`` counts the updates, skipped ones too; ``step``, an
         int64 CUDA tensor of one element, is the number of this update (1 for
         the first) in its place, read on the device: a captured graph needs it,
-        and counts with it.  Gradients may not overlap parameters or states."""
+        and counts with it.  A step below 1, and an lr on the device that is
+        negative or not finite, skip the update too.  Gradients may not overlap
+        parameters or states."""
         grads = list(grads)
         params = self.params
         if len(params) != len(self._sizes):
