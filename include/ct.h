@@ -397,8 +397,9 @@ typedef enum ct_position_type {
  * repeat (strides of 0); y's elements must be apart.  Limits: N, heads, dim
  * and the grid's sizes in [0, 2^30], dim >= 1, sum(sections) <= dim and <=
  * 512, each section >= 0 and even (CT_ERR_CHANNELS), 1 to 3 axes
- * (CT_ERR_SPAN), base > 0 and finite, at most 2^60 elements, and no stride
- * past 2^60 / 4 in magnitude; y's not negative (CT_ERR_ATTR). */
+ * (CT_ERR_SPAN), base > 0 and finite, every frequency finite in 64 bits (bases
+ * from 2^-1022 on are), at most 2^60 elements, and no stride past 2^60 / 4 in
+ * magnitude; y's not negative (CT_ERR_ATTR). */
 typedef struct ct_rotary_desc {
     int32_t dtype;          /* ct_dtype */
     int32_t axes;           /* 1..3 */

@@ -51,3 +51,11 @@ def test_states_that_change_where_they_lie():
     opt.exp_avg_sq = opt.exp_avg_sq.view(torch.uint8)
     with pytest.raises(ValueError, match="exp_avg_sq"):
         opt.step([card(40)])
+
+
+@pytest.mark.parametrize("base, status", [(1e-300, 0), (1e-40, 0), (5e-324, 4), (1e-310, 0), (1e-315, 4)])
+def test_frequencies_past_64_bits(base, status):
+    """They are refused; all others are taken (nothing is launched for no images).  The last of 256 pairs has
+    base^(-255 / 256) / 2 pi: 9.8e307 for 1e-310."""
+    d = rotary_desc(base=base, sections=[0, 512, 0], dim=512, N=0)
+    assert ct.lib().ct_rotary(ctypes.byref(d), None, None, None, None) == status

@@ -39,3 +39,26 @@ def test_device_steps_and_rates_that_skip(bits):
     opt.step(grads, step=step)
     assert not same(everything(opt), kept)
     assert all(bool(p.isfinite().all()) for p in params)
+
+
+# ---- rotary positions ---------------------------------------------------------------
+
+@pytest.mark.parametrize("base", [1e-36, 1e-38, 1e-40, 1e-100, 1e-300])
+def test_frequencies_that_fp32_does_not_hold(base):
+    """Position 0 turns nothing whatever the frequency; others stay turns."""
+    x = normal([2, 3, 2, 132], 3)
+    for kind in (None, torch.int32, torch.int64, torch.float32):
+        at = None if kind is None else torch.tensor([[0], [0], [2]], dtype=kind, device="cuda")
+        for pairs in ("adjacent", "halves"):
+            y = ct.rotary_nhwc(x, [128], base=base, pairs=pairs, positions=at)
+            still = 1 if kind is None else 2
+            assert torch.equal(y[:, :still], x[:, :still])
+            assert bool(y.isfinite().all())
+            # a turn keeps lengths: c and s are good to 1.5 u each (2.2 u of a pair's length), two products and a
+            # sum of each side lose 2 u, twice that of the squares
+            assert torch.allclose((y.double() ** 2).sum(-1), (x.double() ** 2).sum(-1), rtol=16 * ref.U, atol=0)
+            # the first pair turns by its position, 2
+            i, k = (0, 1) if pairs == "adjacent" else (0, 64)
+            v, w = x[:, 2, :, i].double(), x[:, 2, :, k].double()
+            want = v * math.cos(2.0) - w * math.sin(2.0)
+            assert bool(((y[:, 2, :, i].double() - want).abs() <= 5 * ref.U * (v.abs() + w.abs())).all())

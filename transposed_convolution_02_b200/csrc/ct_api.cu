@@ -393,7 +393,10 @@ ct_status resolve_rotary(const ct_rotary_desc *d, RotaryParams *p) {
     // 24 bits, and at most 2^22 turns, so that what is left of them has its bits
     double fastest = 0.0;
     for (int64_t q = 0; q < rot / 2; ++q) fastest = fmax(fastest, p->turns[q]);
+    if (!isfinite(fastest)) return CT_ERR_ATTR;
     p->near = (float)fmin(16777216.0, fastest > 0.0 ? 4194304.0 / fastest : 16777216.0);
+    // a frequency that fp32 does not hold: every position takes 64 bits, 0 too
+    if (!isfinite((float)fastest)) p->near = -1.f;
     p->small_grid = 1;
     for (int a = 0; a < d->axes; ++a) p->small_grid = p->small_grid && (double)d->grid[a] <= (double)p->near;
     for (int a = 0; a < 3; ++a) {

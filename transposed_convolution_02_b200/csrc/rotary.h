@@ -21,7 +21,7 @@ struct RotaryParams {
     int32_t first[3];            // each axis' first pair
     int32_t pos_type;            // ct_position_type
     float sign;                  // -1: the inverse
-    float near;                  // positions up to it take frequencies of two floats
+    float near;                  // positions up to it take frequencies of two floats; -1: none does
     int32_t small_grid;          // all indices of the grid are
     // set by rotary_run
     int32_t items;               // of a head, each one thread's
