@@ -326,10 +326,12 @@ CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const vo
  * sum's; param_dtype weight's and its gradient's, CT_F32 or dtype.
  *
  * e4m3 output: y is not rounded to dtype but held as codes and fp32 scales,
- *     scale = max(max |y| / 448, 2^-126) of a block,   q = e4m3(y * (1 / scale)), to nearest even;
+ *     scale = max(max |y| * (1 / 448), 2^-126) of a block,   q = e4m3(y * (1 / scale)), to nearest even,
+ * each reciprocal and product rounded to fp32;
  * a block is `block` neighbouring channels of a row (32, 64 or 128; the last
  * one of a row may be shorter), or all C of them for 0.  q * scale is the
- * value.  A block with a NaN or an infinity in it has a scale of NaN.
+ * value.  A block with a NaN or an infinity in it (of y: a weight can make one
+ * of a finite h) has a scale of NaN.
  *
  * Limits: 1 <= C <= 2^24 (CT_ERR_CHANNELS), rows * C <= 2^60. */
 typedef struct ct_rms_norm_desc {

@@ -62,3 +62,72 @@ def test_frequencies_that_fp32_does_not_hold(base):
             v, w = x[:, 2, :, i].double(), x[:, 2, :, k].double()
             want = v * math.cos(2.0) - w * math.sin(2.0)
             assert bool(((y[:, 2, :, i].double() - want).abs() <= 5 * ref.U * (v.abs() + w.abs())).all())
+
+
+# ---- root-mean-square norm ------------------------------------------------------------
+
+FULL = [256, 512, 768, 1024, 2048, 4096, 8192]       # rows of whole warps, each thread with all of its vectors
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("c", FULL + [64, 100, 511, 40000])
+def test_values_at_the_edges_with_weights(c, dtype):
+    """Rows of zeros, infinities and NaN in the kernels that whole rows with a weight have: they keep to themselves,
+    with a residual and without, weights in both types."""
+    t, rows = TYPES[dtype], 64
+    for pdtype in (torch.float32, t):
+        for residual in (False, True):
+            x, r, w, _, _ = inputs([rows, c], t, 151, pdtype)
+            r = r if residual else None
+            foul, clean = x.clone(), x
+            foul[2] = 0
+            foul[4, c // 2] = float("inf")
+            foul[6, 3] = float("nan")
+            foul[9, c - 1] = -float("inf")
+            foul[17, 0] = float("nan")
+            odd = [2, 4, 6, 9, 17]
+            rest = [i for i in range(rows) if i not in odd]
+            if r is not None:
+                r[2] = 0
+            for block in (None, 0, 32, 128):       # None: the type's own output
+                def call(v):
+                    if block is None:
+                        return ct.rms_norm_nhwc(v, w, eps=EPS, residual=r, return_rstd=True)
+                    return ct.rms_norm_nhwc_e4m3(v, w, block=block or None, eps=EPS, residual=r, return_rstd=True)
+                a, b = call(clean), call(foul)
+                for p, q in zip(a, b):
+                    p, q = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (p, q))
+                    assert torch.equal(p[rest], q[rest])
+                rstd = b[-1]
+                assert bool(rstd[[6, 17]].isnan().all()) and not rstd[[4, 9]].any()
+                assert abs(float(rstd[2]) * EPS ** 0.5 - 1) < 1e-6
+                y = b[0].float() if block is None else b[0].float() * ref.spread_scales(b[1], block, c)
+                assert not y[2].any() and bool(y[[6, 17]].isnan().all())
+                assert bool(y[4, c // 2].isnan()) and bool(y[9, c - 1].isnan())
+                if block is not None:
+                    assert bool((b[1][2] == ref.LEAST_SCALE).all()) and bool(b[1][[6, 17]].isnan().all())
+                    at = c // 2 // block if block and block < c else None
+                    assert bool((b[1][4] if at is None else b[1][4][at]).isnan().all())
+                    if at is not None:             # blocks beside the infinity's are of zeros
+                        assert int(b[1][4].isnan().sum()) == 1
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("c", [32, 64, 100, 256, 511, 1024, 4096, 20000])
+def test_products_that_overflow(c, dtype):
+    """A block whose y is infinite though its x is not has a scale of NaN, as every block with an infinity has."""
+    t = TYPES[dtype]
+    x = 1 + normal([8, c], 5).abs().to(t)
+    for how in (float("inf"), 3e38):
+        w = torch.ones(c, device="cuda")
+        w[c // 3] = how
+        x[3, c // 3] = 8.0 * c ** 0.5             # alone it is most of the row: 3e38 times its share of sqrt(c)
+        for block in (0, 32, 128):
+            y = (x.double() / ((x.double() ** 2).mean(-1, keepdim=True) + EPS).sqrt() * w.double()).float()
+            q, scale = ct.rms_norm_nhwc_e4m3(x, w, block=block or None, eps=EPS)
+            width = block or c
+            for b in range(-(-c // width)):
+                part, s = y[:, b * width:(b + 1) * width], (scale[:, b] if block else scale)
+                assert torch.equal(s.isnan(), part.isinf().any(-1)), (how, block, b)
+            v = q.float() * ref.spread_scales(scale, block, c)
+            assert bool(v[y.isinf()].isnan().all())

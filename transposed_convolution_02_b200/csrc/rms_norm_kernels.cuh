@@ -289,6 +289,11 @@ __device__ __forceinline__ float inverse_root(float a) {
     return a > 0.f && a <= 3.4028234e38f ? fmaf(0.5f * r, e, r) : r;
 }
 
+// The scale of a block of codes: NaN where the largest magnitude is infinite too
+// (0 times it is NaN; others this leaves as they are), as a finite h has where
+// the weight's product passes fp32.
+__device__ __forceinline__ float scale_of_codes(float amax) { return scale_of(fmaf(amax, 0.f, amax)); }
+
 // What a thread makes of its part of a row, h, once the row's sum is known: y
 // or its codes.  `mine`: vectors k with k * step < mine are there; e0: where the
 // part starts; w: the weights.
@@ -332,14 +337,14 @@ __device__ __forceinline__ void finish_row(const RmsParams &p, const P &at, cons
     if (SHIFT || p.block == 0) {
 #pragma unroll
         for (int k = 1; k < K; ++k) m[0] = max_nan(m[0], m[k]);
-        m[0] = scale_of(across<Max>(m[0], p, at, parts));
+        m[0] = scale_of_codes(across<Max>(m[0], p, at, parts));
         if ((FULL || mine > 0) && at.lead) p.scale[row] = m[0];
     } else {
         block_max<E, K>(m, p.block);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (at.first + k * at.step) * E;
-            m[k] = scale_of(m[k]);
+            m[k] = scale_of_codes(m[k]);
             if ((FULL || k * at.step < mine) && (c & (p.block - 1)) == 0)
                 p.scale[row * p.blocks_c + (c >> p.block_log2)] = m[k];
         }
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const Rms
             if (p.block == 0) {
                 float m = 0.f;
                 for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) m = max_nan(m, fabsf(y(c, h(c), rstd)));
-                const float scale = scale_of(across<Max>(m, p, at, parts[1])), inv = 1.f / scale;
+                const float scale = scale_of_codes(across<Max>(m, p, at, parts[1])), inv = 1.f / scale;
                 if (threadIdx.x == 0) p.scale[row] = scale;
                 for (int64_t c = threadIdx.x; c < p.C; c += kMaxThreads) {
                     const float v = h(c);
@@ -638,7 +643,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_forward_walk_kernel(const Rms
                         m = max_nan(m, fabsf(v[k]));
                     }
                     for (int o = 16; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                    const float scale = scale_of(m), inv = 1.f / scale;
+                    const float scale = scale_of_codes(m), inv = 1.f / scale;
                     if (lane == 0) p.scale[row * p.blocks_c + b] = scale;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
