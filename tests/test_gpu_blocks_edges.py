@@ -41,6 +41,37 @@ def test_device_steps_and_rates_that_skip(bits):
     assert all(bool(p.isfinite().all()) for p in params)
 
 
+# ---- outputs that lie on inputs -----------------------------------------------------
+
+def outputs(x, r):
+    w = torch.ones(x.shape[-1], device="cuda")
+    heads = x.view(x.shape[0], -1, 2, x.shape[-1] // 2)
+    return {
+        "norm": (x, lambda: ct.rms_norm_nhwc(x, w, out=x)),
+        "norm of a sum": (x, lambda: ct.rms_norm_nhwc(x, w, residual=r, out=x)),
+        "sum": (r, lambda: ct.rms_norm_nhwc(x, w, residual=r, sum_out=r)),
+        "e4m3 sum": (r, lambda: ct.rms_norm_nhwc_e4m3(x, w, residual=r, sum_out=r)),
+        "rotary": (x, lambda: ct.rotary_nhwc(heads, [8], out=heads)),
+        "rotary slice": (x, lambda: ct.rotary_nhwc(heads[:, :, :1], [8], out=heads[:, :, :1])),
+        "rotary back": (x, lambda: ct.rotary_nhwc_backward(heads, [8], out=heads)),
+        "dropout": (x, lambda: ct.dropout(x, 0.5, out=x)),
+        "group norm": (x, lambda: ct.group_norm_nhwc(r, 2, out=x)),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm of a sum", "sum", "e4m3 sum", "rotary", "rotary slice", "rotary back",
+                                  "dropout", "group norm"])
+def test_writes_are_seen_by_autograd(name):
+    """A tensor that a backward pass still needs is not overwritten unnoticed."""
+    x, r = normal([3, 5, 16], 1), normal([3, 5, 16], 2)
+    target, call = outputs(x, r)[name]
+    a = torch.ones_like(target, requires_grad=True)
+    loss = (a * target).sum()
+    call()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
 # ---- rotary positions ---------------------------------------------------------------
 
 @pytest.mark.parametrize("base", [1e-36, 1e-38, 1e-40, 1e-100, 1e-300])

@@ -546,6 +546,12 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _written(*outs):
+    """Tell autograd that these tensors of the caller's were overwritten: what saved one of them for its backward
+    pass is then refused there."""
+    torch.autograd.graph.increment_version([t for t in outs if t is not None])
+
+
 class _Norm:
     """A group norm's descriptor and workspace sizes: sizes only, no memory."""
 
@@ -626,6 +632,8 @@ def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="
                                  _addr(rng), y.data_ptr(), _addr(mean), _addr(rstd), _addr(ws), raw)
         if st != CT_OK:
             raise CtError(st, "ct_group_norm")
+        if out is not None:
+            _written(out)
         return (y, mean, rstd) if return_stats else y
 
     return _run_on(call, x, stream)
@@ -693,6 +701,8 @@ def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream
                               _addr(rng), y.data_ptr(), raw)
         if st != CT_OK:
             raise CtError(st, "ct_dropout")
+        if out is not None:
+            _written(out)
         return y
 
     return _run_on(call, x, stream)
@@ -799,6 +809,8 @@ def rms_norm_nhwc(x, weight=None, *, eps=1e-6, residual=None, out=None, sum_out=
         st = lib().ct_rms_norm(r.desc, xc.data_ptr(), _addr(h), _addr(w), y.data_ptr(), _addr(s), _addr(rstd), raw)
         if st != CT_OK:
             raise CtError(st, "ct_rms_norm")
+        if out is not None or sum_out is not None:
+            _written(out, sum_out)
         if residual is None:
             return (y, rstd) if return_rstd else y
         return (y, s, rstd) if return_rstd else (y, s)
@@ -835,6 +847,8 @@ def rms_norm_nhwc_e4m3(x, weight=None, *, block=None, eps=1e-6, residual=None, s
                                     _addr(s), _addr(rstd), raw)
         if st != CT_OK:
             raise CtError(st, "ct_rms_norm_e4m3")
+        if sum_out is not None:
+            _written(sum_out)
         out = (q, scale) if residual is None else (q, scale, s)
         return out + (rstd,) if return_rstd else out
 
@@ -997,6 +1011,8 @@ def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
         st = lib().ct_rotary(r.desc, xc.data_ptr(), _addr(pos), y.data_ptr(), raw)
         if st != CT_OK:
             raise CtError(st, "ct_rotary")
+        if out is not None:
+            _written(out)
         return y
 
     return _run_on(call, x, stream)
