@@ -53,6 +53,27 @@ def test_states_that_change_where_they_lie():
         opt.step([card(40)])
 
 
+def needs(t):
+    return t.clone().as_subclass(Card).requires_grad_()
+
+
+@pytest.mark.parametrize("call", [
+    lambda: ct.rms_norm_nhwc(X.as_subclass(Card), out=needs(OUT)),
+    lambda: ct.rms_norm_nhwc(X.as_subclass(Card), residual=R, sum_out=needs(OUT)),
+    lambda: ct.rms_norm_nhwc_e4m3(X.as_subclass(Card), residual=R, sum_out=needs(OUT)),
+    lambda: ct.rotary_nhwc(HEADS.as_subclass(Card), [4, 8], out=needs(HEADS)),
+    lambda: ct.rotary_nhwc_backward(HEADS.as_subclass(Card), [4, 8], out=needs(HEADS)),
+    lambda: ct.dropout(X.as_subclass(Card), 0.5, out=needs(OUT)),
+    lambda: ct.group_norm_nhwc(X.as_subclass(Card), 3, out=needs(OUT))])
+def test_outputs_that_require_a_gradient(call):
+    """They are refused as inputs are; under no_grad they are taken (and refused further on, for want of a device)."""
+    with pytest.raises(ValueError, match="gradient"):
+        call()
+    with torch.no_grad(), pytest.raises(Exception) as e:
+        call()
+    assert "gradient" not in str(e.value)
+
+
 @pytest.mark.parametrize("base, status", [(1e-300, 0), (1e-40, 0), (5e-324, 4), (1e-310, 0), (1e-315, 4)])
 def test_frequencies_past_64_bits(base, status):
     """They are refused; all others are taken (nothing is launched for no images).  The last of 256 pairs has

@@ -511,13 +511,13 @@ def _check_cuda(x, *leaves):
     if forward_ad._current_level >= 0:      # within a dual_level, whatever the grad mode
         for t in (x,) + leaves:
             if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError("an input carries a forward-mode tangent, and this call computes none")
+                raise ValueError("an input or an output carries a forward-mode tangent, and this call computes none")
     if not torch.is_grad_enabled():
         return
     for t in (x,) + leaves:
         if t is None or not t.requires_grad:
             continue
-        raise ValueError("an input requires a gradient, and this call records none: call it under "
+        raise ValueError("an input or an output requires a gradient, and this call records none: call it under "
                          "torch.no_grad() and use the _backward function")
 
 
@@ -613,7 +613,7 @@ def group_norm_nhwc(x, groups, weight=None, bias=None, *, eps=1e-5, activation="
         check_random(p, seed, offset, rng, x.device)
     if out is not None:
         check_out(out, x, (x, weight, bias, rng if p else None))
-    _check_cuda(x, weight, bias)
+    _check_cuda(x, weight, bias, out)
 
     def call(raw):
         xc = x.contiguous()
@@ -691,7 +691,7 @@ def dropout(x, p, *, seed=0, offset=0, rng=None, residual=None, out=None, stream
     if out is not None:
         check_out(out, x, (x, residual), in_place=True)
         check_out(out, x, (rng,))
-    _check_cuda(x, residual)
+    _check_cuda(x, residual, out)
 
     def call(raw):
         xc = x.contiguous()
@@ -779,7 +779,7 @@ def _rms_inputs(x, weight, residual, *outs):
             check_out(t, x, (weight,))
     if len(outs) == 2 and outs[0] is not None and outs[1] is not None and _overlap(*outs):
         raise ValueError("out and sum_out overlap")
-    _check_cuda(x, weight, residual)
+    _check_cuda(x, weight, residual, *outs)
 
 
 def rms_norm_nhwc(x, weight=None, *, eps=1e-6, residual=None, out=None, sum_out=None, return_rstd=False, stream=None):
@@ -997,7 +997,7 @@ def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
             t0, t1 = _extent(t)
             if t0 < o1 and o0 < t1 and not (t is x and t0 == o0 and x.stride() == out.stride()):
                 raise ValueError("out overlaps an input")
-    _check_cuda(x, positions)
+    _check_cuda(x, positions, out)
 
     def call(raw):
         xc = x.contiguous() if r.copy else x
