@@ -74,6 +74,26 @@ def test_outputs_that_require_a_gradient(call):
     assert "gradient" not in str(e.value)
 
 
+@pytest.mark.parametrize("call", [
+    lambda: ct.grad_norm([card(3), needs(FLAT[:3])]),
+    lambda: ct.grad_norm([needs(FLAT[:3]) * 2]),
+    lambda: ct.AdamW([card(3)]).step([needs(FLAT[:3])]),
+    lambda: ct.AdamW([card(3), card(2)]).step([needs(FLAT[:3]) * 2, None])])
+def test_gradients_that_would_be_dropped(call):
+    """Gradients that carry a graph are refused as inputs are."""
+    with pytest.raises(ValueError, match="gradient"):
+        call()
+
+
+def test_tangents_that_would_be_dropped():
+    for call in (lambda g: ct.grad_norm([card(3), g]), lambda g: ct.AdamW([card(2), card(3)]).step([None, g]),
+                 lambda g: ct.AdamW([card(3)]).step([g])):
+        with forward_ad.dual_level(), torch.no_grad():
+            g = forward_ad.make_dual(torch.zeros(3), torch.ones(3)).as_subclass(Card)
+            with pytest.raises(ValueError, match="tangent"):
+                call(g)
+
+
 @pytest.mark.parametrize("base, status", [(1e-300, 0), (1e-40, 0), (5e-324, 4), (1e-310, 0), (1e-315, 4)])
 def test_frequencies_past_64_bits(base, status):
     """They are refused; all others are taken (nothing is launched for no images).  The last of 256 pairs has

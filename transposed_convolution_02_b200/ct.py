@@ -1048,6 +1048,7 @@ BLOCK = 256     # elements of a block of AdamW's states
 # What a step asks of each of its tensors, as functions that map() runs over a
 # list: a step of dozens of small tensors is bound by these questions.
 _shape, _dtype = torch.Tensor.shape.__get__, torch.Tensor.dtype.__get__
+_wants = torch.Tensor.requires_grad.__get__
 _numel, _device, _dense, _where = (torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous,
                                    torch.Tensor.data_ptr)
 
@@ -1064,6 +1065,17 @@ def _check_grad(g, name):
         raise ValueError("%s must be float32, float16 or bfloat16, not %s" % (name, g.dtype))
     if g.layout != torch.strided:
         raise ValueError("%s must be a dense tensor" % name)
+
+
+def _check_derivatives(grads):
+    """Gradients that carry derivatives of their own are refused, as inputs of the other calls are (_check_cuda)."""
+    if forward_ad._current_level >= 0:
+        for g in grads:
+            if forward_ad.unpack_dual(g).tangent is not None:
+                raise ValueError("a gradient carries a forward-mode tangent, and this call computes none")
+    if torch.is_grad_enabled() and True in map(_wants, grads):
+        raise ValueError("a gradient requires a gradient itself, and this call records none: call it under "
+                         "torch.no_grad(), or detach it")
 
 
 _GRADS = {}
@@ -1106,6 +1118,7 @@ def grad_norm(grads, max_norm=None, *, stream=None):
         max_norm = math.inf
     if not max_norm > 0.0:
         raise ValueError("max_norm must be positive, not %r" % (max_norm,))
+    _check_derivatives(grads)
     shapes, bytes_ = _grads_of(grads)
 
     def call(raw):
@@ -1266,6 +1279,7 @@ class AdamW:
             self._meta = None
             self._grads(grads)
             self._meta = meta
+        _check_derivatives(grads if meta is not None else [g for g in grads if g is not None])
         # all that the kernel relies on: a parameter can become another at its old address
         if (list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes
                 or list(map(_dtype, params)) != self._dtypes or not all(map(_dense, params))):
