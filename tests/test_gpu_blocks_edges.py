@@ -41,6 +41,20 @@ def test_device_steps_and_rates_that_skip(bits):
     assert all(bool(p.isfinite().all()) for p in params)
 
 
+def test_parameters_without_a_gradient_stay_valid():
+    """What a backward pass still needs of a parameter that an update left as it was is not refused."""
+    p, q = (torch.nn.Parameter(normal([40], k)) for k in (1, 2))
+    opt = ct.AdamW([p, q], lr=1e-2)
+    loss = (q * q).sum()
+    opt.step([normal([40], 3), None])
+    loss.backward()
+    assert torch.equal(q.grad, 2 * q.detach())
+    loss = (p * p).sum()
+    opt.step([normal([40], 4), None])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
 # ---- outputs that lie on inputs -----------------------------------------------------
 
 def outputs(x, r):

@@ -1318,4 +1318,6 @@ class AdamW:
         _run_on(call, self.exp_avg, stream)
         if step is None:
             self.steps += 1
-        torch.autograd.graph.increment_version(params)
+        # those that stay as they are stay valid for what saved them
+        torch.autograd.graph.increment_version(
+            params if meta is not None else [p for p, g in zip(params, grads) if g is not None])
