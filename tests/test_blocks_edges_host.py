@@ -94,6 +94,24 @@ def test_tangents_that_would_be_dropped():
                 call(g)
 
 
+def test_numbers_are_kept_by_value():
+    """Settings given as tensors that then change: descriptors are those of the present value."""
+    eps = torch.tensor(1e-6)
+    assert ct._rms_of(X, None, 0, eps).desc.eps == pytest.approx(1e-6)
+    eps.fill_(1e-3)
+    assert ct._rms_of(X, None, 0, eps).desc.eps == pytest.approx(1e-3)
+    assert ct._norm_of(X, 3, None, None, "relu", eps).desc.eps == pytest.approx(1e-3)
+    eps.fill_(1e-2)
+    assert ct._norm_of(X, 3, None, None, "relu", eps).desc.eps == pytest.approx(1e-2)
+
+    ct._ROTARY.clear()
+    for base, sections in ((torch.tensor(100.0), [4, 8]), (100.0, [torch.tensor(4), 8]), (100.0, [4, 8])):
+        with pytest.raises(ValueError, match="CUDA"):
+            ct.rotary_nhwc(HEADS, sections, base=base)
+    assert [r.desc.base for r in ct._ROTARY.values()] == [100.0]
+    assert not any(isinstance(v, torch.Tensor) for key in ct._ROTARY for v in key + key[3])
+
+
 @pytest.mark.parametrize("base, status", [(1e-300, 0), (1e-40, 0), (5e-324, 4), (1e-310, 0), (1e-315, 4)])
 def test_frequencies_past_64_bits(base, status):
     """They are refused; all others are taken (nothing is launched for no images).  The last of 256 pairs has

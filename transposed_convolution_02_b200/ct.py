@@ -16,6 +16,7 @@ import array
 import ctypes
 import functools
 import math
+import numbers
 import os
 
 import torch
@@ -546,6 +547,11 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _kept_by_value(*settings):
+    """Whether numbers can stand in a key: a tensor would be found by what it is, whatever it holds by then."""
+    return all(isinstance(v, numbers.Real) for v in settings)
+
+
 def _written(*outs):
     """Tell autograd that these tensors of the caller's were overwritten: what saved one of them for its backward
     pass is then refused there."""
@@ -583,9 +589,10 @@ def _norm_of(x, groups, weight, bias, activation, eps):
     except (KeyError, TypeError):
         check_norm(x, groups, weight, bias, activation)
         n = _norm(x.shape, x.dtype, int(groups), pd, activation, float(eps))
-        if len(_NORMS) >= 1024:
-            _NORMS.clear()
-        _NORMS[x.shape, x.dtype, groups, pd, activation, eps] = n
+        if _kept_by_value(groups, eps):
+            if len(_NORMS) >= 1024:
+                _NORMS.clear()
+            _NORMS[x.shape, x.dtype, groups, pd, activation, eps] = n
         return n
     dev = x.device
     for t in (weight, bias):
@@ -759,9 +766,10 @@ def _rms_of(x, weight, block, eps):
     except (KeyError, TypeError):
         check_rms(x, weight, block)
         r = _Rms(tuple(x.shape), x.dtype, pd, block, float(eps))
-        if len(_RMS) >= 1024:
-            _RMS.clear()
-        _RMS[key] = r
+        if _kept_by_value(eps, block):
+            if len(_RMS) >= 1024:
+                _RMS.clear()
+            _RMS[key] = r
         return r
     if weight is not None and (weight.dim() != 1 or weight.numel() != r.c or weight.get_device() != x.get_device()):
         check_rms(x, weight, block)
@@ -984,9 +992,10 @@ def _rotate(x, sections, base, pairs, positions, out, stream, inverse):
         r = _ROTARY[key]
     except (KeyError, TypeError):
         r = _Rotary(x, out, sections, base, pairs, positions, inverse)
-        if len(_ROTARY) >= 1024:
-            _ROTARY.clear()
-        _ROTARY[key] = r
+        if _kept_by_value(base, *sections):
+            if len(_ROTARY) >= 1024:
+                _ROTARY.clear()
+            _ROTARY[key] = r
     if positions is not None and positions.device != x.device:
         check_rotary(x, sections, base, pairs, positions)
     if out is not None:
