@@ -382,8 +382,12 @@ CT_API ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *
  *
  *     t = position * base^(-2 j / sections[a]),   (u, v) -> (u cos t - v sin t, u sin t + v cos t).
  *
- * Angles are formed in 64 bits, the rotation in fp32, rounded once.  The
- * gradient in x is the inverse rotation of dy (`inverse`: by -t). */
+ * The frequency is rounded to 64 bits, for positions up to 2^24 (and 2^22
+ * turns) then to two floats of 48 bits together; their product with the position
+ * is formed in two floats, beyond that in 64 bits.  Cosine and sine are fp32, off
+ * by at most 1.5 * 2^-24 plus 2^-45 of the angle (2^-51 in 64 bits); the rotation
+ * is fp32, rounded once.  The gradient in x is the inverse rotation of dy
+ * (`inverse`: by -t). */
 typedef enum ct_pairs { CT_PAIRS_ADJACENT = 0, CT_PAIRS_HALVES = 1 } ct_pairs;
 
 /* Positions: the pixels' indices on the grid, or numbers [S, axes] on the

@@ -109,6 +109,28 @@ def test_frequencies_that_fp32_does_not_hold(base):
             assert bool(((y[:, 2, :, i].double() - want).abs() <= 5 * ref.U * (v.abs() + w.abs())).all())
 
 
+@pytest.mark.parametrize("top", [1 << 10, 1 << 17, 1 << 21, (1 << 24) - 1, 1 << 29])
+def test_cosines_and_sines(top):
+    """Pairs (1, 0) turn into the cosine and the sine.  Of the kernel's forms, u = 2^-24: the angle's remainder
+    within an eighth of a turn is rounded to u / 2 once it is an angle; the cosine's polynomial adds the last sum's
+    u / 2, a quarter of u from the square and a sixth from the sum before it, and 0.35 u of the angle: 1.3 u, the
+    sine's 1.15 u, terms left out 0.03 u.  The position's product with a frequency of 48 bits, and the parts that it
+    is made of, lose at most 2^-45 of the angle; beyond 2^24, in 64 bits, 2^-51."""
+    n = 4096
+    g = torch.Generator(device="cuda").manual_seed(top % 1000)
+    at = torch.randint(-top, top, (n, 1), generator=g, device="cuda")
+    for pairs, i, k in (("adjacent", slice(0, None, 2), slice(1, None, 2)), ("halves", slice(0, 64), slice(64, None))):
+        x = torch.zeros(1, n, 1, 128, device="cuda")
+        x[..., i] = 1.0
+        angles = ref.rotary_angles(at.double(), [128], 10000.0)
+        for call, sign in ((ct.rotary_nhwc, 1), (ct.rotary_nhwc_backward, -1)):
+            y = call(x, [128], pairs=pairs, positions=at)[0, :, 0].double()
+            bound = 1.5 * ref.U + angles.abs() * (2.0 ** -45 if top <= 1 << 24 else 2.0 ** -51)
+            for got, want in ((y[:, i], torch.cos(angles)), (y[:, k], sign * torch.sin(angles))):
+                err = (got - want).abs() / bound
+                assert float(err.max()) <= 1, "%.3g of the bound" % float(err.max())
+
+
 # ---- root-mean-square norm ------------------------------------------------------------
 
 FULL = [256, 512, 768, 1024, 2048, 4096, 8192]       # rows of whole warps, each thread with all of its vectors

@@ -6,9 +6,12 @@
 // one in each half of the head) of one pixel, makes their sines and cosines
 // once and walks the heads (or images) with them in registers.  The angle is formed in
 // turns.  A position of up to 24 bits times a frequency of two floats (48 bits)
-// gives the fraction of a turn to 2^-26 in fp32: the product's rounding is known
-// exactly (fused multiply-add), and so is the part left of whole turns.  Larger
-// positions, and frequencies above a turn a position, take 64 bits.
+// is formed in fp32: the product's rounding is known exactly (fused
+// multiply-add), and so is what whole and quarter turns leave of it; the rounding
+// joins that remainder, an eighth of a turn at most, once it is an angle.  Sines
+// and cosines come out to 1.5 * 2^-24 for positions below 2^17 (2^-45 of the
+// angle is lost beside that, at most).  Larger positions, and frequencies above a
+// turn a position, are multiplied in 64 bits and reduced alike.
 // Measured (GPU time; against the measured copy rate): [2,16x32x32,24,128] bf16
 // 65 us (0.95; 185 with angles in 64 bits and divisions for every pair),
 // [3,57x91,5,72] fp32 10.5 (0.65: two rounds of blocks), one head of 64 at
@@ -149,14 +152,22 @@ __device__ __forceinline__ void positions_of(const RotaryParams &p, int64_t n, i
 
 __device__ __forceinline__ float2 twice(float f) { return make_float2(f, f); }
 
-// Cosine and sine of two angles of f turns, |f| <= 1: to the nearest quarter
-// turn, and Taylor's polynomials of what is left, an eighth of a turn at most
-// (the first terms left out are below 2^-29).  Adding 3 * 2^22 rounds to a whole
-// number of quarters, which then are the sum's last bits.
-__device__ __forceinline__ void turn(float2 f, float2 &c, float2 &s) {
-    const float2 z = __ffma2_rn(f, twice(4.f), twice(12582912.f));
-    const float2 g = __ffma2_rn(__fadd2_rn(z, twice(-12582912.f)), twice(-0.25f), f);
-    const float2 x = __fmul2_rn(g, twice(6.2831853f)), q = __fmul2_rn(x, x);
+// Two angles in turns, without whole ones: `high`, at most half a turn, which
+// holds all its bits, and what it lacks.
+struct Turns {
+    float2 high, low;
+};
+
+// Their cosines and sines: the nearest quarter turn is taken off, and Taylor's
+// polynomials serve what is left, an eighth of a turn at most (the first terms
+// left out are below 2^-29).  Adding 3 * 2^22 rounds to a whole number of
+// quarters, which then are the sum's last bits.
+__device__ __forceinline__ void turn(const Turns &t, float2 &c, float2 &s) {
+    const float2 z = __ffma2_rn(__fadd2_rn(t.high, t.low), twice(4.f), twice(12582912.f));
+    const float2 g = __ffma2_rn(__fadd2_rn(z, twice(-12582912.f)), twice(-0.25f), t.high);      // exact; beside a border to 2^-28
+    // 2 pi in two floats
+    const float2 rest = __ffma2_rn(g, twice(-1.7484556e-7f), __fmul2_rn(t.low, twice(6.2831855f)));
+    const float2 x = __ffma2_rn(g, twice(6.2831855f), rest), q = __fmul2_rn(x, x);
     float2 a = __ffma2_rn(q, twice(1.f / 362880), twice(-1.f / 5040));
     a = __ffma2_rn(a, q, twice(1.f / 120));
     a = __ffma2_rn(a, q, twice(-1.f / 6));
@@ -176,12 +187,19 @@ __device__ __forceinline__ void turn(float2 f, float2 &c, float2 &s) {
     place(__float_as_uint(z.y), a.y, b.y, c.y, s.y);
 }
 
-// Positions times frequencies (as high and low parts) in turns, without the whole ones.
-__device__ __forceinline__ float2 turns_of(float2 pos, float2 hi, float2 lo) {
+// Positions times frequencies (as high and low parts).
+__device__ __forceinline__ Turns turns_of(float2 pos, float2 hi, float2 lo) {
     const float2 t = __fmul2_rn(pos, hi), minus = make_float2(-t.x, -t.y);
     const float2 rest = __ffma2_rn(pos, lo, __ffma2_rn(pos, hi, minus));
     const float2 whole = __fadd2_rn(__fadd2_rn(t, twice(12582912.f)), twice(-12582912.f));
-    return __fadd2_rn(__fadd2_rn(t, make_float2(-whole.x, -whole.y)), rest);
+    return {__fadd2_rn(t, make_float2(-whole.x, -whole.y)), rest};
+}
+
+// A product in 64 bits.
+__device__ __forceinline__ void turns_of(double t, float &high, float &low) {
+    t -= rint(t);
+    high = (float)t;
+    low = (float)(t - (double)high);
 }
 
 // E: elements of a vector.  An item of a head is
@@ -228,16 +246,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                                    : make_float4(p.parts[q][0], p.parts[q][1], 0.f, 0.f);
             auto axis = [&](int i) { return p.axes > 1 && i >= p.first[1] ? p.axes > 2 && i >= p.first[2] ? 2 : 1 : 0; };
             const int a0 = axis(q), a1 = axis(q + 1);
-            float2 r;
+            Turns r;
             if (!where.is_far) {
                 const float2 pos = make_float2(a0 == 2 ? where.near[2] : a0 == 1 ? where.near[1] : where.near[0],
                                                a1 == 2 ? where.near[2] : a1 == 1 ? where.near[1] : where.near[0]);
                 r = turns_of(pos, make_float2(f.x, f.z), make_float2(f.y, f.w));
             } else {
-                const double t0 = (a0 == 2 ? where.far[2] : a0 == 1 ? where.far[1] : where.far[0]) * p.turns[q];
-                const double t1 = P == 1 ? 0.0 : (a1 == 2 ? where.far[2] : a1 == 1 ? where.far[1] : where.far[0]) *
-                                                     p.turns[q + 1];
-                r = make_float2((float)(t0 - rint(t0)), (float)(t1 - rint(t1)));
+                turns_of((a0 == 2 ? where.far[2] : a0 == 1 ? where.far[1] : where.far[0]) * p.turns[q], r.high.x, r.low.x);
+                turns_of(P == 1 ? 0.0 : (a1 == 2 ? where.far[2] : a1 == 1 ? where.far[1] : where.far[0]) * p.turns[q + 1],
+                         r.high.y, r.low.y);
             }
             turn(r, cs[j], sn[j]);
             sn[j] = __fmul2_rn(sn[j], twice(p.sign));
