@@ -321,8 +321,8 @@ CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const vo
  *
  * h is formed in fp32; `sum` gets it rounded to dtype (what the residual
  * stream carries on), y and rstd come from the unrounded values.  Everything
- * is computed in fp32 (the squares too: a row whose root mean square passes
- * 1e19 has an rstd of 0) and rounded once.  dtype is x's, residual's, y's and
+ * is computed in fp32 and rounded once; the squares' sum too: a row whose 2-norm
+ * passes 1.8e19 (a root mean square of 1.8e19 / sqrt(C)) has an rstd of 0.  dtype is x's, residual's, y's and
  * sum's; param_dtype weight's and its gradient's, CT_F32 or dtype.
  *
  * e4m3 output: y is not rounded to dtype but held as codes and fp32 scales,
@@ -483,8 +483,9 @@ CT_API ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_par
                           const void *const *grads, void *exp_avg, void *exp_avg_sq, float *exp_avg_scale,
                           float *exp_avg_sq_scale, float *master, void *stream);
 
-/* *norm = the square root of the sum of all gradients' squares (squares and
- * sums in 64 bits), *scale (may be NULL) = min(1, max_norm / norm), or 0 where
+/* *norm = the square root of the sum of all gradients' squares, to its rounding
+ * (squares and sums in 64 bits; those of 16-bit gradients, exact in fp32, in
+ * sums of two floats, 48 bits, for up to 32 of them), *scale (may be NULL) = min(1, max_norm / norm), or 0 where
  * the norm is not finite in fp32: what ct_adamw's grad_scale takes to clip, or
  * to skip an update that overflowed.
  * Of shapes, n and grad_dtype are read; a NULL gradient counts nothing.

@@ -198,3 +198,16 @@ def test_products_that_overflow(c, dtype):
                 assert torch.equal(s.isnan(), part.isinf().any(-1)), (how, block, b)
             v = q.float() * ref.spread_scales(scale, block, c)
             assert bool(v[y.isinf()].isnan().all())
+
+
+@pytest.mark.parametrize("c", [64, 511, 4096, 40000])
+def test_where_squares_end(c):
+    """Rows whose squares' sum fp32 holds come out right; beyond it rstd is 0."""
+    x = normal([4, c], 7)
+    x[0] *= 1.7e19 / float(torch.linalg.vector_norm(x[0].double()))
+    x[1] *= 2.0e19 / float(torch.linalg.vector_norm(x[1].double()))
+    x[2] = 1.7e19 / c ** 0.5
+    x[3] = 2.0e19 / c ** 0.5
+    y, rstd = ct.rms_norm_nhwc(x, None, eps=EPS, return_rstd=True)
+    check_forward(x[::2], None, None, (y[::2], rstd[::2]), "%d channels" % c)
+    assert not rstd[1::2].any() and not y[1::2].any()
