@@ -211,3 +211,15 @@ def test_where_squares_end(c):
     y, rstd = ct.rms_norm_nhwc(x, None, eps=EPS, return_rstd=True)
     check_forward(x[::2], None, None, (y[::2], rstd[::2]), "%d channels" % c)
     assert not rstd[1::2].any() and not y[1::2].any()
+
+
+@pytest.mark.parametrize("c", [1 << 20, 1 << 24])
+def test_sums_of_the_longest_rows(c):
+    """Terms that are all alike round alike: sums of the longest rows still hold to their bound."""
+    for value in (1.1, -1.3, 0.7):
+        x = torch.full([2, c], value, device="cuda")
+        y, rstd = ct.rms_norm_nhwc(x, None, eps=EPS, return_rstd=True)
+        check_forward(x, None, None, (y, rstd), "%d channels" % c)
+        dy = torch.full_like(x, 0.3)
+        w = torch.full([c], 0.9, device="cuda")
+        check_backward(dy, x, rstd, w, None, ct.rms_norm_nhwc_backward(dy, x, rstd, w), "%d channels" % c)
