@@ -454,13 +454,13 @@ typedef struct ct_param {
     int64_t n;              /* elements */
     int32_t dtype;          /* ct_dtype of the parameter */
     int32_t grad_dtype;     /* of its gradient: dtype or CT_F32 */
-    double weight_decay;    /* read by ct_adamw alone */
+    double weight_decay;    /* >= 0, within fp32; read by ct_adamw alone */
 } ct_param;
 
 typedef struct ct_adamw_desc {
     int32_t bits;           /* 32 or 8 */
     int32_t reserved;       /* not read */
-    double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps >= 2^-126 */
+    double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps >= 2^-126; fp32 holds them (CT_ERR_ATTR) */
     int64_t step;           /* 1 for the first update */
     uint64_t seed;          /* bits = 8 alone */
     /* on the device, read by the kernel in place of the numbers above; NULL:

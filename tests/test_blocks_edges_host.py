@@ -7,7 +7,7 @@ import pytest
 import torch
 from torch.autograd import forward_ad
 
-from test_blocks_host import FLAT, HEADS, OUT, R, X, Card, card, rotary_desc
+from test_blocks_host import FLAT, HEADS, OUT, R, X, Card, adamw_status, card, rotary_desc
 from transposed_convolution_02_b200 import ct
 
 
@@ -118,3 +118,9 @@ def test_frequencies_past_64_bits(base, status):
     base^(-255 / 256) / 2 pi: 9.8e307 for 1e-310."""
     d = rotary_desc(base=base, sections=[0, 512, 0], dim=512, N=0)
     assert ct.lib().ct_rotary(ctypes.byref(d), None, None, None, None) == status
+
+
+@pytest.mark.parametrize("over", [dict(lr=1e39), dict(eps=1e39), dict(rows=((10, 0, 0, 1e39),))])
+def test_settings_that_fp32_does_not_hold(over):
+    """They would become infinite on the way to the kernel."""
+    assert adamw_status(**over) == 4

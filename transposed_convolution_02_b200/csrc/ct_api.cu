@@ -748,8 +748,8 @@ ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_param *sha
                    float *exp_avg_sq_scale, float *master, void *stream) {
     if (!desc) return CT_ERR_NULL;
     if (desc->bits != 32 && desc->bits != 8) return CT_ERR_ATTR;
-    if (!(desc->lr >= 0.0) || !isfinite(desc->lr)) return CT_ERR_ATTR;
-    if (!(desc->eps >= ldexp(1.0, -126)) || !isfinite(desc->eps)) return CT_ERR_ATTR;   // 0 / eps is 0
+    if (!(desc->lr >= 0.0) || !isfinite((float)desc->lr)) return CT_ERR_ATTR;
+    if (!(desc->eps >= ldexp(1.0, -126)) || !isfinite((float)desc->eps)) return CT_ERR_ATTR;   // 0 / eps is 0
     for (double v : {desc->beta1, desc->beta2})
         if (!(v >= 0.0 && v < 1.0)) return CT_ERR_ATTR;
     if (desc->step < 1) return CT_ERR_ATTR;
@@ -757,7 +757,7 @@ ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_param *sha
     if (st != CT_OK) return st;
     bool some = false;
     for (int64_t i = 0; i < count; ++i) {
-        if (!isfinite(shapes[i].weight_decay) || shapes[i].weight_decay < 0.0) return CT_ERR_ATTR;
+        if (!isfinite((float)shapes[i].weight_decay) || shapes[i].weight_decay < 0.0) return CT_ERR_ATTR;
         if (shapes[i].n == 0 || !grads[i]) continue;
         some = true;
         if (!params || !params[i]) return CT_ERR_NULL;
