@@ -223,3 +223,39 @@ def test_sums_of_the_longest_rows(c):
         dy = torch.full_like(x, 0.3)
         w = torch.full([c], 0.9, device="cuda")
         check_backward(dy, x, rstd, w, None, ct.rms_norm_nhwc_backward(dy, x, rstd, w), "%d channels" % c)
+
+
+@pytest.mark.parametrize("c", [1024, 4096])
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("residual", [True, False])
+def test_whole_rows_past_32_bits(c, wide, residual):
+    """Offsets above 2^31 elements in the kernels that whole rows with a weight have: the last rows, and those
+    around the 32nd bit, are as they are alone."""
+    rows = (1 << 31) // c + 64
+    t = torch.float16
+    w = (1 + 0.1 * normal([c], 9)).to(torch.float32 if wide else t)
+    x = torch.empty(rows, c, dtype=t, device="cuda")
+    x[:] = 1.0
+    at = [slice(0, 64), slice(rows - 128, rows - 64), slice(rows - 64, rows)]
+    for i, s in enumerate(at):
+        x[s] = normal([64, c], 10 + i, t)
+    r = x if residual else None
+
+    def own(out, s):
+        return [v[s].clone() for v in out]
+
+    for call in (lambda a, b: ct.rms_norm_nhwc(a, w, eps=EPS, residual=b, return_rstd=True),
+                 lambda a, b: ct.rms_norm_nhwc_e4m3(a, w, eps=EPS, residual=b, return_rstd=True),
+                 lambda a, b: ct.rms_norm_nhwc_e4m3(a, w, block=128, eps=EPS, residual=b, return_rstd=True)):
+        got = call(x, r)
+        parts = [own(got, s) for s in at]
+        middle = [v[1000:1064].clone() for v in got], [v[rows // 2:rows // 2 + 64].clone() for v in got]
+        del got
+        for s, part in zip(at, parts):
+            alone = x[s].clone()
+            for p, q in zip(part, call(alone, alone if residual else None)):
+                p, q = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (p, q))
+                assert torch.equal(p, q)
+        for p, q in zip(*middle):
+            p, q = (v.view(torch.uint8) if v.dtype == torch.float8_e4m3fn else v for v in (p, q))
+            assert torch.equal(p, q)
