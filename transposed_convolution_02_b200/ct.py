@@ -1057,7 +1057,6 @@ BLOCK = 256     # elements of a block of AdamW's states
 # What a step asks of each of its tensors, as functions that map() runs over a
 # list: a step of dozens of small tensors is bound by these questions.
 _shape, _dtype = torch.Tensor.shape.__get__, torch.Tensor.dtype.__get__
-_wants = torch.Tensor.requires_grad.__get__
 _numel, _device, _dense, _where = (torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous,
                                    torch.Tensor.data_ptr)
 
@@ -1082,7 +1081,7 @@ def _check_derivatives(grads):
         for g in grads:
             if forward_ad.unpack_dual(g).tangent is not None:
                 raise ValueError("a gradient carries a forward-mode tangent, and this call computes none")
-    if torch.is_grad_enabled() and True in map(_wants, grads):
+    if torch.is_grad_enabled() and torch._C._any_requires_grad(*grads):
         raise ValueError("a gradient requires a gradient itself, and this call records none: call it under "
                          "torch.no_grad(), or detach it")
 
@@ -1230,7 +1229,7 @@ class AdamW:
         return [_addr(t) for t in self._states()]
 
     def _places(self):
-        """The parameters' addresses; they have to be dense and apart."""
+        """The parameters' addresses, as bytes; they have to be dense and apart."""
         for i, p in enumerate(self.params):
             if not p.is_contiguous():
                 raise ValueError("parameter %d must be contiguous" % i)
@@ -1239,7 +1238,7 @@ class AdamW:
         spans = sorted(_extent(p) for p in self.params if p.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("two parameters overlap")
-        return [p.data_ptr() for p in self.params]
+        return _pointers(map(_where, self.params)).tobytes()
 
     def _grads(self, grads):
         """Check the gradients and make their descriptors; None entries stay."""
@@ -1290,8 +1289,9 @@ class AdamW:
             self._meta = meta
         _check_derivatives(grads if meta is not None else [g for g in grads if g is not None])
         # all that the kernel relies on: a parameter can become another at its old address
-        if (list(map(_where, params)) != self._at or list(map(_numel, params)) != self._sizes
-                or list(map(_dtype, params)) != self._dtypes or not all(map(_dense, params))):
+        to = _pointers(map(_where, params))
+        if (to.tobytes() != self._at or list(map(_numel, params)) != self._sizes
+                or list(map(_dtype, params)) != self._dtypes or False in map(_dense, params)):
             self._at = self._places()
         if self._kept_looks() != self._kept_as:
             self._kept_at = self._kept_places()
@@ -1318,7 +1318,6 @@ class AdamW:
             else:
                 dense = grads if all(map(_dense, grads)) else [g.contiguous() for g in grads]
                 at = _pointers(map(_where, dense))
-            to = _pointers(self._at)
             st = lib().ct_adamw(d, len(dense), self._table, to.buffer_info()[0], at.buffer_info()[0],
                                 *self._kept_at, raw)
             if st != CT_OK:
