@@ -322,8 +322,9 @@ CT_API ct_status ct_group_norm_backward(const ct_group_norm_desc *desc, const vo
  * h is formed in fp32; `sum` gets it rounded to dtype (what the residual
  * stream carries on), y and rstd come from the unrounded values.  Everything
  * is computed in fp32 and rounded once; the squares' sum too: a row whose 2-norm
- * passes 1.8e19 (a root mean square of 1.8e19 / sqrt(C)) has an rstd of 0.  dtype is x's, residual's, y's and
- * sum's; param_dtype weight's and its gradient's, CT_F32 or dtype.
+ * passes 1.8e19 (a root mean square of 1.8e19 / sqrt(C)) has an rstd of 0.
+ * dtype is x's, residual's, y's and sum's; param_dtype weight's and its
+ * gradient's, CT_F32 or dtype.
  *
  * e4m3 output: y is not rounded to dtype but held as codes and fp32 scales,
  *     scale = max(max |y| * (1 / 448), 2^-126) of a block,   q = e4m3(y * (1 / scale)), to nearest even,
@@ -384,8 +385,9 @@ CT_API ct_status ct_rms_norm_backward(const ct_rms_norm_desc *desc, const void *
  *
  * The frequency is rounded to 64 bits, for positions up to 2^24 (and 2^22
  * turns) then to two floats of 48 bits together; their product with the position
- * is formed in two floats, beyond that in 64 bits.  Cosine and sine are fp32, off
- * by at most 1.5 * 2^-24 plus 2^-45 of the angle (2^-51 in 64 bits); the rotation
+ * is formed in two floats, beyond that in 64 bits (one that those do not hold is
+ * no angle, and gives NaN).  Cosine and sine are fp32, off by at most 1.5 * 2^-24
+ * plus 2^-45 of the angle (2^-51 in 64 bits); the rotation
  * is fp32, rounded once.  The gradient in x is the inverse rotation of dy
  * (`inverse`: by -t). */
 typedef enum ct_pairs { CT_PAIRS_ADJACENT = 0, CT_PAIRS_HALVES = 1 } ct_pairs;
@@ -485,9 +487,9 @@ CT_API ct_status ct_adamw(const ct_adamw_desc *desc, int64_t count, const ct_par
 
 /* *norm = the square root of the sum of all gradients' squares, to its rounding
  * (squares and sums in 64 bits; those of 16-bit gradients, exact in fp32, in
- * sums of two floats, 48 bits, for up to 32 of them), *scale (may be NULL) = min(1, max_norm / norm), or 0 where
- * the norm is not finite in fp32: what ct_adamw's grad_scale takes to clip, or
- * to skip an update that overflowed.
+ * sums of two floats, 48 bits, for up to 32 of them), *scale (may be NULL) =
+ * min(1, max_norm / norm), or 0 where the norm is not finite in fp32: what
+ * ct_adamw's grad_scale takes to clip, or to skip an update that overflowed.
  * Of shapes, n and grad_dtype are read; a NULL gradient counts nothing.
  * max_norm > 0, infinity allowed.  The same call gives the same bits. */
 CT_API ct_status ct_grad_norm_workspace_bytes(int64_t count, size_t *bytes);
