@@ -9,7 +9,7 @@ import torch
 
 import blocks_ref as ref
 from test_gpu_adamw import everything, make, same
-from test_gpu_rms_norm import EPS, TYPES, _cuda, check_backward, check_codes, check_forward, inputs, normal  # noqa: F401
+from test_gpu_rms_norm import EPS, TYPES, _cuda, check_backward, check_forward, inputs, normal  # noqa: F401
 from transposed_convolution_02_b200 import ct
 
 pytestmark = pytest.mark.gpu
